@@ -2,10 +2,13 @@
 
 ``linear(x, w, b)`` is the tensor-level call, and ``contract`` the widened
 contraction (bfloat16 heads, no bias, FP32 output, fused epilogue steps);
+``gated_linear``, ``gated_linear_backward``, ``linear_backward`` and
+``clip_grad_norm`` are the feed-forward block, its gradients and the clip
+before an update;
 ``column_parallel_linear`` and ``row_parallel_linear`` split the op over
 torch.distributed ranks;
 the C entry points of include/poot_linear.h are mirrored one to one in
-``binding``.
+``binding``, those of include/poot_ffn.h in ``ffn``.
 """
 from .binding import (  # noqa: F401
     GEMV_MAX_M, Options, options, POOT_ERR_CUDA, POOT_ERR_DEVICE_TIMEOUT, POOT_ERR_INVALID_ARG,
@@ -19,6 +22,11 @@ from .binding import (  # noqa: F401
     EPILOGUE_MAX_STEPS, EpilogueStep, contract, poot_contract, poot_contract_grouped,
     NOALLOC_SCRATCH_BYTES, poot_linear_f16_splitk_noalloc,
     poot_linear_tp_shard, poot_linear_gather_columns, poot_linear_f16_finish, poot_linear_gemm_plan,
+)
+from .ffn import (  # noqa: F401
+    ACT_CODES, ACT_GELU_ERF, ACT_GELU_TANH, ACT_SILU, GRAD_BF16, GRAD_F16, GRAD_F32, GatedLinearArgs,
+    GatedLinearBackwardArgs, GradTensor, LinearBackwardArgs, clip_grad_norm, gated_linear, gated_linear_backward,
+    linear_backward, poot_clip_grad_norm, poot_gated_linear, poot_gated_linear_backward, poot_linear_backward,
 )
 from .tensor_parallel import (  # noqa: F401
     shard_range, column_parallel_linear, row_parallel_linear,

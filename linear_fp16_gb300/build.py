@@ -10,6 +10,7 @@ import re
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,12 +18,14 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpoot_linear.so")
-SOURCES = [os.path.join(CSRC, "poot_linear.cu")]
-DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("ptx.cuh", "gemm_tcgen05.cuh", "gemv.cuh", "epilogue.cuh", "splitk.cuh", "pack.cuh", "shards.cuh")] + [
-    os.path.join(INCLUDE, "poot_linear.h")]
+SOURCES = [os.path.join(CSRC, f) for f in ("poot_linear.cu", "poot_ffn.cu")]
+DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in (
+    "ptx.cuh", "gemm_tcgen05.cuh", "gemv.cuh", "epilogue.cuh", "splitk.cuh", "pack.cuh", "shards.cuh", "host.cuh",
+    "ffn_gemm.cuh", "ffn_elem.cuh", "clip.cuh")] + [
+    os.path.join(INCLUDE, f) for f in ("poot_linear.h", "poot_ffn.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr"]
 
 
@@ -40,12 +43,7 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in DEPENDS)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, *FLAGS, "-Xptxas=-v", "-I", INCLUDE, "-I", CSRC, *SOURCES, "-o", tmp]
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -54,6 +52,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
         sys.stderr.write(r.stderr)
     if r.returncode != 0:
         raise subprocess.CalledProcessError(r.returncode, cmd)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    if not force and up_to_date():
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    tag = f".tmp{os.getpid()}"
+    objs = [os.path.join(BUILD, os.path.basename(src) + tag + ".o") for src in SOURCES]
+    tmp = LIB + tag
+    compiles = [[nvcc(), *ARCH, *FLAGS, "-Xptxas=-v", "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", o]
+                for src, o in zip(SOURCES, objs)]
+    link = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp]
+    try:
+        # the translation units side by side, then the link
+        with ThreadPoolExecutor(len(compiles)) as pool:
+            list(pool.map(lambda cmd: _run(cmd, verbose), compiles))
+        _run(link, verbose)
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
     os.replace(tmp, LIB)
     return LIB
 

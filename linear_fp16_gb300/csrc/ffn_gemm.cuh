@@ -1,0 +1,545 @@
+// The matrix products of the feed-forward block and of its gradients on the
+// 5th-generation tensor cores (tcgen05), head dtype binary16 or bfloat16:
+//
+//   kFfnGated  g = x Wg^T + bg, u = x Wu^T + bu, h = act(g) u   (one pass)
+//              A = x [M,K], B = Wg | Wu [N,K]; both contracted along their
+//              rows (K-major)
+//   kFfnDx     dx = sum_p D_p W_p, p = 1 or 2 products into one sum
+//              A = D_p [M,N] K-major, B = W_p [N,K] contracted over its
+//              rows' index (MN-major: the layout in memory is the transpose
+//              of what the product needs, and the tensor core reads it so)
+//   kFfnDw     dW_q = D_q^T x, q = 1 or 2 outputs
+//              A = D_q [M,N] and B = x [M,K], both MN-major
+//
+// A persistent CTA (or a CTA pair on one 256-row tile, 2-SM MMA) per SM walks
+// output tiles.  Warp roles as in the linear's GEMM: eight epilogue warps, one
+// thread that issues the MMAs, one that issues the TMA loads.  A sum stays
+// in TMEM over the whole K range (FP32 accumulators): unlike the linear's
+// kernel there is no promotion into registers every 1024 elements, because
+// these operators' outputs are rounded once from the FP32 value to 11 or 8
+// bits and carry no 2-ulp rule; the accumulators of two tiles fit TMEM, so
+// the epilogue of a tile runs under the main loop of the next.
+//
+// The gated tile: half of the tile's BN accumulator columns hold gate
+// columns and half the same columns of up, so that one thread has g and u
+// of an output side by side, and x's tile is read from shared memory once
+// for both.  In a CTA pair each CTA loads half of the B rows: the even one
+// gate rows, the odd one up rows.
+//
+// MN-major operands: a TMA box is 64 (contiguous) x 64 (K) elements with the
+// 128-byte swizzle; boxes of a tile lie 8 KB apart (the descriptor's leading
+// offset), groups of 8 K rows 1 KB apart (its stride offset), and a K step
+// of 16 is 2 KB.
+#pragma once
+
+#include <type_traits>
+
+#include "epilogue.cuh"
+#include "ptx.cuh"
+
+namespace poot {
+
+enum FfnKind : int { kFfnGated = 0, kFfnDx = 1, kFfnDw = 2 };
+enum FfnAct : int { kActSilu = 0, kActGeluTanh = 1, kActGeluErf = 2 };
+
+constexpr int kFfnBM = 128;
+constexpr int kFfnBK = 64;  // one 128-byte swizzle row
+constexpr int kFfnEpiWarps = 8;
+constexpr int kFfnMmaWarp = 8;
+constexpr int kFfnProdWarp = 9;
+constexpr int kFfnThreads = 10 * 32;
+constexpr int kFfnMaxBN = 256;
+constexpr int kFfnMaxStages = 8;
+constexpr uint32_t kFfnTmemCols = 2 * kFfnMaxBN;
+
+// Activations in FP32 and their derivatives, from the formulas (s is the
+// logistic function):
+//   silu       t s(t)                     s + t s (1 - s)
+//   gelu_tanh  t s(z), z = a (t + b t^3)  s + t s (1 - s) z'
+//              a = 2 sqrt(2/pi), b = 0.044715: the tanh form 0.5 t (1 +
+//              tanh(z / 2)) written with the logistic function
+//   gelu_erf   t P(t), P = 0.5 (1 + erf(t / sqrt 2));  P + t p(t), p the
+//              normal density
+// Where s is 0 or 1 in FP32 the product s (1 - s) is 0 and z' may overflow:
+// the second term is then dropped, as in the limit.
+__device__ __forceinline__ float act_sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+template <int ACT>
+__device__ __forceinline__ float act_value_t(float t) {
+  if constexpr (ACT == kActSilu) {
+    return t * act_sigmoid(t);
+  } else if constexpr (ACT == kActGeluTanh) {
+    return t * act_sigmoid(1.5957691216057308f * fmaf(0.044715f * t * t, t, t));
+  } else {
+    return 0.5f * t * (1.0f + erff(t * 0.70710678118654752f));
+  }
+}
+__device__ __forceinline__ float act_value(int act, float t) {
+  return act == kActSilu ? act_value_t<kActSilu>(t)
+                         : (act == kActGeluTanh ? act_value_t<kActGeluTanh>(t) : act_value_t<kActGeluErf>(t));
+}
+
+// value in v, derivative in d
+template <int ACT>
+__device__ __forceinline__ void act_both_t(float t, float& v, float& d) {
+  if constexpr (ACT == kActGeluErf) {
+    const float p = 0.5f * (1.0f + erff(t * 0.70710678118654752f));
+    v = t * p;
+    d = fmaf(t, 0.3989422804014327f * __expf(-0.5f * t * t), p);
+  } else {
+    float z = t, dz = 1.0f;
+    if constexpr (ACT == kActGeluTanh) {
+      const float t2 = t * t;
+      z = 1.5957691216057308f * fmaf(0.044715f * t2, t, t);
+      dz = 1.5957691216057308f * fmaf(0.134145f, t2, 1.0f);
+    }
+    const float s = act_sigmoid(z);
+    const float q = s * (1.0f - s);
+    v = t * s;
+    d = q != 0.0f ? fmaf(t * q, dz, s) : s;
+  }
+}
+
+// Tile index -> (M block, N block): groups of group_m M blocks walked column
+// by column, odd groups from the far end, so that CTAs running together share
+// rows of both operands in L2.
+__device__ __forceinline__ void ffn_tile_coords(int t, int num_m, int num_n, int group_m, int& mb, int& nb) {
+  const int span = group_m * num_n;
+  const int g = t / span;
+  const int first_m = g * group_m;
+  const int gsize = min(num_m - first_m, group_m);
+  const int local = t - g * span;
+  mb = first_m + local % gsize;
+  nb = local / gsize;
+  if (g & 1) nb = num_n - 1 - nb;
+}
+
+struct FfnMaps {
+  CUtensorMap a[2];  // kFfnGated: x; kFfnDx: D_p; kFfnDw: D_q
+  CUtensorMap b[2];  // kFfnGated: Wg, Wu; kFfnDx: W_p; kFfnDw: x
+  CUtensorMap y[3];  // outputs: h, g, u / dx / dW_q (or one FP32 map of the partial sums)
+};
+
+struct FfnGemmArgs {
+  int M, N;          // rows and columns of one output (kFfnGated: N columns of h)
+  int bn;            // accumulator columns of a tile (kFfnGated: bn / 2 columns of h)
+  int cols;          // output columns of a tile
+  int stages;
+  int group_m;       // M blocks walked together (ffn_tile_coords)
+  int num_m_blocks, num_n_blocks, num_tiles, tiles_per_group;
+  int kb_part;       // K blocks (of SUB * 64) of one part
+  int kb_total;      // K blocks over all parts
+  int split;         // K ranges (tiles of their own), 1: none
+  int kb_split;      // K blocks of a range (the last may be shorter)
+  int dtype, act;
+  int tma_store;     // outputs stored by TMA; 0: plain stores
+  int save;          // kFfnGated: store g and u too
+  const uint16_t* bias[2];  // kFfnGated: bg, bu or nullptr
+  uint16_t* y[3];    // output bases for plain stores, row pitch N
+  float* partial;    // split > 1: FP32 sums [outputs][split][M][N] (gated: gate, up)
+};
+
+// Shared memory: operand ring, then per epilogue warp two 2 KB staging boxes,
+// then barriers.
+struct FfnLayout {
+  static constexpr int RING_BYTES = 192 * 1024;
+  static constexpr int STG_BYTES = 32 * 32 * 2;
+  static constexpr int OFF_STG = RING_BYTES;
+  static constexpr int OFF_BAR = OFF_STG + kFfnEpiWarps * 2 * STG_BYTES;
+  static constexpr int NUM_BARS = 2 * kFfnMaxStages + 5;  // full, empty, acc full x2, acc empty x2, drain
+  static constexpr int OFF_TMEM_SLOT = OFF_BAR + NUM_BARS * 8;
+  static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
+  static constexpr int DYN_BYTES = OFF_ABORT + 4 + 1024;
+  static_assert(OFF_BAR % 8 == 0, "mbarriers are 8-byte objects");
+  static_assert(DYN_BYTES <= 232448, "more shared memory than a CTA can have");
+};
+
+// 64-element sub-blocks of K per stage.  A CTA pair takes two, so that the
+// issuing thread waits and commits once per eight MMAs (one wait and commit
+// per four leaves gaps in the tensor pipe); a single CTA takes one, for a
+// deeper ring on the small problems it serves.
+__host__ __device__ constexpr int ffn_sub(int cl) { return cl == 2 ? 2 : 1; }
+__host__ __device__ constexpr int ffn_a_bytes(int cl) { return kFfnBM * kFfnBK * 2 * ffn_sub(cl); }
+__host__ __device__ constexpr int ffn_b_bytes(int cl, int bn) { return bn / cl * kFfnBK * 2 * ffn_sub(cl); }
+__host__ __device__ constexpr int ffn_stages(int cl, int bn) {
+  return FfnLayout::RING_BYTES / (ffn_a_bytes(cl) + ffn_b_bytes(cl, bn)) < kFfnMaxStages
+             ? FfnLayout::RING_BYTES / (ffn_a_bytes(cl) + ffn_b_bytes(cl, bn))
+             : kFfnMaxStages;
+}
+
+// Shared-memory matrix descriptor of an MN-major operand in the 128-byte
+// swizzle: 64-element chunks of the contiguous dimension 8 KB apart (leading
+// byte offset), 8-row groups along K 1 KB apart (stride byte offset).
+__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(8192u >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// Loads `rows` x 64 (K) elements of one operand into consecutive shared
+// memory: K-major in one box of `rows` rows, MN-major in boxes of 64.
+template <bool MN, int CL>
+__device__ __forceinline__ void ffn_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int row0, int rows,
+                                         int k0) {
+  if constexpr (MN) {
+    for (int r = 0; r < rows; r += 64) {
+      if constexpr (CL == 2) tma_load_2d_pair(dst + (uint32_t)r * 128u, map, bar, row0 + r, k0);
+      else tma_load_2d(dst + (uint32_t)r * 128u, map, bar, row0 + r, k0);
+    }
+  } else {
+    if constexpr (CL == 2) tma_load_2d_pair(dst, map, bar, k0, row0);
+    else tma_load_2d(dst, map, bar, k0, row0);
+  }
+}
+
+template <int CL, int KIND>
+__global__ void __launch_bounds__(kFfnThreads, 1)
+    ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const FfnGemmArgs args) {
+  using L = FfnLayout;
+  constexpr bool PAIR = CL == 2;
+  constexpr bool A_MN = KIND == kFfnDw;
+  constexpr bool B_MN = KIND != kFfnGated;
+  constexpr int SUB = ffn_sub(CL);
+  constexpr int A_BYTES = ffn_a_bytes(CL);
+  constexpr int A_SUB = A_BYTES / SUB;
+  const int BN = args.bn;
+  const int STAGES = args.stages;
+  const int B_BYTES = ffn_b_bytes(CL, BN);
+  const int B_SUB = B_BYTES / SUB;
+  const int STAGE_BYTES = A_BYTES + B_BYTES;
+  const uint32_t IDESC = idesc_f16_f32acc(PAIR ? 2 * kFfnBM : kFfnBM, (uint32_t)BN) |
+                         (args.dtype == kEpiBf16 ? ((1u << 7) | (1u << 10)) : 0u) |
+                         (A_MN ? (1u << 15) : 0u) | (B_MN ? (1u << 16) : 0u);
+  const uint32_t crank = PAIR ? cluster_ctarank() : 0u;
+  const uint32_t rank = crank & 1u;
+  const bool leader = rank == 0;
+  const int unit = (int)(blockIdx.x / CL);
+  const int units = (int)(gridDim.x / CL);
+  const int tile_rows = CL * kFfnBM;
+
+  // tile t -> (K range, output, M block, N block)
+  auto tile_decode = [&](int t, int& s, int& g, int& mb, int& nb) {
+    int q = t / args.tiles_per_group;
+    const int tl = t - q * args.tiles_per_group;
+    s = q % args.split;
+    g = q / args.split;
+    ffn_tile_coords(tl, args.num_m_blocks, args.num_n_blocks, args.group_m, mb, nb);
+  };
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_addr(smem);
+  const uint32_t bar0 = sbase + L::OFF_BAR;
+  auto bar_full = [&](int s) { return bar0 + 8u * s; };
+  auto bar_empty = [&](int s) { return bar0 + 8u * (kFfnMaxStages + s); };
+  auto bar_cfull = [&](int a) { return bar0 + 8u * (2 * kFfnMaxStages + a); };
+  auto bar_cempty = [&](int a) { return bar0 + 8u * (2 * kFfnMaxStages + 2 + a); };
+  const uint32_t bar_drain = bar0 + 8u * (2 * kFfnMaxStages + 4);
+  auto stage_a = [&](int s) { return sbase + (uint32_t)(s * STAGE_BYTES); };
+  auto stage_b = [&](int s) { return sbase + (uint32_t)(s * STAGE_BYTES + A_BYTES); };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_ABORT);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_TMEM_SLOT);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(bar_full(s), 1u);
+      mbar_init(bar_empty(s), 1u);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(bar_cfull(a), 1u);
+      mbar_init(bar_cempty(a), (uint32_t)(CL * kFfnEpiWarps));
+    }
+    mbar_init(bar_drain, 1u);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kFfnMmaWarp) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_addr(tmem_slot), kFfnTmemCols);
+      tmem_relinquish_alloc_permit_pair();
+    } else {
+      tmem_alloc(smem_addr(tmem_slot), kFfnTmemCols);
+      tmem_relinquish_alloc_permit();
+    }
+  }
+  if (warp == kFfnProdWarp && lane == 0) {
+    tma_prefetch_desc(&maps.a[0]);
+    tma_prefetch_desc(&maps.b[0]);
+  }
+  grid_dep_launch();
+  tc_fence_before_sync();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // both CTAs' barriers exist before any remote signal
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_dep_wait();
+
+  if (warp == kFfnProdWarp) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      long long issued = 0;
+      bool ok = true;
+      for (int t = unit; t < args.num_tiles && ok; t += units) {
+        int s, g, mb, nb;
+        tile_decode(t, s, g, mb, nb);
+        const int kb0 = s * args.kb_split, kb1 = min(args.kb_total, kb0 + args.kb_split);
+        const int arow = mb * tile_rows + (int)rank * kFfnBM;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (issued >= STAGES && !mbar_wait(bar_empty(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
+          const uint32_t fb = bar_full(stage);
+          const uint32_t fbl = PAIR ? map_to_cta(fb, 0u) : fb;  // both CTAs' bytes complete on the even CTA's barrier
+          if (leader) mbar_arrive_expect_tx(fb, (uint32_t)(CL * STAGE_BYTES));
+          const int part = KIND == kFfnDx && kb >= args.kb_part ? 1 : 0;
+          const int kc = (kb - part * args.kb_part) * (SUB * kFfnBK);
+          const CUtensorMap* ma = KIND == kFfnGated ? &maps.a[0] : (KIND == kFfnDx ? &maps.a[part] : &maps.a[g]);
+#pragma unroll
+          for (int h = 0; h < SUB; ++h) {
+            const uint32_t da = stage_a(stage) + (uint32_t)(h * A_SUB), db = stage_b(stage) + (uint32_t)(h * B_SUB);
+            const int k0 = kc + h * kFfnBK;
+            ffn_load<A_MN, CL>(da, ma, fbl, arow, kFfnBM, k0);
+            if constexpr (KIND == kFfnGated) {
+              if constexpr (PAIR) {
+                ffn_load<false, CL>(db, &maps.b[rank], fbl, nb * args.cols, BN / 2, k0);
+              } else {
+                ffn_load<false, CL>(db, &maps.b[0], fbl, nb * args.cols, BN / 2, k0);
+                ffn_load<false, CL>(db + (uint32_t)(BN / 2) * 128u, &maps.b[1], fbl, nb * args.cols, BN / 2, k0);
+              }
+            } else {
+              const CUtensorMap* mbp = KIND == kFfnDx ? &maps.b[part] : &maps.b[0];
+              ffn_load<true, CL>(db, mbp, fbl, nb * args.cols + (int)rank * (BN / CL), BN / CL, k0);
+            }
+          }
+          ++issued;
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      // the last loads land before the CTA can exit (in a pair the odd CTA is
+      // held by the closing cluster barrier)
+      if (leader) {
+        int s = stage;
+        uint32_t ph = phase;
+        for (int i = 0; i < STAGES && i < issued; ++i) {
+          if (s == 0) { s = STAGES - 1; ph ^= 1u; } else { --s; }
+          mbar_wait(bar_full(s), ph, nullptr);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kFfnMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && leader) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int buf = 0;
+      uint32_t buf_phase = 0;
+      bool ok = true;
+      for (int t = unit; t < args.num_tiles && ok; t += units) {
+        int s, g, mb, nb;
+        tile_decode(t, s, g, mb, nb);
+        const int kb0 = s * args.kb_split, kb1 = min(args.kb_total, kb0 + args.kb_split);
+        if (!mbar_wait(bar_cempty(buf), buf_phase ^ 1u, abort_flag)) break;
+        tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(buf * kFfnMaxBN);
+        uint32_t acc = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(bar_full(stage), phase, abort_flag)) { ok = false; break; }
+          tc_fence_after_sync();
+#pragma unroll
+          for (int h = 0; h < SUB; ++h) {
+            const uint32_t sa = stage_a(stage) + (uint32_t)(h * A_SUB), sb = stage_b(stage) + (uint32_t)(h * B_SUB);
+            const uint64_t ad = A_MN ? sdesc_mnmajor_sw128(sa) : sdesc_kmajor_sw128(sa);
+            const uint64_t bd = B_MN ? sdesc_mnmajor_sw128(sb) : sdesc_kmajor_sw128(sb);
+            // 16 elements along K: 32 bytes inside the swizzle row (K-major),
+            // two 8-row groups (MN-major)
+            constexpr uint32_t AK = A_MN ? 2048u >> 4 : 2u, BKS = B_MN ? 2048u >> 4 : 2u;
+#pragma unroll
+            for (int k = 0; k < kFfnBK / 16; ++k) {
+              if constexpr (PAIR) umma_f16_pair(d_tmem, ad + AK * k, bd + BKS * k, IDESC, acc);
+              else umma_f16(d_tmem, ad + AK * k, bd + BKS * k, IDESC, acc);
+              acc = 1u;
+            }
+          }
+          if constexpr (PAIR) umma_commit_pair(bar_empty(stage), 3);
+          else umma_commit(bar_empty(stage));
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        if constexpr (PAIR) umma_commit_pair(bar_cfull(buf), 3);
+        else umma_commit(bar_cfull(buf));
+        if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+      }
+      // every MMA this thread issued has finished before TMEM is released
+      if constexpr (PAIR) umma_commit_pair(bar_drain, 1);
+      else umma_commit(bar_drain);
+      mbar_wait(bar_drain, 0u, nullptr);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;   // TMEM lanes 32q .. 32q+31
+    const int half = warp >> 2;
+    // output columns of this warp: 32-column boxes half, half + 2, ...
+    const int boxes = args.cols / 32;
+    uint8_t* stg = smem + L::OFF_STG + warp * 2 * L::STG_BYTES;
+    const uint32_t stg_addr = sbase + L::OFF_STG + warp * 2 * L::STG_BYTES;
+    int sbuf = 0;
+    int buf = 0;
+    uint32_t buf_phase = 0;
+    const int M = args.M, N = args.N, dt = args.dtype;
+
+    // 16 packed pairs (this lane's row of a 32 x 32 box) to output `o`
+    auto store_box = [&](const uint32_t (&packed)[16], int o, int row0, int nc) {
+      if (args.tma_store) {
+        if (lane == 0) bulk_wait_group_read<1>();
+        __syncwarp();
+      }
+      uint8_t* rowp = stg + sbuf * L::STG_BYTES + lane * 64;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int pos = j ^ ((lane >> 1) & 3);
+        *reinterpret_cast<uint4*>(rowp + pos * 16) =
+            make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+      }
+      if (args.tma_store) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&maps.y[o], stg_addr + sbuf * L::STG_BYTES, nc, row0);
+          bulk_commit_group();
+        }
+      } else {
+        __syncwarp();
+        const uint8_t* box = stg + sbuf * L::STG_BYTES;
+        uint16_t* const yo = o == 0 ? args.y[0] : (o == 1 ? args.y[1] : args.y[2]);
+        const int col = nc + lane;
+#pragma unroll 4
+        for (int rr = 0; rr < 32; ++rr) {
+          const int r = row0 + rr;
+          if (r < M && col < N) {
+            const int pos = (lane >> 3) ^ ((rr >> 1) & 3);
+            yo[(size_t)r * N + col] = *reinterpret_cast<const uint16_t*>(box + rr * 64 + pos * 16 + (lane & 7) * 2);
+          }
+        }
+        __syncwarp();
+      }
+      sbuf ^= 1;
+    };
+    // this lane's row of FP32 sums of a 32 x 32 box to the partial sums
+    auto store_partial = [&](const uint32_t (&r)[32], int slab, int row, int nc) {
+      if (row >= M) return;
+      float* p = args.partial + ((size_t)slab * M + row) * N + nc;
+      if (N % 4 == 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (nc + 4 * j < N)
+            *reinterpret_cast<uint4*>(p + 4 * j) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (nc + j < N) p[j] = __uint_as_float(r[j]);
+      }
+    };
+
+    for (int t = unit; t < args.num_tiles; t += units) {
+      int s, g, mb, nb;
+      tile_decode(t, s, g, mb, nb);
+      const int m0 = mb * tile_rows + (int)rank * kFfnBM + q * 32, n0 = nb * args.cols;
+      const bool got = mbar_wait(bar_cfull(buf), buf_phase, abort_flag);
+      if (!__all_sync(0xffffffffu, got)) break;
+      tc_fence_after_sync();
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kFfnMaxBN);
+#pragma unroll 1
+      for (int bx = half; bx < boxes; bx += 2) {
+        const int nc = n0 + bx * 32;
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(taddr + (uint32_t)(bx * 32), r);
+        if constexpr (KIND == kFfnGated) {
+          uint32_t r2[32];
+          tmem_ld_32x32b_x32(taddr + (uint32_t)(BN / 2 + bx * 32), r2);
+          tmem_ld_wait();
+          if (nc >= N) continue;  // warp-uniform
+          if (args.split > 1) {
+            store_partial(r, s, m0 + lane, nc);
+            store_partial(r2, args.split + s, m0 + lane, nc);
+            continue;
+          }
+          if (args.bias[0] != nullptr || args.bias[1] != nullptr) {
+            // lane l holds the biases of column nc + l
+            const int col = nc + lane;
+            const float bg = (args.bias[0] != nullptr && col < N) ? ep_widen(__ldg(args.bias[0] + col), dt) : 0.0f;
+            const float bu = (args.bias[1] != nullptr && col < N) ? ep_widen(__ldg(args.bias[1] + col), dt) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              r[j] = __float_as_uint(__uint_as_float(r[j]) + __shfl_sync(0xffffffffu, bg, j));
+              r2[j] = __float_as_uint(__uint_as_float(r2[j]) + __shfl_sync(0xffffffffu, bu, j));
+            }
+          }
+          uint32_t packed[16];
+          if (args.save) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              packed[i] = ep_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), dt);
+            store_box(packed, 1, m0, nc);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              packed[i] = ep_pack(__uint_as_float(r2[2 * i]), __uint_as_float(r2[2 * i + 1]), dt);
+            store_box(packed, 2, m0, nc);
+          }
+          auto gate = [&](auto act) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              packed[i] = ep_pack(act_value_t<decltype(act)::value>(__uint_as_float(r[2 * i])) * __uint_as_float(r2[2 * i]),
+                                  act_value_t<decltype(act)::value>(__uint_as_float(r[2 * i + 1])) * __uint_as_float(r2[2 * i + 1]),
+                                  dt);
+          };
+          if (args.act == kActSilu) gate(std::integral_constant<int, kActSilu>{});
+          else if (args.act == kActGeluTanh) gate(std::integral_constant<int, kActGeluTanh>{});
+          else gate(std::integral_constant<int, kActGeluErf>{});
+          store_box(packed, 0, m0, nc);
+        } else {
+          tmem_ld_wait();
+          if (nc >= N) continue;
+          if (args.split > 1) {
+            store_partial(r, g * args.split + s, m0 + lane, nc);
+            continue;
+          }
+          uint32_t packed[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            packed[i] = ep_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), dt);
+          store_box(packed, KIND == kFfnDw ? g : 0, m0, nc);
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_cluster(map_to_cta(bar_cempty(buf), 0u));
+        else mbar_arrive(bar_cempty(buf));
+      }
+      if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+    }
+    if (args.tma_store && lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();
+  if (warp == kFfnMmaWarp) {
+    tc_fence_after_sync();
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, kFfnTmemCols);
+    else tmem_dealloc(tmem_base, kFfnTmemCols);
+  }
+}
+
+}  // namespace poot

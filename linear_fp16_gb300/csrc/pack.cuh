@@ -45,7 +45,7 @@ __device__ __forceinline__ uint4 pack_load8(const uint16_t* __restrict__ s) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a) {
+static __global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a) {
   grid_dep_wait();  // x and W may come from the previous grid
   grid_dep_launch();
   const long long cpr = a.Kp / 8;  // 16-byte chunks per packed row

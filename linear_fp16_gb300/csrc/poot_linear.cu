@@ -17,6 +17,7 @@
 #include "poot_linear.h"
 #include "gemm_tcgen05.cuh"
 #include "gemv.cuh"
+#include "host.cuh"
 #include "pack.cuh"
 #include "shards.cuh"
 #include "splitk.cuh"
@@ -24,6 +25,7 @@
 namespace {
 
 using namespace poot;
+using namespace poot_host;
 
 constexpr int kVersion = 100;  // 0.1.0
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
@@ -46,8 +48,6 @@ constexpr int kStepsChunkK = 2048;
 
 constexpr int kGemvSmemBudget = 64 * 1024;  // bytes of x staged per GEMV block
 
-thread_local cudaError_t t_last_cuda_error = cudaSuccess;
-
 struct DeviceState {
   bool ready = false;
   int status = POOT_OK;  // POOT_OK or POOT_ERR_UNSUPPORTED_DEVICE / CUDA
@@ -57,13 +57,6 @@ struct DeviceState {
 
 std::mutex g_mu;
 DeviceState g_devices[kMaxDevices];
-using EncodeTiledFn = decltype(&cuTensorMapEncodeTiled);
-EncodeTiledFn g_encode_tiled = nullptr;
-
-int cuda_fail(cudaError_t e) {
-  t_last_cuda_error = e;
-  return POOT_ERR_CUDA;
-}
 
 template <int MODE, int CL, int EPI = kEpiPlain>
 cudaError_t set_gemm_attrs() {
@@ -96,23 +89,13 @@ int device_state(int* dev_out, DeviceState** st_out) {
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState& st = g_devices[dev];
   if (!st.ready) {
-    int major = 0, minor = 0, sms = 0;
-    if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev)) != cudaSuccess ||
-        (e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev)) != cudaSuccess ||
-        (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-      return cuda_fail(e);
-    if (major != 10 || minor != 3) {
+    int sms = 0;
+    const int q = device_query(dev, &sms);
+    if (q == POOT_ERR_CUDA) return q;
+    if (q != POOT_OK) {
       st.ready = true;
-      st.status = POOT_ERR_UNSUPPORTED_DEVICE;
+      st.status = q;
     } else {
-      if (g_encode_tiled == nullptr) {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
-        if (e != cudaSuccess) return cuda_fail(e);
-        if (q != cudaDriverEntryPointSuccess || fn == nullptr) return cuda_fail(cudaErrorNotSupported);
-        g_encode_tiled = reinterpret_cast<EncodeTiledFn>(fn);
-      }
       if ((e = set_gemm_attrs<kLoadTma, 1>()) != cudaSuccess || (e = set_gemm_attrs<kLoadTma, 2>()) != cudaSuccess ||
           (e = set_gemm_attrs<kLoadCpAsync4, 1>()) != cudaSuccess ||
           (e = set_gemm_attrs<kLoadReg16, 1>()) != cudaSuccess ||
@@ -142,49 +125,6 @@ int device_state(int* dev_out, DeviceState** st_out) {
   *dev_out = dev;
   *st_out = &st;
   return st.status;
-}
-
-// Launch with programmatic stream serialisation (see grid_dep_wait in
-// ptx.cuh): the kernel may be scheduled while the previous kernel in the
-// stream drains; it waits for that kernel before touching global memory.
-// cluster_x > 1 launches clusters of that many CTAs along x.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_clustered(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                             unsigned cluster_x, Args&&... args) {
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  std::memset(attr, 0, sizeof(attr));
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.numAttrs = 1;
-  if (cluster_x > 1) {
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster_x;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
-  }
-  cfg.attrs = attr;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
-template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                   Args&&... args) {
-  return launch_clustered(kernel, grid, block, smem, stream, 1u, std::forward<Args>(args)...);
-}
-
-inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-inline bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
-  if (a == nullptr || b == nullptr || abytes <= 0 || bbytes <= 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + static_cast<uintptr_t>(bbytes) && b0 < a0 + static_cast<uintptr_t>(abytes);
 }
 
 // Argument checks shared by every entry point (no CUDA calls).
@@ -229,50 +169,6 @@ bool variant_applicable(int v, const void* x, const void* w, int64_t M, int64_t 
     case POOT_VARIANT_GEMM_PACKED: return !empty && K > 0;
     default: return false;
   }
-}
-
-// [slabs][outer][inner] tensor of FP32, box [1][box_outer][box_inner].
-bool encode_3d_f32(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t slabs,
-                   uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle) {
-  const cuuint64_t dims[3] = {inner, outer, slabs};
-  const cuuint64_t strides[2] = {inner * 4, inner * outer * 4};
-  const cuuint32_t box[3] = {box_inner, box_outer, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = g_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides,
-                                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-// Row-major [outer, inner] tensor of 2-byte elements (binary16, or bfloat16
-// when bf16), rows `pitch` elements apart (default inner), box [box_outer,
-// box_inner].
-bool encode_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
-               uint32_t box_outer, CUtensorMapSwizzle swizzle, bool bf16 = false, uint64_t pitch = 0) {
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {(pitch != 0 ? pitch : inner) * 2};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = g_encode_tiled(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                                    2, const_cast<void*>(base), dims,
-                                    strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-// [slabs][outer][inner] tensor of 2-byte elements, box [1][box_outer][box_inner]
-// (each box stays inside one slab: stores clip at `outer` per slab).
-bool encode_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t slabs,
-               uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle, bool bf16) {
-  const cuuint64_t dims[3] = {inner, outer, slabs};
-  const cuuint64_t strides[2] = {inner * 2, inner * outer * 2};
-  const cuuint32_t box[3] = {box_inner, box_outer, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = g_encode_tiled(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                                    3, const_cast<void*>(base), dims, strides, box, estr,
-                                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
 }
 
 struct GemmPlan {
@@ -390,112 +286,6 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, int sms, int bn_req, int gro
   const int chunk_k = chunk_req > 0 ? chunk_req : kDefaultChunkK;
   p.chunk_kb = chunk_k / kGemmBK;
   return p;
-}
-
-// ---- split-K workspace ------------------------------------------------------
-struct Workspace {
-  void* ptr = nullptr;
-  size_t bytes = 0;
-};
-std::mutex g_ws_mu;
-// key: (device, stream, thread): the thread is part of the key only for
-// cudaStreamPerThread, one handle that names a different stream in each thread
-struct WorkspaceKey {
-  int dev;
-  cudaStream_t stream;
-  std::thread::id thread;
-  bool operator<(const WorkspaceKey& o) const {
-    if (dev != o.dev) return dev < o.dev;
-    if (stream != o.stream) return std::less<cudaStream_t>()(stream, o.stream);
-    return thread < o.thread;
-  }
-};
-std::map<WorkspaceKey, Workspace> g_ws;
-std::vector<void*> g_ws_retired;
-
-struct WorkspaceRelease {
-  ~WorkspaceRelease() {
-    for (auto& kv : g_ws)
-      if (kv.second.ptr != nullptr) cudaFree(kv.second.ptr);
-    for (void* p : g_ws_retired) cudaFree(p);
-  }
-} g_ws_release;
-
-// Workspace of a call (split-K partial sums, packed operands).  Outside
-// stream capture: one buffer per (device, stream; thread for
-// cudaStreamPerThread), grown by doubling and kept for the life of the process
-// (calls on one stream are ordered, so they can share it; a buffer outgrown
-// is kept too, as work queued earlier may still read it).  Under capture:
-// a graph-owned allocation (cudaMallocAsync / cudaFreeAsync on the capturing
-// stream become memory nodes of the graph), so that a graph never shares a
-// buffer with calls made outside it.  nullptr: no workspace, no split.
-struct WorkspaceLease {
-  void* ptr = nullptr;
-  bool graph_owned = false;
-  cudaStream_t stream = nullptr;
-  // a graph-owned workspace is freed on its stream after the last kernel
-  // that reads it (or on any early return before those launches)
-  cudaError_t release() {
-    cudaError_t e = cudaSuccess;
-    if (graph_owned) e = cudaFreeAsync(ptr, stream);
-    graph_owned = false;
-    return e;
-  }
-  WorkspaceLease() = default;
-  WorkspaceLease(const WorkspaceLease&) = delete;
-  WorkspaceLease& operator=(const WorkspaceLease&) = delete;
-  WorkspaceLease(WorkspaceLease&& o) noexcept : ptr(o.ptr), graph_owned(o.graph_owned), stream(o.stream) {
-    o.graph_owned = false;
-  }
-  WorkspaceLease& operator=(WorkspaceLease&& o) noexcept {
-    if (this != &o) {
-      (void)release();
-      ptr = o.ptr;
-      graph_owned = o.graph_owned;
-      stream = o.stream;
-      o.graph_owned = false;
-    }
-    return *this;
-  }
-  ~WorkspaceLease() { (void)release(); }
-};
-
-WorkspaceLease stream_workspace(int dev, cudaStream_t stream, size_t bytes) {
-  WorkspaceLease lease;
-  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return lease;
-  }
-  if (cs != cudaStreamCaptureStatusNone) {
-    if (cs != cudaStreamCaptureStatusActive || cudaMallocAsync(&lease.ptr, bytes, stream) != cudaSuccess) {
-      (void)cudaGetLastError();
-      lease.ptr = nullptr;
-      return lease;
-    }
-    lease.graph_owned = true;
-    lease.stream = stream;
-    return lease;
-  }
-  std::lock_guard<std::mutex> lock(g_ws_mu);
-  const std::thread::id tid = stream == cudaStreamPerThread ? std::this_thread::get_id() : std::thread::id();
-  Workspace& ws = g_ws[WorkspaceKey{dev, stream, tid}];
-  if (ws.bytes >= bytes) {
-    lease.ptr = ws.ptr;
-    return lease;
-  }
-  size_t want = bytes > 2 * ws.bytes ? bytes : 2 * ws.bytes;
-  want = (want + (size_t(1) << 20) - 1) & ~((size_t(1) << 20) - 1);
-  void* p = nullptr;
-  if (cudaMalloc(&p, want) != cudaSuccess) {
-    (void)cudaGetLastError();  // no split-K then; not an error of the call
-    return lease;
-  }
-  if (ws.ptr != nullptr) g_ws_retired.push_back(ws.ptr);
-  ws.ptr = p;
-  ws.bytes = want;
-  lease.ptr = p;
-  return lease;
 }
 
 constexpr int kMaxSplitK = 16;
@@ -1279,9 +1069,12 @@ int poot_linear_device_status(poot_stream_t stream) {
     const unsigned int zero = 0;
     e = cudaMemcpyToSymbol(poot::g_device_error, &zero, sizeof(zero));
     if (e != cudaSuccess) return cuda_fail(e);
-    return POOT_ERR_DEVICE_TIMEOUT;
   }
-  return POOT_OK;
+  // the feed-forward kernels' word (their own translation unit)
+  unsigned int ffn_word = 0;
+  e = take_ffn_device_error(&ffn_word);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return (word | ffn_word) != 0 ? POOT_ERR_DEVICE_TIMEOUT : POOT_OK;
 }
 
 int poot_linear_version(void) { return kVersion; }

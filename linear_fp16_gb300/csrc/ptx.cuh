@@ -10,8 +10,9 @@
 namespace poot {
 
 // Device-side error word (one per device): bit 0 = a bounded wait ran out.
-// Defined here: the library is one translation unit (poot_linear.cu).
-__device__ unsigned int g_device_error = 0;
+// Each translation unit has its own word; poot_linear_device_status() reads
+// them all.
+static __device__ unsigned int g_device_error = 0;
 constexpr unsigned int kErrTimeout = 1u;
 
 // A wait that takes longer than this has lost its producer; normal waits in
