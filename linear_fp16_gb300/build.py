@@ -21,7 +21,7 @@ LIB = os.path.join(BUILD, "libpoot_linear.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("poot_linear.cu", "poot_ffn.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in (
     "ptx.cuh", "gemm_tcgen05.cuh", "gemv.cuh", "epilogue.cuh", "splitk.cuh", "pack.cuh", "shards.cuh", "host.cuh",
-    "ffn_gemm.cuh", "ffn_elem.cuh", "clip.cuh")] + [
+    "mma.cuh", "ffn_gemm.cuh", "ffn_gemv.cuh", "ffn_elem.cuh", "clip.cuh")] + [
     os.path.join(INCLUDE, f) for f in ("poot_linear.h", "poot_ffn.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

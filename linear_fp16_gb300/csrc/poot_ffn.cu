@@ -14,6 +14,7 @@
 #include "clip.cuh"
 #include "ffn_elem.cuh"
 #include "ffn_gemm.cuh"
+#include "ffn_gemv.cuh"
 #include "host.cuh"
 
 namespace poot_host {
@@ -94,15 +95,15 @@ int64_t span_bytes(int64_t rows, int64_t cols, int64_t ld) {
 }
 
 // outputs may overlap neither an input nor one another; 2-byte alignment
-int check_spans(const std::vector<Span>& in, const std::vector<Span>& out) {
-  for (const auto* v : {&in, &out})
-    for (const Span& s : *v)
+int check_spans(std::initializer_list<Span> in, std::initializer_list<Span> out) {
+  for (const auto& v : {in, out})
+    for (const Span& s : v)
       if (s.p != nullptr && !aligned(s.p, 2)) return POOT_ERR_MISALIGNED;
-  for (size_t i = 0; i < out.size(); ++i) {
+  for (const Span* o = out.begin(); o != out.end(); ++o) {
     for (const Span& s : in)
-      if (overlaps(out[i].p, out[i].bytes, s.p, s.bytes)) return POOT_ERR_INVALID_ARG;
-    for (size_t j = 0; j < i; ++j)
-      if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return POOT_ERR_INVALID_ARG;
+      if (overlaps(o->p, o->bytes, s.p, s.bytes)) return POOT_ERR_INVALID_ARG;
+    for (const Span* q = out.begin(); q != o; ++q)
+      if (overlaps(o->p, o->bytes, q->p, q->bytes)) return POOT_ERR_INVALID_ARG;
   }
   return POOT_OK;
 }
@@ -296,6 +297,44 @@ int finish(WorkspaceLease& lease, int rc) {
 }
 
 // ---- the gated block ------------------------------------------------------------
+template <int NT, int WARPS>
+cudaError_t launch_gated_gemv(const GatedGemvArgs& a, bool bf16, bool vec, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(ceil_div(a.N, 16))), block(WARPS * 32);
+  if (bf16)
+    return vec ? launch(gated_gemv_kernel<NT, WARPS, kEpiBf16, true>, grid, block, 0, stream, a)
+               : launch(gated_gemv_kernel<NT, WARPS, kEpiBf16, false>, grid, block, 0, stream, a);
+  return vec ? launch(gated_gemv_kernel<NT, WARPS, kEpiF16, true>, grid, block, 0, stream, a)
+             : launch(gated_gemv_kernel<NT, WARPS, kEpiF16, false>, grid, block, 0, stream, a);
+}
+
+int gated_gemv(const poot_gated_linear_args& p, int64_t ldx, const FfnDevice& d, cudaStream_t stream) {
+  GatedGemvArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = static_cast<const uint16_t*>(p.x);
+  a.wg = static_cast<const uint16_t*>(p.wg);
+  a.wu = static_cast<const uint16_t*>(p.wu);
+  a.bias[0] = static_cast<const uint16_t*>(p.bg);
+  a.bias[1] = static_cast<const uint16_t*>(p.bu);
+  a.y[0] = static_cast<uint16_t*>(p.h);
+  a.y[1] = static_cast<uint16_t*>(p.g);
+  a.y[2] = static_cast<uint16_t*>(p.u);
+  a.ldx = ldx;
+  a.M = static_cast<int>(p.M);
+  a.N = static_cast<int>(p.N);
+  a.K = static_cast<int>(p.K);
+  a.act = p.activation;
+  a.save = p.g != nullptr;
+  const bool bf16 = p.dtype == POOT_DTYPE_BF16;
+  const bool vec = p.K % 8 == 0 && ldx % 8 == 0 && aligned(p.x, 16) && aligned(p.wg, 16) && aligned(p.wu, 16);
+  const bool few = ceil_div(p.N, 16) < 2 * int64_t(d.sms);
+  cudaError_t e;
+  if (p.M <= 8)
+    e = few ? launch_gated_gemv<1, 16>(a, bf16, vec, stream) : launch_gated_gemv<1, 8>(a, bf16, vec, stream);
+  else
+    e = few ? launch_gated_gemv<2, 16>(a, bf16, vec, stream) : launch_gated_gemv<2, 8>(a, bf16, vec, stream);
+  return e == cudaSuccess ? POOT_OK : cuda_fail(e);
+}
+
 int gated_linear(const poot_gated_linear_args* ap, cudaStream_t stream) {
   if (ap == nullptr) return POOT_ERR_INVALID_ARG;
   const poot_gated_linear_args& p = *ap;
@@ -327,6 +366,7 @@ int gated_linear(const poot_gated_linear_args* ap, cudaStream_t stream) {
     const cudaError_t e = launch(gated_bias_kernel, dim3(grid_for(M * N, d->sms)), dim3(256), 0, stream, r);
     return e == cudaSuccess ? POOT_OK : cuda_fail(e);
   }
+  if (M <= POOT_GEMV_MAX_M) return gated_gemv(p, ldx, *d, stream);
   FfnCall c;
   c.kind = kFfnGated;
   c.a[0] = {p.x, M, K, ldx};

@@ -9,7 +9,10 @@ the status code; every step of the computation runs in the CUDA library.
 from __future__ import annotations
 
 import ctypes
+import struct
 import threading
+
+import torch
 
 from . import binding as _b
 
@@ -102,82 +105,135 @@ def poot_clip_grad_norm(tensors, count: int, max_norm: float, norm: int, stream:
 
 
 # ---- tensor-level calls ----------------------------------------------------
-def _matrix(t, name, shape, like=None):
-    """t as a 2-D CUDA tensor of `shape` (None: any extent), unit column stride."""
-    import torch
+# Decode-sized calls take a few microseconds on the GPU, so the host's part
+# is kept short: one combined check per tensor (the error texts are made only
+# when it fails), the argument structures packed as bytes, the stream handle
+# read directly.
+_PACK_GATED = struct.Struct("@8P4q2i")
+_PACK_GATED_BWD = struct.Struct("@11P7q2i")
+_PACK_LINEAR_BWD = struct.Struct("@6P5qi4x")
+_PACK_GRAD = struct.Struct("@2Pqi4x")
+_packed = {}
+
+
+def _packed_fn(name):
+    """The C function `name` taking its arguments as packed bytes."""
+    fn = _packed.get(name)
+    if fn is None:
+        fn = load_library()[name]  # a function object of its own
+        fn.restype = _INT
+        args = [ctypes.c_char_p, _VP]
+        if name == "poot_clip_grad_norm":
+            args = [ctypes.c_char_p, _I64, ctypes.c_float, _VP, _VP]
+        fn.argtypes = args
+        _packed[name] = fn
+    return fn
+
+
+def _refuse(t, name, dtype, device, shape, dense):
+    """Raises what _ok found wrong with t."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in (torch.float16, torch.bfloat16) or (like is not None and t.dtype != like.dtype):
+    if t.dtype not in _CODES or t.dtype != dtype:
         raise TypeError(f"{name} must be float16 or bfloat16, one dtype for all tensors, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if like is not None and t.device != like.device:
+    if t.get_device() != device:
         raise ValueError(f"{name} must be on the same device as the other tensors")
-    if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    return t
+    raise ValueError(f"{name} must be contiguous" if dense else
+                     f"{name} must have unit column stride and rows that do not overlap")
 
 
-def _rows(t, name, shape, like=None):
-    """A matrix whose rows may be further apart than its columns (a view)."""
-    _matrix(t, name, shape, like)
-    rows, cols = t.shape
-    if t.numel() > 0 and ((cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols)):
-        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
-    return t
+_CODES = {torch.float16: _b.DTYPE_F16, torch.bfloat16: _b.DTYPE_BF16}
 
 
-def _dense(t, name, shape, like=None):
-    _matrix(t, name, shape, like)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+def _first(x):
+    """dtype, its code, device index, rows, columns and row pitch of x [M,K]."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dtype = x.dtype
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"x must be float16 or bfloat16, got {dtype}")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if x.dim() != 2:
+        raise ValueError(f"x must have 2 dims, got {tuple(x.shape)}")
+    device = x.get_device()
+    M, K = x.shape
+    return dtype, code, device, M, K, _pitch(x, "x", dtype, device, (M, K))
 
 
-def _ld(t):
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _pitch(t, name, dtype, device, shape):
+    """Row pitch of a matrix whose rows may be further apart than its columns."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.shape == shape):
+        _refuse(t, name, dtype, device, shape, False)
+    if t.is_contiguous():
+        return shape[1]
+    rows, cols = shape
+    s0, s1 = t.stride()
+    if (cols > 1 and s1 != 1) or (rows > 1 and s0 < cols):
+        _refuse(t, name, dtype, device, shape, False)
+    return s0 if rows > 1 else cols
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _dense(t, name, dtype, device, shape):
+    """Address of a contiguous tensor."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.shape == shape
+            and t.is_contiguous()):
+        _refuse(t, name, dtype, device, shape, True)
+    return t.data_ptr()
+
+
+def _rows_of(w, name):
+    if not isinstance(w, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if w.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got {tuple(w.shape)}")
+    return w.shape[0]
 
 
 def _act(activation):
-    if activation not in ACT_CODES:
+    act = ACT_CODES.get(activation)
+    if act is None:
         raise ValueError(f"unknown activation {activation!r}; one of {sorted(ACT_CODES)}")
-    return ACT_CODES[activation]
+    return act
 
 
-def _dtype(t):
-    import torch
-    return _b.DTYPE_BF16 if t.dtype == torch.bfloat16 else _b.DTYPE_F16
+def _stream(device, stream):
+    """(handle, other): the stream's handle, and whether it is not the current one."""
+    current = torch._C._cuda_getCurrentRawStream(device)
+    if stream is None:
+        return current, None
+    return stream.cuda_stream, (stream if stream.cuda_stream != current else None)
 
 
-class _Launch:
-    """The stream of a call, and the tensors it allocates: from that stream's
-    memory, and kept from reuse while the caller's stream may still read them."""
+def _empty(like, shape, other, dtype=None):
+    """An output of the call: from its stream's memory, and kept from reuse
+    while the caller's current stream may still read it."""
+    if other is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(other):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
 
-    def __init__(self, device, stream):
-        import torch
-        self.current = torch.cuda.current_stream(device)
-        self.stream = self.current if stream is None else stream
-        self.device = device
 
-    def empty(self, shape, dtype):
-        import torch
-        if self.stream == self.current:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.stream):
-            t = torch.empty(shape, dtype=dtype, device=self.device)
-        t.record_stream(self.current)
-        return t
+def _call(name, device, *args):
+    fn = _packed_fn(name)
+    if torch._C._cuda_getDevice() == device:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args)
+    if rc != _b.POOT_OK:
+        raise _b.PootLinearError(rc, name)
 
-    def call(self, fn, name, *args):
-        import torch
-        with torch.cuda.device(self.device):
-            rc = fn(*args, self.stream.cuda_stream)
-        if rc != _b.POOT_OK:
-            raise _b.PootLinearError(rc, name)
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
 
 
 def gated_linear(x, wg, wu, bg=None, bu=None, *, activation: str = "silu", save: bool = False, out=None,
@@ -191,25 +247,23 @@ def gated_linear(x, wg, wu, bg=None, bu=None, *, activation: str = "silu", save:
     pre-activations, rounded to the dtype, that gated_linear_backward reads.
     Runs on ``stream`` (default: the current stream of x's device).
     """
-    _rows(x, "x", (None, None))
-    M, K = x.shape
-    _dense(wg, "wg", (None, K), x)
-    N = wg.shape[0]
-    _dense(wu, "wu", (N, K), x)
-    for name, b in (("bg", bg), ("bu", bu)):
-        if b is not None:
-            _dense(b, name, (N,), x)
+    dtype, code, dev, M, K, ldx = _first(x)
+    N = _rows_of(wg, "wg")
+    pg, pu = _dense(wg, "wg", dtype, dev, (N, K)), _dense(wu, "wu", dtype, dev, (N, K))
+    pbg = 0 if bg is None else _dense(bg, "bg", dtype, dev, (N,))
+    pbu = 0 if bu is None else _dense(bu, "bu", dtype, dev, (N,))
     act = _act(activation)
-    run = _Launch(x.device, stream)
+    handle, other = _stream(dev, stream)
     if out is None:
-        out = run.empty((M, N), x.dtype)
+        out = _empty(x, (M, N), other)
+        po = out.data_ptr()
     else:
-        _dense(out, "out", (M, N), x)
-    g = run.empty((M, N), x.dtype) if save else None
-    u = run.empty((M, N), x.dtype) if save else None
-    args = GatedLinearArgs(_ptr(x), _ptr(wg), _ptr(wu), _ptr(bg), _ptr(bu), _ptr(out), _ptr(g), _ptr(u), M, N, K,
-                           _ld(x), _dtype(x), act)
-    run.call(poot_gated_linear, "poot_gated_linear", args)
+        po = _dense(out, "out", dtype, dev, (M, N))
+    g = u = None
+    if save:
+        g, u = _empty(x, (M, N), other), _empty(x, (M, N), other)
+    _call("poot_gated_linear", dev,
+          _PACK_GATED.pack(x.data_ptr(), pg, pu, pbg, pbu, po, _ptr(g), _ptr(u), M, N, K, ldx, code, act), handle)
     return (out, g, u) if save else out
 
 
@@ -220,42 +274,49 @@ def gated_linear_backward(dh, x, wg, wu, g, u, *, activation: str = "silu", need
     dh, g and u [M,N] and x [M,K] may have rows further apart than their
     columns; g and u are what gated_linear returned with ``save``.
     """
-    _rows(x, "x", (None, None))
-    M, K = x.shape
-    _dense(wg, "wg", (None, K), x)
-    N = wg.shape[0]
-    _dense(wu, "wu", (N, K), x)
-    for name, t in (("dh", dh), ("g", g), ("u", u)):
-        _rows(t, name, (M, N), x)
+    dtype, code, dev, M, K, ldx = _first(x)
+    N = _rows_of(wg, "wg")
+    pg, pu = _dense(wg, "wg", dtype, dev, (N, K)), _dense(wu, "wu", dtype, dev, (N, K))
+    ld_dh = _pitch(dh, "dh", dtype, dev, (M, N))
+    ld_g, ld_u = _pitch(g, "g", dtype, dev, (M, N)), _pitch(u, "u", dtype, dev, (M, N))
     act = _act(activation)
-    run = _Launch(x.device, stream)
-    dx = run.empty((M, K), x.dtype) if need_dx else None
-    dwg = run.empty((N, K), x.dtype) if need_dw else None
-    dwu = run.empty((N, K), x.dtype) if need_dw else None
-    dbg = run.empty((N,), x.dtype) if need_db else None
-    dbu = run.empty((N,), x.dtype) if need_db else None
-    args = GatedLinearBackwardArgs(_ptr(dh), _ptr(x), _ptr(wg), _ptr(wu), _ptr(g), _ptr(u), _ptr(dx), _ptr(dwg),
-                                   _ptr(dwu), _ptr(dbg), _ptr(dbu), M, N, K, _ld(dh), _ld(x), _ld(g), _ld(u),
-                                   _dtype(x), act)
-    run.call(poot_gated_linear_backward, "poot_gated_linear_backward", args)
+    handle, other = _stream(dev, stream)
+    dx = _empty(x, (M, K), other) if need_dx else None
+    dwg, dwu = (_empty(x, (N, K), other), _empty(x, (N, K), other)) if need_dw else (None, None)
+    dbg, dbu = (_empty(x, (N,), other), _empty(x, (N,), other)) if need_db else (None, None)
+    _call("poot_gated_linear_backward", dev,
+          _PACK_GATED_BWD.pack(dh.data_ptr(), x.data_ptr(), pg, pu, g.data_ptr(), u.data_ptr(), _ptr(dx), _ptr(dwg),
+                               _ptr(dwu), _ptr(dbg), _ptr(dbu), M, N, K, ld_dh, ldx, ld_g, ld_u, code, act), handle)
     return dx, dwg, dwu, dbg, dbu
 
 
 def linear_backward(dy, x, w, *, need_dx: bool = True, need_dw: bool = True, need_db: bool = True, stream=None):
     """Gradients (dx, dw, db) of y = x W^T + b for dy [M,N]; None where not needed."""
-    _rows(x, "x", (None, None))
-    M, K = x.shape
-    _dense(w, "w", (None, K), x)
-    N = w.shape[0]
-    _rows(dy, "dy", (M, N), x)
-    run = _Launch(x.device, stream)
-    dx = run.empty((M, K), x.dtype) if need_dx else None
-    dw = run.empty((N, K), x.dtype) if need_dw else None
-    db = run.empty((N,), x.dtype) if need_db else None
-    args = LinearBackwardArgs(_ptr(dy), _ptr(x), _ptr(w), _ptr(dx), _ptr(dw), _ptr(db), M, N, K, _ld(dy), _ld(x),
-                              _dtype(x))
-    run.call(poot_linear_backward, "poot_linear_backward", args)
+    dtype, code, dev, M, K, ldx = _first(x)
+    N = _rows_of(w, "w")
+    pw = _dense(w, "w", dtype, dev, (N, K))
+    ld_dy = _pitch(dy, "dy", dtype, dev, (M, N))
+    handle, other = _stream(dev, stream)
+    dx = _empty(x, (M, K), other) if need_dx else None
+    dw = _empty(x, (N, K), other) if need_dw else None
+    db = _empty(x, (N,), other) if need_db else None
+    _call("poot_linear_backward", dev,
+          _PACK_LINEAR_BWD.pack(dy.data_ptr(), x.data_ptr(), pw, _ptr(dx), _ptr(dw), _ptr(db), M, N, K, ld_dy, ldx,
+                                code), handle)
     return dx, dw, db
+
+
+_GRAD_CODES = {torch.float16: GRAD_F16, torch.bfloat16: GRAD_BF16, torch.float32: GRAD_F32}
+
+
+def _refuse_grad(g, d, i, device):
+    """Raises what clip_grad_norm found wrong with pair i."""
+    for name, t in (("grads", g), ("out", d)):
+        if not isinstance(t, torch.Tensor) or t.dtype not in _GRAD_CODES:
+            raise TypeError(f"{name}[{i}] must be a float16, bfloat16 or float32 tensor")
+        if t.get_device() != device or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor on the device of the first")
+    raise ValueError(f"out[{i}] must have the shape and dtype of grads[{i}]")
 
 
 def clip_grad_norm(grads, max_norm: float, *, out=None, stream=None):
@@ -267,26 +328,24 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, stream=None):
     instead.  The norm, over all tensors together, is a float32 scalar tensor
     on the device (the call does not synchronise).
     """
-    import torch
-    codes = {torch.float16: GRAD_F16, torch.bfloat16: GRAD_BF16, torch.float32: GRAD_F32}
     grads = list(grads)
     dsts = grads if out is None else list(out)
     if not grads:
         raise ValueError("grads must hold at least one tensor")
     if len(dsts) != len(grads):
         raise ValueError(f"out must hold {len(grads)} tensors, got {len(dsts)}")
-    table = (GradTensor * len(grads))()
-    device = grads[0].device if isinstance(grads[0], torch.Tensor) else None
+    first = grads[0]
+    device = first.get_device() if isinstance(first, torch.Tensor) and first.is_cuda else -1
+    pack, codes, rows = _PACK_GRAD.pack, _GRAD_CODES, []
     for i, (g, d) in enumerate(zip(grads, dsts)):
-        for name, t in (("grads", g), ("out", d)):
-            if not isinstance(t, torch.Tensor) or t.dtype not in codes:
-                raise TypeError(f"{name}[{i}] must be a float16, bfloat16 or float32 tensor")
-            if not t.is_cuda or t.device != device or not t.is_contiguous():
-                raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor on the device of the first")
-        if d.dtype != g.dtype or d.shape != g.shape:
-            raise ValueError(f"out[{i}] must have the shape and dtype of grads[{i}]")
-        table[i] = GradTensor(g.data_ptr(), d.data_ptr(), g.numel(), codes[g.dtype])
-    run = _Launch(device, stream)
-    norm = run.empty((), torch.float32)
-    run.call(poot_clip_grad_norm, "poot_clip_grad_norm", table, len(grads), float(max_norm), norm.data_ptr())
+        if not (device >= 0 and isinstance(g, torch.Tensor) and g.dtype in codes and g.get_device() == device
+                and g.is_contiguous()):
+            _refuse_grad(g, d, i, device)
+        if d is not g and not (isinstance(d, torch.Tensor) and d.dtype is g.dtype and d.get_device() == device
+                               and d.shape == g.shape and d.is_contiguous()):
+            _refuse_grad(g, d, i, device)
+        rows.append(pack(g.data_ptr(), d.data_ptr(), g.numel(), codes[g.dtype]))
+    handle, other = _stream(device, stream)
+    norm = _empty(first, (), other, torch.float32)
+    _call("poot_clip_grad_norm", device, b"".join(rows), len(grads), max_norm, norm.data_ptr(), handle)
     return norm
