@@ -1,15 +1,22 @@
 // The gated block for up to 16 rows of x (a decode step): a stream of both
-// weights.
+// weights, bound by HBM (4 K bytes per output column).
 //
-// A block owns 16 output columns, i.e. 16 rows of Wg and the same 16 of Wu;
-// its warps split K.  Per step of 32 along K lane (r = lane / 4, t = lane % 4)
-// loads the 16-byte vectors [r][k + 8t ..) and [r + 8][k + 8t ..) of both
-// weights and x[r][k + 8t ..) (x[r + 8] too when M > 8).  The summation order
-// is free, so K is permuted inside a step: these registers then are the A (W)
-// and B (x^T) fragments of two m16n8k16 MMAs per weight, without shuffles,
-// and both weights share the x fragments.  Warps meet in shared memory in a
-// fixed order; one thread holds g and u of an output and finishes it.
-// Bound by HBM: 4 K bytes per output column.
+// gated_gemv_kernel: operands on 16-byte boundaries.  One block per SM owns
+// an equal share of consecutive output columns, whatever their number (its
+// last columns may fill only part of an MMA: what is not there is not loaded),
+// and walks it in passes of up to 16 columns; sixteen warps split K.  Lane
+// (r = lane / 4, t = lane % 4) takes, per step of 32 along K and group of 8
+// columns, the vectors Wg[n + r][k + 8t ..) and Wu[n + r][k + 8t ..) and
+// x[r][k + 8t ..) (x[r + 8] too when M > 8).  The summation order is free, so
+// K is permuted inside a step: these registers then are the A fragment (rows
+// 0-7 of the MMA: gate, 8-15: up) and the B fragment (x^T) of two m16n8k16
+// MMAs, without shuffles, and a thread ends up with g and u of the same
+// output.  The weights pass through a ring of cp.async copies whose slots a
+// lane fills and reads alone (no barriers): the bytes in flight per SM are
+// the ring's 192 KB, not what registers can hold, and they keep flowing over
+// the ends of passes.  Warps meet in shared memory in a fixed order.
+//
+// gated_gemv_any_kernel: any alignment (rows gathered by smaller loads).
 #pragma once
 
 #include "ffn_elem.cuh"
@@ -23,19 +30,191 @@ struct GatedGemvArgs {
   uint16_t* y[3];  // h, g, u
   long long ldx;
   int M, N, K, act, save;
+  int kw;  // warps that split K
 };
 
-// VEC: x and the weights 16-byte aligned, K and ldx multiples of 8; else
-// elements are gathered at whatever alignment each row has.
-template <int DT, bool VEC>
-__device__ __forceinline__ uint4 gemv_w8(const uint16_t* __restrict__ p, int n) {
-  if constexpr (VEC) return ldg_stream_16(p);
-  else return ffn_load8(p, n);
+constexpr int kGgWarps = 16;
+constexpr int kGgSub = 2;    // groups of 8 columns per pass
+constexpr int kGgSteps = 2;  // steps of 32 along K per ring slot
+constexpr int kGgRing = 3;   // slots
+constexpr int kGgSlot = kGgSteps * kGgSub * 2 * 512;  // bytes of a warp's slot
+constexpr int kGgRingBytes = kGgWarps * kGgRing * kGgSlot;
+__host__ __device__ constexpr int gg_red_floats(int nt) { return kGgWarps * kGgSub * 16 * (8 * nt + 1); }
+__host__ __device__ constexpr int gg_smem_bytes(int nt) { return kGgRingBytes + gg_red_floats(nt) * 4; }
+static_assert(gg_smem_bytes(2) <= 232448, "more shared memory than a CTA can have");
+
+// biases, then one rounding of each result
+template <int DT>
+__device__ __forceinline__ void gg_finish(const GatedGemvArgs& a, float g, float u, int m, int col) {
+  if (a.bias[0] != nullptr) g += ep_widen(__ldg(a.bias[0] + col), DT);
+  if (a.bias[1] != nullptr) u += ep_widen(__ldg(a.bias[1] + col), DT);
+  const size_t at = (size_t)m * a.N + col;
+  if (a.save) {
+    const uint32_t gu = ep_pack_t<DT>(g, u);
+    a.y[1][at] = (uint16_t)gu;
+    a.y[2][at] = (uint16_t)(gu >> 16);
+  }
+  a.y[0][at] = (uint16_t)ep_pack_t<DT>(act_value(a.act, g) * u, 0.0f);
 }
 
 // NT: 8-column blocks of tokens (1: M <= 8, 2: M <= 16)
-template <int NT, int WARPS, int DT, bool VEC>
-__global__ void __launch_bounds__(WARPS * 32) gated_gemv_kernel(const GatedGemvArgs a) {
+template <int NT, int DT>
+__global__ void __launch_bounds__(kGgWarps * 32, 1) gated_gemv_kernel(const GatedGemvArgs a) {
+  constexpr int MT = 8 * NT;
+  extern __shared__ __align__(16) uint8_t gg_smem[];
+  float* red = reinterpret_cast<float*>(gg_smem + kGgRingBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane >> 2, t = lane & 3;
+  const int K = a.K, N = a.N, M = a.M;
+  // this block's columns, this warp's K range (a multiple of a slot's)
+  const int per = N / (int)gridDim.x, extra = N % (int)gridDim.x;
+  const int c_begin = (int)blockIdx.x * per + min((int)blockIdx.x, extra);
+  const int c_end = c_begin + per + ((int)blockIdx.x < extra ? 1 : 0);
+  constexpr int KS = 32 * kGgSteps;
+  // K is split over a.kw warps (as many as have a slot's worth of it, a power
+  // of two); the warps are 16 / kw teams, each with every (16 / kw)-th pass
+  const int kw = a.kw, teams = kGgWarps / kw, team = warp / kw;
+  const int slice = ((K + kw * KS - 1) / (kw * KS)) * KS;
+  const int k_begin = min(K, (warp & (kw - 1)) * slice), k_end = min(K, k_begin + slice);
+  const int kchunks = (k_end - k_begin + KS - 1) / KS;
+  const int passes = (c_end - c_begin + 8 * kGgSub - 1) / (8 * kGgSub);
+  const int rounds = (passes + teams - 1) / teams;
+  const int total = rounds * kchunks;  // (a team's last round may be past the last pass: nothing is loaded)
+  const uint32_t ring = smem_addr(gg_smem) + (uint32_t)(warp * kGgRing * kGgSlot + lane * 16);
+  const bool okx0 = r < M, okx1 = NT > 1 && r + 8 < M;
+  const uint16_t* __restrict__ x0 = a.x + (okx0 ? r : 0) * a.ldx;
+  const uint16_t* __restrict__ x1 = a.x + (okx1 ? r + 8 : 0) * a.ldx;
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // slot layout: vector (step, group, weight) of lane l at ((step * kGgSub + group) * 2 + weight) * 512 + 16 l
+  const ptrdiff_t up = a.wu - a.wg;
+  auto issue = [&](int p, int c, int slot) {
+    const int n0 = c_begin + p * 8 * kGgSub, k0 = k_begin + c * KS;
+    const uint32_t dst = ring + (uint32_t)(slot * kGgSlot);
+    const uint16_t* src = a.wg + (size_t)(n0 + r) * K + (k0 + 8 * t);
+    if (n0 + 8 * kGgSub <= c_end && k0 + KS <= k_end) {
+      // all there: addresses advance by immediates
+#pragma unroll
+      for (int g = 0; g < kGgSub; ++g, src += (size_t)8 * K) {
+        const uint16_t* usrc = src + up;
+        static_assert(kGgSteps == 2, "two steps below");
+        const uint32_t gd = dst + (uint32_t)(g * 1024);
+        cp_async_16_at<0, 0>(gd, src);
+        cp_async_16_at<512, 0>(gd, usrc);
+        cp_async_16_at<kGgSub * 1024, 64>(gd, src);
+        cp_async_16_at<kGgSub * 1024 + 512, 64>(gd, usrc);
+      }
+      return;
+    }
+#pragma unroll
+    for (int s = 0; s < kGgSteps; ++s) {
+#pragma unroll
+      for (int g = 0; g < kGgSub; ++g) {
+        const int n = n0 + 8 * g;
+        if (n < c_end) {  // warp-uniform
+          const bool in = n + r < c_end && k0 + 32 * s + 8 * t < k_end;  // K % 8 == 0: a vector is all in or all out
+          const uint16_t* q = in ? src + (size_t)(8 * g) * K + 32 * s : a.wg;
+          const uint32_t at = dst + (uint32_t)(((s * kGgSub + g) * 2) * 512);
+          cp_async_16(at, q, in ? 16u : 0u);
+          cp_async_16(at + 512, in ? q + up : a.wu, in ? 16u : 0u);
+        }
+      }
+    }
+  };
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  auto load_x = [&](int c, uint4 (&v)[kGgSteps][NT]) {
+#pragma unroll
+    for (int s = 0; s < kGgSteps; ++s) {
+      const int k = k_begin + c * KS + 32 * s + 8 * t;
+      v[s][0] = okx0 && k < k_end ? __ldg(reinterpret_cast<const uint4*>(x0 + k)) : zero;
+      if (NT > 1) v[s][NT - 1] = okx1 && k < k_end ? __ldg(reinterpret_cast<const uint4*>(x1 + k)) : zero;
+    }
+  };
+
+  int ip = team, ic = 0;  // next chunk to issue
+  auto issue_next = [&](int slot) {
+    if (ip < passes && kchunks > 0) {
+      issue(ip, ic, slot);
+      if (++ic == kchunks) { ic = 0; ip += teams; }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kGgRing - 1; ++i) issue_next(i);
+  int slot = 0, fill = kGgRing - 1;
+  uint4 vx[kGgSteps][NT];
+  if (total > 0) load_x(0, vx);
+
+  for (int rd = 0; rd < rounds; ++rd) {
+    const int p = rd * teams + team;
+    float d[kGgSub][NT][4];
+#pragma unroll
+    for (int g = 0; g < kGgSub; ++g)
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[g][q][i] = 0.0f;
+    const int n0 = c_begin + p * 8 * kGgSub;
+    for (int c = 0; c < kchunks; ++c) {
+      issue_next(fill);
+      cp_async_wait_group<kGgRing - 1>();  // this chunk's copies have landed
+      uint4 nx[kGgSteps][NT];
+      load_x(c + 1 == kchunks ? 0 : c + 1, nx);
+      const uint8_t* src = gg_smem + warp * kGgRing * kGgSlot + slot * kGgSlot + lane * 16;
+#pragma unroll
+      for (int s = 0; s < kGgSteps; ++s) {
+#pragma unroll
+        for (int g = 0; g < kGgSub; ++g) {
+          if (n0 + 8 * g < c_end) {
+            const uint4 wg = *reinterpret_cast<const uint4*>(src + ((s * kGgSub + g) * 2) * 512);
+            const uint4 wu = *reinterpret_cast<const uint4*>(src + ((s * kGgSub + g) * 2 + 1) * 512);
+#pragma unroll
+            for (int q = 0; q < NT; ++q) {
+              mma_16816_f32<DT>(d[g][q], wg.x, wu.x, wg.y, wu.y, vx[s][q].x, vx[s][q].y);
+              mma_16816_f32<DT>(d[g][q], wg.z, wu.z, wg.w, wu.w, vx[s][q].z, vx[s][q].w);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < kGgSteps; ++s)
+#pragma unroll
+        for (int q = 0; q < NT; ++q) vx[s][q] = nx[s][q];
+      slot = slot + 1 == kGgRing ? 0 : slot + 1;
+      fill = fill + 1 == kGgRing ? 0 : fill + 1;
+    }
+    // D rows 0-7: gate of column r, rows 8-15: up; columns 2t, 2t + 1: tokens
+    if (rd > 0) __syncthreads();  // the previous round has been read
+#pragma unroll
+    for (int g = 0; g < kGgSub; ++g)
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          red[((warp * kGgSub + g) * 16 + r + (i < 2 ? 0 : 8)) * (MT + 1) + 8 * q + 2 * t + (i & 1)] = d[g][q][i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < teams * 8 * kGgSub * M; o += kGgWarps * 32) {
+      const int n = o & (8 * kGgSub - 1), j = (o / (8 * kGgSub)) & (teams - 1), m = o / (8 * kGgSub * teams);
+      const int col = c_begin + (rd * teams + j) * 8 * kGgSub + n;
+      if (col >= c_end) continue;
+      float g = 0.0f, u = 0.0f;
+#pragma unroll 4
+      for (int w = 0; w < kw; ++w) {
+        const float* e = red + (((j * kw + w) * kGgSub + (n >> 3)) * 16 + (n & 7)) * (MT + 1) + m;
+        g += e[0];
+        u += e[8 * (MT + 1)];
+      }
+      gg_finish<DT>(a, g, u, m, col);
+    }
+  }
+  cp_async_wait_all();
+}
+
+// Any alignment: a block owns 16 columns, its warps split K; a lane gathers
+// the eight elements of a vector by the widest loads its row allows.
+template <int NT, int WARPS, int DT>
+__global__ void __launch_bounds__(WARPS * 32) gated_gemv_any_kernel(const GatedGemvArgs a) {
   constexpr int MT = 8 * NT;
   __shared__ float red[WARPS][2][16][MT + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -67,15 +246,15 @@ __global__ void __launch_bounds__(WARPS * 32) gated_gemv_kernel(const GatedGemvA
 #pragma unroll
     for (int s = 0; s < U; ++s) {
       const int k = k0 + 32 * s + 8 * t;
-      const int n = k_end - k;  // VEC: whole vectors only (K % 8 == 0)
+      const int n = k_end - k;
       const bool in = n > 0;
-      vga[s] = in && okA ? gemv_w8<DT, VEC>(gA + k, n) : zero;
-      vgb[s] = in && okB ? gemv_w8<DT, VEC>(gB + k, n) : zero;
-      vua[s] = in && okA ? gemv_w8<DT, VEC>(uA + k, n) : zero;
-      vub[s] = in && okB ? gemv_w8<DT, VEC>(uB + k, n) : zero;
-      vx[s][0] = in && okx0 ? (VEC ? __ldg(reinterpret_cast<const uint4*>(x0 + k)) : ffn_load8(x0 + k, n)) : zero;
+      vga[s] = in && okA ? ffn_load8(gA + k, n) : zero;
+      vgb[s] = in && okB ? ffn_load8(gB + k, n) : zero;
+      vua[s] = in && okA ? ffn_load8(uA + k, n) : zero;
+      vub[s] = in && okB ? ffn_load8(uB + k, n) : zero;
+      vx[s][0] = in && okx0 ? ffn_load8(x0 + k, n) : zero;
       if (NT > 1)
-        vx[s][NT - 1] = in && okx1 ? (VEC ? __ldg(reinterpret_cast<const uint4*>(x1 + k)) : ffn_load8(x1 + k, n)) : zero;
+        vx[s][NT - 1] = in && okx1 ? ffn_load8(x1 + k, n) : zero;
     }
 #pragma unroll
     for (int s = 0; s < U; ++s) {
@@ -109,15 +288,7 @@ __global__ void __launch_bounds__(WARPS * 32) gated_gemv_kernel(const GatedGemvA
       g += red[w][0][n][m];
       u += red[w][1][n][m];
     }
-    if (a.bias[0] != nullptr) g += ep_widen(__ldg(a.bias[0] + col), DT);
-    if (a.bias[1] != nullptr) u += ep_widen(__ldg(a.bias[1] + col), DT);
-    const size_t at = (size_t)m * N + col;
-    const uint32_t gu = ep_pack_t<DT>(g, u);
-    if (a.save) {
-      a.y[1][at] = (uint16_t)gu;
-      a.y[2][at] = (uint16_t)(gu >> 16);
-    }
-    a.y[0][at] = (uint16_t)ep_pack_t<DT>(act_value(a.act, g) * u, 0.0f);
+    gg_finish<DT>(a, g, u, m, col);
   }
 }
 

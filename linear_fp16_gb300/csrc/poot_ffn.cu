@@ -49,6 +49,12 @@ cudaError_t set_attr() {
                               FfnLayout::DYN_BYTES);
 }
 
+template <int NT, int DT>
+cudaError_t set_gemv_attr() {
+  return cudaFuncSetAttribute(gated_gemv_kernel<NT, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              gg_smem_bytes(NT));
+}
+
 int ffn_device(FfnDevice** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -62,7 +68,9 @@ int ffn_device(FfnDevice** out) {
     if (q == POOT_OK &&
         ((e = set_attr<1, kFfnGated>()) != cudaSuccess || (e = set_attr<2, kFfnGated>()) != cudaSuccess ||
          (e = set_attr<1, kFfnDx>()) != cudaSuccess || (e = set_attr<2, kFfnDx>()) != cudaSuccess ||
-         (e = set_attr<1, kFfnDw>()) != cudaSuccess || (e = set_attr<2, kFfnDw>()) != cudaSuccess))
+         (e = set_attr<1, kFfnDw>()) != cudaSuccess || (e = set_attr<2, kFfnDw>()) != cudaSuccess ||
+         (e = set_gemv_attr<1, kEpiF16>()) != cudaSuccess || (e = set_gemv_attr<1, kEpiBf16>()) != cudaSuccess ||
+         (e = set_gemv_attr<2, kEpiF16>()) != cudaSuccess || (e = set_gemv_attr<2, kEpiBf16>()) != cudaSuccess))
       return cuda_fail(e);
     d.dev = dev;
     d.status = q;
@@ -297,14 +305,20 @@ int finish(WorkspaceLease& lease, int rc) {
 }
 
 // ---- the gated block ------------------------------------------------------------
-template <int NT, int WARPS>
-cudaError_t launch_gated_gemv(const GatedGemvArgs& a, bool bf16, bool vec, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.N, 16))), block(WARPS * 32);
-  if (bf16)
-    return vec ? launch(gated_gemv_kernel<NT, WARPS, kEpiBf16, true>, grid, block, 0, stream, a)
-               : launch(gated_gemv_kernel<NT, WARPS, kEpiBf16, false>, grid, block, 0, stream, a);
-  return vec ? launch(gated_gemv_kernel<NT, WARPS, kEpiF16, true>, grid, block, 0, stream, a)
-             : launch(gated_gemv_kernel<NT, WARPS, kEpiF16, false>, grid, block, 0, stream, a);
+template <int NT>
+cudaError_t launch_gated_gemv(const GatedGemvArgs& a, bool bf16, bool vec, int sms, cudaStream_t stream) {
+  if (vec) {
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(sms, a.N)));
+    return launch(bf16 ? gated_gemv_kernel<NT, kEpiBf16> : gated_gemv_kernel<NT, kEpiF16>, grid, dim3(kGgWarps * 32),
+                  gg_smem_bytes(NT), stream, a);
+  }
+  const int64_t tiles = ceil_div(a.N, 16);
+  const dim3 grid(static_cast<unsigned>(tiles));
+  if (tiles < 2 * int64_t(sms))
+    return launch(bf16 ? gated_gemv_any_kernel<NT, 16, kEpiBf16> : gated_gemv_any_kernel<NT, 16, kEpiF16>, grid,
+                  dim3(16 * 32), 0, stream, a);
+  return launch(bf16 ? gated_gemv_any_kernel<NT, 8, kEpiBf16> : gated_gemv_any_kernel<NT, 8, kEpiF16>, grid,
+                dim3(8 * 32), 0, stream, a);
 }
 
 int gated_gemv(const poot_gated_linear_args& p, int64_t ldx, const FfnDevice& d, cudaStream_t stream) {
@@ -324,14 +338,19 @@ int gated_gemv(const poot_gated_linear_args& p, int64_t ldx, const FfnDevice& d,
   a.K = static_cast<int>(p.K);
   a.act = p.activation;
   a.save = p.g != nullptr;
+  // Warps that split K: never more than there are ring slots of K; and, as
+  // far as the block has a pass for each team, so few that a warp's share of a
+  // pass is four slots (8 x 8192 x 2048 on GB300: 16.3 us with two slots, 14.1
+  // with four)
+  const int64_t passes = ceil_div(ceil_div(p.N, std::min<int64_t>(d.sms, p.N)), 8 * kGgSub);
+  a.kw = kGgWarps;
+  while (a.kw > 1 && (a.kw / 2 * 32 * kGgSteps >= p.K ||
+                      (p.K < a.kw * 128 * kGgSteps && 2 * kGgWarps / a.kw <= passes)))
+    a.kw /= 2;
   const bool bf16 = p.dtype == POOT_DTYPE_BF16;
   const bool vec = p.K % 8 == 0 && ldx % 8 == 0 && aligned(p.x, 16) && aligned(p.wg, 16) && aligned(p.wu, 16);
-  const bool few = ceil_div(p.N, 16) < 2 * int64_t(d.sms);
-  cudaError_t e;
-  if (p.M <= 8)
-    e = few ? launch_gated_gemv<1, 16>(a, bf16, vec, stream) : launch_gated_gemv<1, 8>(a, bf16, vec, stream);
-  else
-    e = few ? launch_gated_gemv<2, 16>(a, bf16, vec, stream) : launch_gated_gemv<2, 8>(a, bf16, vec, stream);
+  const cudaError_t e = p.M <= 8 ? launch_gated_gemv<1>(a, bf16, vec, d.sms, stream)
+                                 : launch_gated_gemv<2>(a, bf16, vec, d.sms, stream);
   return e == cudaSuccess ? POOT_OK : cuda_fail(e);
 }
 
