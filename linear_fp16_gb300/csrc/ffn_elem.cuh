@@ -1,182 +1,140 @@
 // The memory-bound steps around the feed-forward products: the gate's
-// gradient, column sums (bias gradients), the second half of a split-K
-// product, row repacking for operands TMA cannot read in place.
+// gradient, the second half of a split-K product, row repacking for operands
+// TMA cannot read in place.
 #pragma once
 
 #include "ffn_gemm.cuh"
-#include "pack.cuh"
 
 namespace poot {
 
-// Eight consecutive head-dtype elements p[0 .. n) (n <= 8, the rest zero) at
-// any 2-byte alignment.
-__device__ __forceinline__ uint4 ffn_load8(const uint16_t* __restrict__ p, int n) {
-  if (n >= 8) return pack_load8(p);
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
+struct FfnPackArgs {
+  const uint16_t* src[4];
+  uint16_t* dst[4];      // row pitch ldd (a multiple of 8), 16-byte aligned
+  long long ld[4], ldd[4], rows[4];
+  int cols[4];
+  int count;
+};
+
+// Copies up to four matrices into rows of a 16-byte pitch: a warp takes a row,
+// 16 bytes a lane.  The pad columns are written as zeros and never read (the
+// tensor maps end at the matrix's own columns).  Blocks `block` of `blocks`.
+__device__ __forceinline__ void ffn_pack_rows(const FfnPackArgs& a, int block, int blocks) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < n) w[j >> 1] |= (uint32_t)__ldg(p + j) << ((j & 1) * 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  for (int t = 0; t < 4; ++t) {
+    if (t >= a.count) break;
+    for (long long r = (long long)block * 8 + warp; r < a.rows[t]; r += (long long)blocks * 8) {
+      const uint16_t* s = a.src[t] + r * a.ld[t];
+      uint16_t* d = a.dst[t] + r * a.ldd[t];
+#pragma unroll 4
+      for (int c = lane * 8; c < a.cols[t]; c += 256)
+        *reinterpret_cast<uint4*>(d + c) = ffn_load8(s + c, a.cols[t] - c);
+    }
+  }
 }
 
-template <int DT>
-__device__ __forceinline__ void ffn_unpack8(const uint4& v, float (&f)[8]) {
-  const float2 a = ep_unpack_t<DT>(v.x), b = ep_unpack_t<DT>(v.y), c = ep_unpack_t<DT>(v.z), d = ep_unpack_t<DT>(v.w);
-  f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y; f[4] = c.x; f[5] = c.y; f[6] = d.x; f[7] = d.y;
-}
-template <int DT>
-__device__ __forceinline__ uint4 ffn_pack8(const float (&f)[8]) {
-  return make_uint4(ep_pack_t<DT>(f[0], f[1]), ep_pack_t<DT>(f[2], f[3]), ep_pack_t<DT>(f[4], f[5]),
-                    ep_pack_t<DT>(f[6], f[7]));
+__global__ void __launch_bounds__(256) ffn_pack_kernel(const FfnPackArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  ffn_pack_rows(a, blockIdx.x, gridDim.x);
 }
 
-constexpr int kColThreads = 256;
-constexpr int kColWidth = 256;  // columns of a block: 32 lanes x 8
-constexpr int kColRows = 64;    // rows of a block: 8 warps x 8
+constexpr int kGateThreads = 256;
+constexpr int kGateWidth = 256;  // columns of a block: 32 lanes x 8
 
 struct GateGradArgs {
   const uint16_t *dh, *g, *u;
   long long ld_dh, ld_g, ld_u;
   uint16_t *dg, *du;  // row pitch ldo, 16-byte aligned rows
   long long ldo;
-  float* colsum;      // [row blocks][2][N] FP32, or nullptr
+  float* sums;        // [row blocks][2][N] FP32 column sums, or nullptr
   int M, N, act;
+  int rows;           // rows of a block, a multiple of 16
+  int blocks;         // blocks of the gradient; the grid's others repack
+  FfnPackArgs pack;
 };
 
 // dg = dh u act'(g), du = dh act(g), in FP32, each rounded once to the head
 // dtype: they are operands of the tensor core, which takes 16-bit values.
-// The bias gradients sum the unrounded values.  A block covers 64 rows x 256
-// columns, a lane eight columns of eight rows; column sums go through
-// registers, then shared memory, in a fixed order.  Bound by its five
-// streams (three read, two written).
-template <int DT, bool SUMS>
-__global__ void __launch_bounds__(kColThreads) gate_grad_kernel(const GateGradArgs a) {
+// The bias gradients sum the unrounded values: column sums of a block go
+// through registers, then shared memory, in a fixed order.  A lane has eight
+// columns of every eighth row, two rows in flight.  Bound by its five streams
+// (three read, two written).  VEC: rows on 16-byte boundaries.
+template <int DT, bool SUMS, bool VEC>
+__global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const __grid_constant__ GateGradArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  if ((int)blockIdx.x >= a.blocks) {
+    ffn_pack_rows(a.pack, (int)blockIdx.x - a.blocks, (int)gridDim.x - a.blocks);
+    return;
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned cblocks = (a.N + kColWidth - 1) / kColWidth;
+  const unsigned cblocks = (a.N + kGateWidth - 1) / kGateWidth;
   const int cb = blockIdx.x % cblocks, rb = blockIdx.x / cblocks;
-  const int c = cb * kColWidth + lane * 8;
+  const int c = cb * kGateWidth + lane * 8;
   const int n = min(8, a.N - c);  // columns of this lane (<= 0: none)
-  const long long row0 = (long long)rb * kColRows + warp;
+  const long long row_end = min((long long)a.M, ((long long)rb + 1) * a.rows);
   float sg[8], su[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sg[j] = su[j] = 0.0f;
-  grid_dep_wait();
-  grid_dep_launch();
-  if (n > 0) {
-#pragma unroll 2
-    for (int i = 0; i < kColRows / 8; ++i) {
-      const long long row = row0 + i * 8;
-      if (row >= a.M) break;
-      float dh[8], g[8], u[8], dg[8], du[8];
-      ffn_unpack8<DT>(ffn_load8(a.dh + row * a.ld_dh + c, n), dh);
-      ffn_unpack8<DT>(ffn_load8(a.g + row * a.ld_g + c, n), g);
-      ffn_unpack8<DT>(ffn_load8(a.u + row * a.ld_u + c, n), u);
-      auto grad = [&](auto act) {
+  auto load = [&](const uint16_t* p) { return VEC ? ldg_stream_16(p) : ffn_load8(p, n); };
+  auto grad = [&](auto act, const uint4& vh, const uint4& vg, const uint4& vu, long long row) {
+    float dh[8], g[8], u[8], dg[8], du[8];
+    ffn_unpack8<DT>(vh, dh);
+    ffn_unpack8<DT>(vg, g);
+    ffn_unpack8<DT>(vu, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float v, d;
-          act_both_t<decltype(act)::value>(g[j], v, d);
-          dg[j] = dh[j] * u[j] * d;
-          du[j] = dh[j] * v;
-        }
-      };
-      if (a.act == kActSilu) grad(std::integral_constant<int, kActSilu>{});
-      else if (a.act == kActGeluTanh) grad(std::integral_constant<int, kActGeluTanh>{});
-      else grad(std::integral_constant<int, kActGeluErf>{});
+    for (int j = 0; j < 8; ++j) {
+      float v, d;
+      act_both_t<decltype(act)::value>(g[j], v, d);
+      dg[j] = dh[j] * u[j] * d;
+      du[j] = dh[j] * v;
       if constexpr (SUMS) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) { sg[j] += dg[j]; su[j] += du[j]; }
+        sg[j] += dg[j];
+        su[j] += du[j];
       }
-      // whole chunks: the rows' pad columns may be written (never read)
-      *reinterpret_cast<uint4*>(a.dg + row * a.ldo + c) = ffn_pack8<DT>(dg);
-      *reinterpret_cast<uint4*>(a.du + row * a.ldo + c) = ffn_pack8<DT>(du);
     }
+    // whole chunks: the rows' pad columns may be written (never read)
+    *reinterpret_cast<uint4*>(a.dg + row * a.ldo + c) = ffn_pack8<DT>(dg);
+    *reinterpret_cast<uint4*>(a.du + row * a.ldo + c) = ffn_pack8<DT>(du);
+  };
+  auto rows = [&](auto act) {
+    for (long long row = (long long)rb * a.rows + warp; row < row_end; row += 16) {
+      const bool two = row + 8 < row_end;
+      const uint16_t *ph = a.dh + row * a.ld_dh + c, *pg = a.g + row * a.ld_g + c, *pu = a.u + row * a.ld_u + c;
+      const uint4 h0 = load(ph), g0 = load(pg), u0 = load(pu);
+      uint4 h1 = make_uint4(0, 0, 0, 0), g1 = h1, u1 = h1;
+      if (two) {
+        h1 = load(ph + 8 * a.ld_dh);
+        g1 = load(pg + 8 * a.ld_g);
+        u1 = load(pu + 8 * a.ld_u);
+      }
+      grad(act, h0, g0, u0, row);
+      if (two) grad(act, h1, g1, u1, row + 8);
+    }
+  };
+  if (n > 0) {
+    if (a.act == kActSilu) rows(std::integral_constant<int, kActSilu>{});
+    else if (a.act == kActGeluTanh) rows(std::integral_constant<int, kActGeluTanh>{});
+    else rows(std::integral_constant<int, kActGeluErf>{});
   }
   if constexpr (SUMS) {
-    __shared__ float red[8][kColWidth];
+    __shared__ float red[8][kGateWidth];
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < 8; ++j) red[warp][lane * 8 + j] = o ? su[j] : sg[j];
       __syncthreads();
-      const int col = cb * kColWidth + threadIdx.x;
+      const int col = cb * kGateWidth + threadIdx.x;
       if (col < a.N) {
         float s = red[0][threadIdx.x];
 #pragma unroll
         for (int w = 1; w < 8; ++w) s += red[w][threadIdx.x];
-        a.colsum[((size_t)rb * 2 + o) * a.N + col] = s;
+        a.sums[((size_t)rb * 2 + o) * a.N + col] = s;
       }
     }
   }
-}
-
-struct ColSumArgs {
-  const uint16_t* d;
-  long long ld;
-  float* colsum;  // [row blocks][N]
-  int M, N;
-};
-
-// FP32 column sums of D [M, N] over blocks of 64 rows.
-template <int DT>
-__global__ void __launch_bounds__(kColThreads) col_sum_kernel(const ColSumArgs a) {
-  __shared__ float red[8][kColWidth];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned cblocks = (a.N + kColWidth - 1) / kColWidth;
-  const int cb = blockIdx.x % cblocks, rb = blockIdx.x / cblocks;
-  const int c = cb * kColWidth + lane * 8;
-  const int n = min(8, a.N - c);
-  const long long row0 = (long long)rb * kColRows + warp;
-  float s[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) s[j] = 0.0f;
-  grid_dep_wait();
-  grid_dep_launch();
-  if (n > 0) {
-#pragma unroll
-    for (int i = 0; i < kColRows / 8; ++i) {
-      const long long row = row0 + i * 8;
-      if (row < a.M) {
-        float d[8];
-        ffn_unpack8<DT>(ffn_load8(a.d + row * a.ld + c, n), d);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] += d[j];
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) red[warp][lane * 8 + j] = s[j];
-  __syncthreads();
-  const int col = cb * kColWidth + threadIdx.x;
-  if (col < a.N) {
-    float t = red[0][threadIdx.x];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) t += red[w][threadIdx.x];
-    a.colsum[(size_t)rb * a.N + col] = t;
-  }
-}
-
-struct ColFinishArgs {
-  const float* colsum;  // [blocks][outputs][N]
-  uint16_t* out[2];     // either may be nullptr
-  int blocks, outputs, N, dtype;
-};
-
-// Adds the row blocks' sums in order; one rounding to the head dtype.
-__global__ void __launch_bounds__(256) col_finish_kernel(const ColFinishArgs a) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.outputs * a.N) return;
-  const int o = i / a.N, col = i - o * a.N;
-  uint16_t* out = o ? a.out[1] : a.out[0];
-  if (out == nullptr) return;
-  const size_t step = (size_t)a.outputs * a.N;
-  const float* p = a.colsum + i;
-  float s = 0.0f;
-  for (int b = 0; b < a.blocks; ++b) s += __ldg(p + b * step);
-  out[col] = (uint16_t)(ep_pack(s, 0.0f, a.dtype) & 0xffffu);
 }
 
 struct FfnReduceArgs {
@@ -262,33 +220,6 @@ __global__ void __launch_bounds__(256) gated_bias_kernel(const FfnReduceArgs a) 
       a.y[2][i] = (uint16_t)(gu >> 16);
     }
     a.y[0][i] = (uint16_t)ep_pack(act_value(a.act, g) * u, 0.0f, dt);
-  }
-}
-
-struct FfnPackArgs {
-  const uint16_t* src[4];
-  uint16_t* dst[4];      // row pitch ldd (a multiple of 8), 16-byte aligned
-  long long ld[4], ldd[4], rows[4];
-  int cols[4];
-  int count;
-};
-
-// Copies up to four matrices into rows of a 16-byte pitch, 16 bytes a thread;
-// the pad columns are written as zeros and never read (the tensor maps end at
-// the matrix's own columns).
-__global__ void __launch_bounds__(256) ffn_pack_kernel(const FfnPackArgs a) {
-  grid_dep_wait();
-  grid_dep_launch();
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    if (t >= a.count) break;
-    const long long cpr = a.ldd[t] / 8, total = a.rows[t] * cpr;
-    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
-      const long long r = i / cpr;
-      const int c = (int)(i - r * cpr) * 8;
-      const uint4 v = ffn_load8(a.src[t] + r * a.ld[t] + c, a.cols[t] - c);
-      *reinterpret_cast<uint4*>(a.dst[t] + r * a.ldd[t] + c) = v;
-    }
   }
 }
 

@@ -43,9 +43,9 @@ struct FfnDevice {
 std::mutex g_mu;
 FfnDevice g_devices[kMaxDevices];
 
-template <int CL, int KIND>
+template <int CL, bool GATED>
 cudaError_t set_attr() {
-  return cudaFuncSetAttribute(ffn_gemm_kernel<CL, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(ffn_gemm_kernel<CL, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               FfnLayout::DYN_BYTES);
 }
 
@@ -66,9 +66,8 @@ int ffn_device(FfnDevice** out) {
     const int q = device_query(dev, &d.sms);
     if (q == POOT_ERR_CUDA) return q;
     if (q == POOT_OK &&
-        ((e = set_attr<1, kFfnGated>()) != cudaSuccess || (e = set_attr<2, kFfnGated>()) != cudaSuccess ||
-         (e = set_attr<1, kFfnDx>()) != cudaSuccess || (e = set_attr<2, kFfnDx>()) != cudaSuccess ||
-         (e = set_attr<1, kFfnDw>()) != cudaSuccess || (e = set_attr<2, kFfnDw>()) != cudaSuccess ||
+        ((e = set_attr<1, true>()) != cudaSuccess || (e = set_attr<2, true>()) != cudaSuccess ||
+         (e = set_attr<1, false>()) != cudaSuccess || (e = set_attr<2, false>()) != cudaSuccess ||
          (e = set_gemv_attr<1, kEpiF16>()) != cudaSuccess || (e = set_gemv_attr<1, kEpiBf16>()) != cudaSuccess ||
          (e = set_gemv_attr<2, kEpiF16>()) != cudaSuccess || (e = set_gemv_attr<2, kEpiBf16>()) != cudaSuccess))
       return cuda_fail(e);
@@ -150,148 +149,193 @@ struct Packer {
       base += round256(size_t(a.rows[t]) * a.ldd[t] * 2);
     }
   }
+  // blocks that copy eight rows each, a few times over
+  int blocks(int sms) const {
+    int64_t rows = 0;
+    for (int t = 0; t < a.count; ++t) rows = std::max<int64_t>(rows, a.rows[t]);
+    return static_cast<int>(std::min<int64_t>(ceil_div(rows, 8), int64_t(sms) * 6));
+  }
   cudaError_t run(int sms, cudaStream_t stream) const {
     if (a.count == 0) return cudaSuccess;
-    int64_t most = 0;
-    for (int t = 0; t < a.count; ++t) most = std::max<int64_t>(most, a.rows[t] * (a.ldd[t] / 8));
-    return launch(ffn_pack_kernel, dim3(grid_for(most, sms)), dim3(256), 0, stream, a);
+    return launch(ffn_pack_kernel, dim3(static_cast<unsigned>(blocks(sms))), dim3(256), 0, stream, a);
   }
 };
 
 // ---- tile plan -------------------------------------------------------------------
 struct FfnPlan {
-  int cl, bn, split;
+  int cl = 1, bn = 64;
+  int split[2] = {1, 1};
 };
 
-// Cost model: every CTA (pair) runs ceil(tiles / slots) tiles; a 64-element K
-// block of a 128-row tile takes max(2 bn, 128 + bn) cycles of MMA or operand
-// reads, divided by the efficiency of the shape; plus a fixed fill and drain.
-// A split over K adds the second kernel and its bytes.
-FfnPlan plan_ffn(int64_t rows, int64_t cols, int64_t kb, int outputs, bool gated, int sms) {
+// One family of products (see FfnJob) before it is planned.
+struct FfnProduct {
+  bool gated = false, mn_a = false;
+  Operand a[2], b[2];
+  int parts = 1, outputs = 1;
+  int64_t rows = 0, cols = 0, kext = 0;  // of one output; K extent of one part
+  void* y[3] = {nullptr, nullptr, nullptr};
+  int64_t kb() const { return ceil_div(kext, kFfnBK) * parts; }
+  size_t partial_bytes(int split) const {
+    return split > 1 ? round256(size_t(split) * (gated ? 2 : outputs) * rows * cols * 4) : 0;
+  }
+};
+
+// Cost model: a 64-element K block of a 128-row tile takes max(2 bn, 128 + bn)
+// cycles of MMA or operand reads, divided by the efficiency of the shape, plus
+// a fixed fill and drain per tile; the tiles of all products fill the CTA
+// (pair) slots together, the longest tile at least.  A split over K adds the
+// second kernel and its bytes.
+FfnPlan plan_ffn(const FfnProduct* const* ps, int count, int sms) {
   static const struct { int cl, bn, eff; } shapes[] = {{2, 256, 100}, {2, 128, 80}, {1, 256, 85}, {1, 128, 70}, {1, 64, 55}};
-  FfnPlan best = {1, 64, 1};
+  FfnPlan best;
   int64_t best_cost = INT64_MAX;
   for (const auto& s : shapes) {
-    const int64_t width = gated ? s.bn / 2 : s.bn;
-    const int64_t tiles = ceil_div(rows, 128 * s.cl) * ceil_div(cols, width) * outputs;
     const int64_t slots = s.cl == 2 ? sms / 2 : sms;
-    const int64_t per_kb = std::max<int64_t>(2 * s.bn, 128 + s.bn);
-    for (int S = 1; S <= 16; ++S) {
-      if (S > 1 && (kb / S < 8 || tiles * S > 2 * slots)) break;
-      const int64_t waves = ceil_div(tiles * S, slots);
-      int64_t cost = waves * (ceil_div(kb, S) * per_kb * 100 / s.eff + 1500) + (s.cl == 2 ? 1500 : 0);
-      if (S > 1) cost += 6000 + S * rows * cols * outputs * (gated ? 2 : 1) * 4 / 2048;
-      if (cost < best_cost) { best_cost = cost; best = {s.cl, s.bn, S}; }
+    const int64_t per_kb = std::max<int64_t>(2 * s.bn, 128 + s.bn) * 100 / s.eff;
+    FfnPlan p;
+    p.cl = s.cl;
+    p.bn = s.bn;
+    // tiles and their times at a split; the best split of each product alone
+    int64_t work = 0, longest = 0, waves = 0, added = s.cl == 2 ? 1500 : 0;
+    for (int i = 0; i < count; ++i) {
+      const FfnProduct& q = *ps[i];
+      const int64_t tiles = ceil_div(q.rows, 128 * s.cl) * ceil_div(q.cols, q.gated ? s.bn / 2 : s.bn) * q.outputs;
+      const int64_t kb = q.kb();
+      int64_t alone = INT64_MAX, w = 0, l = 0, e = 0, t_of = 0;
+      for (int S = 1; S <= 16; ++S) {
+        if (S > 1 && (kb / S < 8 || tiles * S > 2 * slots)) break;
+        const int64_t t = ceil_div(kb, S) * per_kb + 1500;
+        const int64_t x = S > 1 ? 6000 + S * q.rows * q.cols * q.outputs * (q.gated ? 2 : 1) * 4 / 2048 : 0;
+        const int64_t cost = ceil_div(tiles * S, slots) * t + x;
+        if (cost < alone) {
+          alone = cost;
+          p.split[i] = S;
+          w = tiles * S * t;
+          l = ceil_div(tiles * S, slots) * t;
+          e = x;
+          t_of = t;
+        }
+      }
+      work += w;
+      longest = std::max(longest, t_of);
+      waves = l;
+      added += e;
     }
+    // one product runs in whole waves; two fill each other's gaps
+    const int64_t cost = (count == 1 ? waves : std::max(ceil_div(work, slots) + longest / 2, longest)) + added;
+    if (cost < best_cost) { best_cost = cost; best = p; }
   }
   return best;
 }
 
-struct FfnCall {
-  int kind;
-  Operand a[2], b[2];
-  int parts = 1;    // kFfnDx: products in one sum
-  int outputs = 1;  // kFfnDw: outputs
-  int64_t rows = 0, cols = 0, kext = 0;  // of one output; K extent of one part
-  void* y[3] = {nullptr, nullptr, nullptr};
-  const void* bias[2] = {nullptr, nullptr};
+struct FfnEpilogue {
   int dtype = 0, act = 0, save = 0;
-  FfnPlan plan;
-
-  void make_plan(int sms) {
-    plan = plan_ffn(rows, cols, ceil_div(kext, kFfnBK) * parts, outputs, kind == kFfnGated, sms);
-  }
-  size_t partial_bytes() const {
-    return plan.split > 1 ? size_t(plan.split) * (kind == kFfnGated ? 2 : outputs) * rows * cols * 4 : 0;
-  }
+  const void* bias[2] = {nullptr, nullptr};
 };
 
-template <int CL, int KIND>
-cudaError_t launch_ffn(const FfnMaps& m, const FfnGemmArgs& a, int sms, cudaStream_t stream) {
-  const int64_t units = std::min<int64_t>(a.num_tiles, sms / CL);
-  return launch_clustered(ffn_gemm_kernel<CL, KIND>, dim3(static_cast<unsigned>(units * CL)), dim3(kFfnThreads),
+template <int CL, bool GATED>
+cudaError_t launch_ffn(const FfnMaps& m, const FfnGemmArgs& a, int64_t units, cudaStream_t stream) {
+  return launch_clustered(ffn_gemm_kernel<CL, GATED>, dim3(static_cast<unsigned>(units * CL)), dim3(kFfnThreads),
                           FfnLayout::DYN_BYTES, stream, unsigned(CL), m, a);
 }
 
-int run_ffn_gemm(const FfnCall& c, const FfnDevice& d, float* partial, cudaStream_t stream) {
-  const FfnPlan& p = c.plan;
-  const bool gated = c.kind == kFfnGated, bf16 = c.dtype == POOT_DTYPE_BF16;
-  const bool a_mn = c.kind == kFfnDw, b_mn = !gated;
+// Runs up to two products (dx and dW) in one launch, with the
+// bias gradients `bg` (may be nullptr) beside them, then the second halves of
+// split products.  `partial[i]`: workspace of product i.
+int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const FfnEpilogue& ep,
+                 const FfnBiasGrad* bg, float* const* partial, const FfnDevice& d, cudaStream_t stream) {
+  const bool bf16 = ep.dtype == POOT_DTYPE_BF16;
   FfnGemmArgs a;
-  std::memset(&a, 0, sizeof(a));
-  a.M = static_cast<int>(c.rows);
-  a.N = static_cast<int>(c.cols);
-  a.bn = p.bn;
-  a.cols = gated ? p.bn / 2 : p.bn;
-  a.stages = ffn_stages(p.cl, p.bn);
-  a.num_m_blocks = static_cast<int>(ceil_div(c.rows, kFfnBM * p.cl));
-  a.num_n_blocks = static_cast<int>(ceil_div(c.cols, a.cols));
-  const int64_t bk = kFfnBK * ffn_sub(p.cl);
-  a.kb_part = static_cast<int>(ceil_div(c.kext, bk));
-  if (int64_t(a.kb_part) * c.parts > INT32_MAX) return POOT_ERR_INVALID_ARG;
-  a.kb_total = a.kb_part * c.parts;
-  a.kb_split = static_cast<int>(ceil_div(a.kb_total, p.split));
-  a.split = static_cast<int>(ceil_div(a.kb_total, a.kb_split));  // no empty range
-  // M blocks walked together: their A rows within 32 MB of L2, and at least
-  // eight, about the square of tiles that run at one time
-  int64_t group = (int64_t(32) << 20) / (2 * c.kext * c.parts * kFfnBM * p.cl);
-  group = std::max<int64_t>(8, std::min<int64_t>(group, 64));
-  a.group_m = static_cast<int>(std::min<int64_t>(group, a.num_m_blocks));
-  const int64_t tpg = int64_t(a.num_m_blocks) * a.num_n_blocks;
-  const int64_t tiles = tpg * c.outputs * a.split;
-  if (tiles > INT32_MAX) return POOT_ERR_INVALID_ARG;
-  a.tiles_per_group = static_cast<int>(tpg);
-  a.num_tiles = static_cast<int>(tiles);
-  a.dtype = c.dtype;
-  a.act = c.act;
-  a.save = c.save;
-  a.partial = a.split > 1 ? partial : nullptr;
-  const int ny = gated ? (c.save ? 3 : 1) : c.outputs;
-  a.tma_store = a.split == 1 && c.cols % 8 == 0;
-  for (int i = 0; i < ny; ++i) {
-    a.y[i] = static_cast<uint16_t*>(c.y[i]);
-    if (!aligned(c.y[i], 16)) a.tma_store = 0;
-  }
-  for (int i = 0; i < 2; ++i) a.bias[i] = static_cast<const uint16_t*>(c.bias[i]);
-
   FfnMaps m;
+  std::memset(&a, 0, sizeof(a));
   std::memset(&m, 0, sizeof(m));
-  const int na = c.kind == kFfnDx ? c.parts : (c.kind == kFfnDw ? c.outputs : 1);
-  const int nbm = gated ? 2 : (c.kind == kFfnDx ? c.parts : 1);
-  auto encode = [&](CUtensorMap* map, const Operand& o, bool mn, int rows) {
-    return encode_2d(map, o.p, o.cols, o.rows, kFfnBK, mn ? kFfnBK : static_cast<uint32_t>(rows),
-                     CU_TENSOR_MAP_SWIZZLE_128B, bf16, o.ld);
-  };
-  for (int i = 0; i < na; ++i)
-    if (!encode(&m.a[i], c.a[i], a_mn, kFfnBM)) return cuda_fail(cudaErrorInvalidValue);
-  for (int i = 0; i < nbm; ++i)
-    if (!encode(&m.b[i], c.b[i], b_mn, p.bn / 2)) return cuda_fail(cudaErrorInvalidValue);
-  if (a.tma_store)
-    for (int i = 0; i < ny; ++i)
-      if (!encode_2d(&m.y[i], c.y[i], c.cols, c.rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, bf16))
-        return cuda_fail(cudaErrorInvalidValue);
-  cudaError_t e;
-  const bool pair = p.cl == 2;
-  switch (c.kind) {
-    case kFfnGated: e = pair ? launch_ffn<2, kFfnGated>(m, a, d.sms, stream) : launch_ffn<1, kFfnGated>(m, a, d.sms, stream); break;
-    case kFfnDx: e = pair ? launch_ffn<2, kFfnDx>(m, a, d.sms, stream) : launch_ffn<1, kFfnDx>(m, a, d.sms, stream); break;
-    default: e = pair ? launch_ffn<2, kFfnDw>(m, a, d.sms, stream) : launch_ffn<1, kFfnDw>(m, a, d.sms, stream); break;
+  a.bn = p.bn;
+  a.stages = ffn_stages(p.cl, p.bn);
+  const bool gated = count > 0 && ps[0]->gated;
+  a.cols = gated ? p.bn / 2 : p.bn;
+  a.dtype = ep.dtype;
+  a.act = ep.act;
+  a.save = ep.save;
+  for (int i = 0; i < 2; ++i) a.bias[i] = static_cast<const uint16_t*>(ep.bias[i]);
+  if (bg != nullptr) a.bias_grad = *bg;
+  const int64_t units_max = d.sms / p.cl, bk = kFfnBK * ffn_sub(p.cl);
+  int64_t total = 0;
+  for (int i = 0; i < count; ++i) {
+    const FfnProduct& q = *ps[i];
+    const int ji = q.mn_a ? 1 : 0;
+    FfnJob& j = a.job[ji];
+    j.M = static_cast<int>(q.rows);
+    j.N = static_cast<int>(q.cols);
+    j.parts = q.parts;
+    j.num_m = static_cast<int>(ceil_div(q.rows, kFfnBM * p.cl));
+    j.num_n = static_cast<int>(ceil_div(q.cols, a.cols));
+    const int64_t kb_part = ceil_div(q.kext, bk);
+    if (kb_part * q.parts > INT32_MAX) return POOT_ERR_INVALID_ARG;
+    // (one part: the part index never advances)
+    j.kb_part = q.parts > 1 ? static_cast<int>(kb_part) : INT32_MAX;
+    j.kb_total = static_cast<int>(kb_part * q.parts);
+    j.kb_split = static_cast<int>(ceil_div(j.kb_total, p.split[i]));
+    j.split = static_cast<int>(ceil_div(j.kb_total, j.kb_split));  // no empty range
+    // M blocks walked together: their A rows within 32 MB of L2, and at least
+    // eight, about the square of tiles that run at one time
+    int64_t group = (int64_t(32) << 20) / (2 * q.kext * q.parts * kFfnBM * p.cl);
+    group = std::max<int64_t>(8, std::min<int64_t>(group, 64));
+    j.group_m = static_cast<int>(std::min<int64_t>(group, j.num_m));
+    const int64_t tpo = int64_t(j.num_m) * j.num_n, tiles = tpo * q.outputs * j.split;
+    total += tiles;
+    if (total > INT32_MAX / 4) return POOT_ERR_INVALID_ARG;
+    j.tiles_per_out = static_cast<int>(tpo);
+    j.tiles = static_cast<int>(tiles);
+    j.partial = j.split > 1 ? partial[i] : nullptr;
+    const int ny = q.gated ? (ep.save ? 3 : 1) : q.outputs;
+    j.tma_store = j.split == 1 && q.cols % 8 == 0;
+    for (int o = 0; o < ny; ++o) {
+      j.y[o] = static_cast<uint16_t*>(q.y[o]);
+      if (!aligned(q.y[o], 16)) j.tma_store = 0;
+    }
+    auto encode = [&](CUtensorMap* map, const Operand& o, bool mn, int rows) {
+      return encode_2d(map, o.p, o.cols, o.rows, kFfnBK, mn ? kFfnBK : static_cast<uint32_t>(rows),
+                       CU_TENSOR_MAP_SWIZZLE_128B, bf16, o.ld);
+    };
+    const int na = q.gated ? 1 : (q.mn_a ? q.outputs : q.parts), nb = q.gated ? 2 : (q.mn_a ? 1 : q.parts);
+    bool ok = true;
+    for (int o = 0; o < na; ++o) ok = ok && encode(&m.a[ji][o], q.a[o], q.mn_a, kFfnBM);
+    for (int o = 0; o < nb; ++o) ok = ok && encode(&m.b[ji][o], q.b[o], !q.gated, p.bn / 2);
+    if (j.tma_store)
+      for (int o = 0; o < ny; ++o)
+        ok = ok && encode_2d(&m.y[ji][o], q.y[o], q.cols, q.rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, bf16);
+    if (!ok) return cuda_fail(cudaErrorInvalidValue);
   }
+  for (FfnJob& j : a.job) {
+    if (j.tiles > 0) continue;
+    j.tiles_per_out = 1;
+    j.split = 1;
+  }
+  if (count == 2) a.extra = (2 * a.job[0].kb_split + a.job[1].kb_split) / (2 * a.job[1].kb_split);
+  // without bias gradients no more CTAs than tiles
+  const int64_t units = a.bias_grad.outputs > 0 ? units_max : std::min<int64_t>(total, units_max);
+  const bool pair = p.cl == 2;
+  cudaError_t e;
+  if (gated) e = pair ? launch_ffn<2, true>(m, a, units, stream) : launch_ffn<1, true>(m, a, units, stream);
+  else e = pair ? launch_ffn<2, false>(m, a, units, stream) : launch_ffn<1, false>(m, a, units, stream);
   if (e != cudaSuccess) return cuda_fail(e);
-  if (a.split > 1) {
+  for (int i = 0; i < count; ++i) {
+    const FfnProduct& q = *ps[i];
+    const FfnJob& j = a.job[q.mn_a ? 1 : 0];
+    if (j.split == 1) continue;
     FfnReduceArgs r;
     std::memset(&r, 0, sizeof(r));
-    r.ws = partial;
-    for (int i = 0; i < 3; ++i) r.y[i] = i < ny ? static_cast<uint16_t*>(c.y[i]) : nullptr;
-    for (int i = 0; i < 2; ++i) r.bias[i] = a.bias[i];
-    r.MN = c.rows * c.cols;
-    r.S = a.split;
-    r.N = a.N;
-    r.outputs = c.outputs;
-    r.dtype = c.dtype;
-    r.act = c.act;
-    r.gated = gated;
-    e = launch(ffn_reduce_kernel, dim3(grid_for(r.MN * c.outputs / (c.cols % 4 == 0 ? 4 : 1), d.sms)), dim3(256), 0,
+    r.ws = j.partial;
+    for (int o = 0; o < 3; ++o) r.y[o] = j.y[o];
+    for (int o = 0; o < 2; ++o) r.bias[o] = a.bias[o];
+    r.MN = q.rows * q.cols;
+    r.S = j.split;
+    r.N = j.N;
+    r.outputs = q.outputs;
+    r.dtype = ep.dtype;
+    r.act = ep.act;
+    r.gated = q.gated;
+    e = launch(ffn_reduce_kernel, dim3(grid_for(r.MN * q.outputs / (q.cols % 4 == 0 ? 4 : 1), d.sms)), dim3(256), 0,
                stream, r);
     if (e != cudaSuccess) return cuda_fail(e);
   }
@@ -386,28 +430,30 @@ int gated_linear(const poot_gated_linear_args* ap, cudaStream_t stream) {
     return e == cudaSuccess ? POOT_OK : cuda_fail(e);
   }
   if (M <= POOT_GEMV_MAX_M) return gated_gemv(p, ldx, *d, stream);
-  FfnCall c;
-  c.kind = kFfnGated;
-  c.a[0] = {p.x, M, K, ldx};
-  c.b[0] = {p.wg, N, K, K};
-  c.b[1] = {p.wu, N, K, K};
-  c.rows = M;
-  c.cols = N;
-  c.kext = K;
-  c.y[0] = p.h;
-  c.y[1] = p.g;
-  c.y[2] = p.u;
-  c.bias[0] = p.bg;
-  c.bias[1] = p.bu;
-  c.dtype = p.dtype;
-  c.act = p.activation;
-  c.save = p.g != nullptr;
-  c.make_plan(d->sms);
+  FfnProduct q;
+  q.gated = true;
+  q.a[0] = {p.x, M, K, ldx};
+  q.b[0] = {p.wg, N, K, K};
+  q.b[1] = {p.wu, N, K, K};
+  q.rows = M;
+  q.cols = N;
+  q.kext = K;
+  q.y[0] = p.h;
+  q.y[1] = p.g;
+  q.y[2] = p.u;
+  FfnEpilogue ep;
+  ep.dtype = p.dtype;
+  ep.act = p.activation;
+  ep.save = p.g != nullptr;
+  ep.bias[0] = p.bg;
+  ep.bias[1] = p.bu;
+  const FfnProduct* const ps[1] = {&q};
+  const FfnPlan plan = plan_ffn(ps, 1, d->sms);
   Packer pk;
-  pk.need(&c.a[0]);
-  pk.need(&c.b[0]);
-  pk.need(&c.b[1]);
-  const size_t partial = round256(c.partial_bytes());
+  pk.need(&q.a[0]);
+  pk.need(&q.b[0]);
+  pk.need(&q.b[1]);
+  const size_t partial = q.partial_bytes(plan.split[0]);
   WorkspaceLease lease;
   if (partial + pk.bytes > 0) {
     lease = stream_workspace(d->dev, stream, partial + pk.bytes);
@@ -417,7 +463,8 @@ int gated_linear(const poot_gated_linear_args* ap, cudaStream_t stream) {
   pk.place(ws + partial);
   const cudaError_t e = pk.run(d->sms, stream);
   if (e != cudaSuccess) return finish(lease, cuda_fail(e));
-  return finish(lease, run_ffn_gemm(c, *d, reinterpret_cast<float*>(ws), stream));
+  float* const part[1] = {reinterpret_cast<float*>(ws)};
+  return finish(lease, run_products(ps, 1, plan, ep, nullptr, part, *d, stream));
 }
 
 int zero(void* p, int64_t bytes, cudaStream_t stream) {
@@ -426,84 +473,61 @@ int zero(void* p, int64_t bytes, cudaStream_t stream) {
   return e == cudaSuccess ? POOT_OK : cuda_fail(e);
 }
 
-// The products behind dx and dw: D_q (one or two, TMA-readable) with W_q and x.
+// The products behind dx and dw of D_q (one or two) with W_q and x.
 struct Grads {
-  int count;            // D matrices
-  Operand d[2], w[2], x;
-  void* dx;
-  void* dw[2];
-  int64_t M, N, K;
-  int dtype;
+  FfnProduct dx, dw;
+  const FfnProduct* ps[2];
+  int count = 0;
+  FfnPlan plan;
 
-  FfnCall dx_call, dw_call;
-  int ndw = 0;
-
-  void plan(int sms, Packer* pk) {
-    if (dx != nullptr && K > 0) {
-      FfnCall& c = dx_call;
-      c.kind = kFfnDx;
-      c.parts = count;
-      c.rows = M;
-      c.cols = K;
-      c.kext = N;
-      c.y[0] = dx;
-      c.dtype = dtype;
-      c.make_plan(sms);
-      for (int i = 0; i < count; ++i) pk->need(&w[i]);
+  // d: the D matrices (their addresses may be filled in later, by set_d)
+  void make(int nd, const Operand* d, const Operand* w, const Operand& x, void* dxp, void* const* dwp, int64_t M,
+            int64_t N, int64_t K, int sms, Packer* pk) {
+    if (dxp != nullptr && K > 0) {
+      dx.parts = nd;
+      dx.rows = M;
+      dx.cols = K;
+      dx.kext = N;
+      dx.y[0] = dxp;
+      for (int i = 0; i < nd; ++i) {
+        dx.a[i] = d[i];
+        dx.b[i] = w[i];
+        pk->need(&dx.b[i]);
+      }
+      ps[count++] = &dx;
     }
-    for (int i = 0; i < count; ++i) ndw += dw[i] != nullptr;
-    if (K == 0) ndw = 0;
-    if (ndw > 0) {
-      FfnCall& c = dw_call;
-      c.kind = kFfnDw;
-      c.outputs = ndw;
-      c.rows = N;
-      c.cols = K;
-      c.kext = M;
-      c.dtype = dtype;
-      c.make_plan(sms);
-      pk->need(&x);
+    dw.outputs = 0;
+    if (K > 0)
+      for (int i = 0; i < nd; ++i)
+        if (dwp[i] != nullptr) {
+          dw.a[dw.outputs] = d[i];
+          dw.y[dw.outputs++] = dwp[i];
+        }
+    if (dw.outputs > 0) {
+      dw.mn_a = true;
+      dw.rows = N;
+      dw.cols = K;
+      dw.kext = M;
+      dw.b[0] = x;
+      pk->need(&dw.b[0]);
+      ps[count++] = &dw;
     }
+    plan = plan_ffn(ps, count, sms);
   }
   size_t partial_bytes() const {
-    return round256(std::max(dx != nullptr && K > 0 ? dx_call.partial_bytes() : 0, ndw > 0 ? dw_call.partial_bytes() : 0));
+    size_t b = 0;
+    for (int i = 0; i < count; ++i) b += ps[i]->partial_bytes(plan.split[i]);
+    return b;
   }
-  int run(const FfnDevice& dev, float* partial, cudaStream_t stream) {
-    if (dx != nullptr && K > 0) {
-      for (int i = 0; i < count; ++i) {
-        dx_call.a[i] = d[i];
-        dx_call.b[i] = w[i];
-      }
-      const int rc = run_ffn_gemm(dx_call, dev, partial, stream);
-      if (rc != POOT_OK) return rc;
+  int run(const FfnEpilogue& ep, const FfnBiasGrad* bg, char* ws, const FfnDevice& dev, cudaStream_t stream) const {
+    float* part[2] = {nullptr, nullptr};
+    for (int i = 0; i < count; ++i) {
+      part[i] = reinterpret_cast<float*>(ws);
+      ws += ps[i]->partial_bytes(plan.split[i]);
     }
-    if (ndw > 0) {
-      int o = 0;
-      for (int i = 0; i < count; ++i) {
-        if (dw[i] == nullptr) continue;
-        dw_call.a[o] = d[i];
-        dw_call.y[o] = dw[i];
-        ++o;
-      }
-      dw_call.b[0] = x;
-      return run_ffn_gemm(dw_call, dev, partial, stream);
-    }
-    return POOT_OK;
+    return run_products(ps, count, plan, ep, bg, part, dev, stream);
   }
 };
-
-cudaError_t finish_columns(const float* colsum, int64_t blocks, int outputs, int64_t N, int dtype, void* o0, void* o1,
-                           cudaStream_t stream) {
-  ColFinishArgs f;
-  f.colsum = colsum;
-  f.out[0] = static_cast<uint16_t*>(o0);
-  f.out[1] = static_cast<uint16_t*>(o1);
-  f.blocks = static_cast<int>(blocks);
-  f.outputs = outputs;
-  f.N = static_cast<int>(N);
-  f.dtype = dtype;
-  return launch(col_finish_kernel, dim3(static_cast<unsigned>(ceil_div(outputs * N, 256))), dim3(256), 0, stream, f);
-}
 
 int gated_linear_backward(const poot_gated_linear_backward_args* ap, cudaStream_t stream) {
   if (ap == nullptr) return POOT_ERR_INVALID_ARG;
@@ -541,57 +565,72 @@ int gated_linear_backward(const poot_gated_linear_backward_args* ap, cudaStream_
       if (z == POOT_OK) z = zero(const_cast<void*>(s.p), s.bytes, stream);
     return z;
   }
-  Grads g;
-  g.count = 2;
-  g.w[0] = {p.wg, N, K, K};
-  g.w[1] = {p.wu, N, K, K};
-  g.x = {p.x, M, K, ldx};
-  g.dx = p.dx;
-  g.dw[0] = p.dwg;
-  g.dw[1] = p.dwu;
-  g.M = M;
-  g.N = N;
-  g.K = K;
-  g.dtype = p.dtype;
+  // Rows of a block of the gate's gradient: 64, less while the blocks are
+  // fewer than four per SM
+  int rows = 64;
+  while (rows > 16 && ceil_div(M, rows) * ceil_div(N, kGateWidth) < 4 * int64_t(d->sms)) rows /= 2;
+  const int64_t Np = ceil8(N), row_blocks = ceil_div(M, rows), gate_blocks = row_blocks * ceil_div(N, kGateWidth);
+  if (gate_blocks > INT32_MAX / 2) return POOT_ERR_INVALID_ARG;
   Packer pk;
-  g.plan(d->sms, &pk);
-  const int64_t Np = ceil8(N), row_blocks = ceil_div(M, kColRows);
-  if (ceil_div(N, kColWidth) * row_blocks > INT32_MAX) return POOT_ERR_INVALID_ARG;
+  Grads g;
+  const Operand dmat[2] = {{nullptr, M, N, Np}, {nullptr, M, N, Np}}, w[2] = {{p.wg, N, K, K}, {p.wu, N, K, K}};
+  void* const dwp[2] = {p.dwg, p.dwu};
+  g.make(2, dmat, w, {p.x, M, K, ldx}, p.dx, dwp, M, N, K, d->sms, &pk);
   const size_t dbytes = round256(size_t(M) * Np * 2), partial = g.partial_bytes();
-  const size_t cbytes = want_db ? round256(size_t(row_blocks) * 2 * N * 4) : 0;
-  WorkspaceLease lease = stream_workspace(d->dev, stream, 2 * dbytes + partial + cbytes + pk.bytes);
+  const size_t sbytes = want_db ? round256(size_t(row_blocks) * 2 * N * 4) : 0;
+  WorkspaceLease lease = stream_workspace(d->dev, stream, 2 * dbytes + partial + sbytes + pk.bytes);
   if (lease.ptr == nullptr) return cuda_fail(cudaErrorMemoryAllocation);
-  char* ws = static_cast<char*>(lease.ptr);
-  g.d[0] = {ws, M, N, Np};
-  g.d[1] = {ws + dbytes, M, N, Np};
-  float* const part = reinterpret_cast<float*>(ws + 2 * dbytes);
-  float* const colsum = reinterpret_cast<float*>(ws + 2 * dbytes + partial);
-  pk.place(ws + 2 * dbytes + partial + cbytes);
-  cudaError_t e = pk.run(d->sms, stream);
-  if (e != cudaSuccess) return finish(lease, cuda_fail(e));
+  char* const ws = static_cast<char*>(lease.ptr);
+  char* const dgp = ws;
+  char* const dup = ws + dbytes;
+  float* const sums = reinterpret_cast<float*>(ws + 2 * dbytes + partial);
+  pk.place(ws + 2 * dbytes + partial + sbytes);
+  g.dx.a[0].p = dgp;
+  g.dx.a[1].p = dup;
+  for (int i = 0; i < g.dw.outputs; ++i) g.dw.a[i].p = g.dw.y[i] == p.dwg ? dgp : dup;
   GateGradArgs ga;
+  std::memset(&ga, 0, sizeof(ga));
   ga.dh = static_cast<const uint16_t*>(p.dh);
   ga.g = static_cast<const uint16_t*>(p.g);
   ga.u = static_cast<const uint16_t*>(p.u);
   ga.ld_dh = ld_dh;
   ga.ld_g = ld_g;
   ga.ld_u = ld_u;
-  ga.dg = reinterpret_cast<uint16_t*>(ws);
-  ga.du = reinterpret_cast<uint16_t*>(ws + dbytes);
+  ga.dg = reinterpret_cast<uint16_t*>(dgp);
+  ga.du = reinterpret_cast<uint16_t*>(dup);
   ga.ldo = Np;
-  ga.colsum = want_db ? colsum : nullptr;
+  ga.sums = want_db ? sums : nullptr;
   ga.M = static_cast<int>(M);
   ga.N = static_cast<int>(N);
   ga.act = p.activation;
-  const dim3 grid(static_cast<unsigned>(ceil_div(N, kColWidth) * row_blocks));
-  const bool bf16 = p.dtype == POOT_DTYPE_BF16;
-  auto kern = bf16 ? (want_db ? gate_grad_kernel<kEpiBf16, true> : gate_grad_kernel<kEpiBf16, false>)
-                   : (want_db ? gate_grad_kernel<kEpiF16, true> : gate_grad_kernel<kEpiF16, false>);
-  e = launch(kern, grid, dim3(kColThreads), 0, stream, ga);
-  if (e == cudaSuccess && want_db)
-    e = finish_columns(colsum, row_blocks, 2, N, p.dtype, p.dbg, p.dbu, stream);
+  ga.rows = rows;
+  ga.blocks = static_cast<int>(gate_blocks);
+  ga.pack = pk.a;
+  const dim3 grid(static_cast<unsigned>(gate_blocks + pk.blocks(d->sms)));
+  const bool vec = N % 8 == 0 && ld_dh % 8 == 0 && ld_g % 8 == 0 && ld_u % 8 == 0 && aligned(p.dh, 16) &&
+                   aligned(p.g, 16) && aligned(p.u, 16);
+  auto pick = [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    return want_db ? (vec ? gate_grad_kernel<DT, true, true> : gate_grad_kernel<DT, true, false>)
+                   : (vec ? gate_grad_kernel<DT, false, true> : gate_grad_kernel<DT, false, false>);
+  };
+  auto kern = p.dtype == POOT_DTYPE_BF16 ? pick(std::integral_constant<int, kEpiBf16>{})
+                                         : pick(std::integral_constant<int, kEpiF16>{});
+  const cudaError_t e = launch(kern, grid, dim3(kGateThreads), 0, stream, ga);
   if (e != cudaSuccess) return finish(lease, cuda_fail(e));
-  return finish(lease, g.run(*d, part, stream));
+  FfnEpilogue ep;
+  ep.dtype = p.dtype;
+  FfnBiasGrad bg;
+  std::memset(&bg, 0, sizeof(bg));
+  if (want_db) {
+    bg.sums = sums;
+    bg.rows = row_blocks;
+    bg.outputs = 2;
+    bg.N = static_cast<int>(N);
+    bg.out[0] = static_cast<uint16_t*>(p.dbg);
+    bg.out[1] = static_cast<uint16_t*>(p.dbu);
+  }
+  return finish(lease, g.run(ep, &bg, ws + 2 * dbytes, *d, stream));
 }
 
 int linear_backward(const poot_linear_backward_args* ap, cudaStream_t stream) {
@@ -618,47 +657,37 @@ int linear_backward(const poot_linear_backward_args* ap, cudaStream_t stream) {
     if (z == POOT_OK) z = zero(p.dw, wb, stream);
     return z == POOT_OK ? zero(p.db, 2 * N, stream) : z;
   }
-  Grads g;
-  g.count = 1;
-  g.d[0] = {p.dy, M, N, ld_dy};
-  g.w[0] = {p.w, N, K, K};
-  g.x = {p.x, M, K, ldx};
-  g.dx = p.dx;
-  g.dw[0] = p.dw;
-  g.dw[1] = nullptr;
-  g.M = M;
-  g.N = N;
-  g.K = K;
-  g.dtype = p.dtype;
   Packer pk;
-  g.plan(d->sms, &pk);
-  if (K > 0 && (p.dx != nullptr || p.dw != nullptr)) pk.need(&g.d[0]);
-  const int64_t row_blocks = ceil_div(M, kColRows);
-  if (ceil_div(N, kColWidth) * row_blocks > INT32_MAX) return POOT_ERR_INVALID_ARG;
+  Operand dy = {p.dy, M, N, ld_dy};
+  Grads g;
+  const Operand w = {p.w, N, K, K};
+  g.make(1, &dy, &w, {p.x, M, K, ldx}, p.dx, &p.dw, M, N, K, d->sms, &pk);
+  if (g.count > 0) pk.need(&dy);
   const size_t partial = g.partial_bytes();
-  const size_t cbytes = p.db != nullptr ? round256(size_t(row_blocks) * N * 4) : 0;
   WorkspaceLease lease;
-  if (partial + cbytes + pk.bytes > 0) {
-    lease = stream_workspace(d->dev, stream, partial + cbytes + pk.bytes);
+  if (partial + pk.bytes > 0) {
+    lease = stream_workspace(d->dev, stream, partial + pk.bytes);
     if (lease.ptr == nullptr) return cuda_fail(cudaErrorMemoryAllocation);
   }
-  char* ws = static_cast<char*>(lease.ptr);
-  pk.place(ws + partial + cbytes);
-  cudaError_t e = pk.run(d->sms, stream);
-  if (e == cudaSuccess && p.db != nullptr) {
-    ColSumArgs ca;
-    ca.d = static_cast<const uint16_t*>(p.dy);
-    ca.ld = ld_dy;
-    ca.colsum = reinterpret_cast<float*>(ws + partial);
-    ca.M = static_cast<int>(M);
-    ca.N = static_cast<int>(N);
-    const dim3 grid(static_cast<unsigned>(ceil_div(N, kColWidth) * row_blocks));
-    e = launch(p.dtype == POOT_DTYPE_BF16 ? col_sum_kernel<kEpiBf16> : col_sum_kernel<kEpiF16>, grid, dim3(kColThreads),
-               0, stream, ca);
-    if (e == cudaSuccess) e = finish_columns(ca.colsum, row_blocks, 1, N, p.dtype, p.db, nullptr, stream);
-  }
+  char* const ws = static_cast<char*>(lease.ptr);
+  pk.place(ws + partial);
+  g.dx.a[0] = g.dw.a[0] = dy;
+  const cudaError_t e = pk.run(d->sms, stream);
   if (e != cudaSuccess) return finish(lease, cuda_fail(e));
-  return finish(lease, g.run(*d, reinterpret_cast<float*>(ws), stream));
+  FfnEpilogue ep;
+  ep.dtype = p.dtype;
+  FfnBiasGrad bg;
+  std::memset(&bg, 0, sizeof(bg));
+  if (p.db != nullptr) {
+    bg.d = static_cast<const uint16_t*>(p.dy);
+    bg.ld = ld_dy;
+    bg.rows = M;
+    bg.outputs = 1;
+    bg.N = static_cast<int>(N);
+    bg.out[0] = static_cast<uint16_t*>(p.db);
+  }
+  if (g.count == 0 && p.db == nullptr) return finish(lease, POOT_OK);
+  return finish(lease, g.run(ep, &bg, ws, *d, stream));
 }
 
 // ---- clipping ----------------------------------------------------------------------
