@@ -131,9 +131,8 @@ typedef struct poot_grad_tensor {
  *   scale = min(1, max_norm / (norm + 1e-6))
  *   dst   = RN(src * scale), in the tensor's dtype
  * norm: device pointer to one float, written on `stream` (the call does not
- * synchronise).  Squares are summed in FP32 over at most 64 elements and in
- * FP64 beyond (in FP64 throughout where FP32 squares would overflow or
- * vanish).  A norm that is NaN makes every result NaN; an infinite norm gives
+ * synchronise).  Squares are summed in FP32 over at most 33 elements and in
+ * FP64 beyond (scaled first where FP32 squares would overflow or vanish).  A norm that is NaN makes every result NaN; an infinite norm gives
  * scale 0.  Tensors may be empty, of mixed dtypes and at any alignment of
  * their elements; count == 0 writes norm = 0.
  * A dst must be its own src or overlap no src and no other dst.

@@ -39,6 +39,7 @@ struct FfnDevice {
   int status = POOT_OK;
   int dev = 0;
   int sms = 0;
+  int clip_blocks = 0;  // blocks of the cooperative clip that run at one time
 };
 std::mutex g_mu;
 FfnDevice g_devices[kMaxDevices];
@@ -71,6 +72,16 @@ int ffn_device(FfnDevice** out) {
          (e = set_gemv_attr<1, kEpiF16>()) != cudaSuccess || (e = set_gemv_attr<1, kEpiBf16>()) != cudaSuccess ||
          (e = set_gemv_attr<2, kEpiF16>()) != cudaSuccess || (e = set_gemv_attr<2, kEpiBf16>()) != cudaSuccess))
       return cuda_fail(e);
+    if (q == POOT_OK) {
+      int few = 0, many = 0;
+      if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&few, clip_kernel<kClipTableFew, kClipBoth>, kClipThreads,
+                                                             0)) != cudaSuccess ||
+          (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&many, clip_kernel<kClipTable, kClipBoth>, kClipThreads,
+                                                             0)) != cudaSuccess)
+        return cuda_fail(e);
+      d.clip_blocks = std::min(std::min(few, many), kClipBlocksPerSm) * d.sms;
+      if (d.clip_blocks == 0) return cuda_fail(cudaErrorCooperativeLaunchTooLarge);
+    }
     d.dev = dev;
     d.status = q;
     d.ready = true;
@@ -691,6 +702,46 @@ int linear_backward(const poot_linear_backward_args* ap, cudaStream_t stream) {
 }
 
 // ---- clipping ----------------------------------------------------------------------
+// The table of `count` tensors; returns the launch's blocks.
+template <int T>
+int fill_clip(ClipTable<T>* table, const poot_grad_tensor* t, int64_t count, int max_blocks) {
+  int n = 0;
+  table->first[0] = 0;
+  for (int64_t k = 0; k < count; ++k) {
+    const poot_grad_tensor& g = t[k];
+    if (g.n == 0) continue;
+    table->src[n] = g.src;
+    table->dst[n] = g.dst;
+    table->n[n] = g.n;
+    table->dtype[n] = static_cast<unsigned char>(g.dtype);
+    table->first[n + 1] =
+        table->first[n] + static_cast<int>(ceil_div(g.n, kClipPieceBytes / (g.dtype == POOT_GRAD_F32 ? 4 : 2)));
+    ++n;
+  }
+  table->count = n;
+  return std::max(1, std::min(table->first[n], max_blocks));
+}
+
+template <int T>
+int clip_fused(const poot_grad_tensor* t, int64_t count, ClipArgs a, int max_blocks, cudaStream_t stream) {
+  ClipTable<T> table;
+  const int blocks = fill_clip(&table, t, count, max_blocks);
+  a.parts = blocks;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kClipThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  std::memset(&attr, 0, sizeof(attr));
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, clip_kernel<T, kClipBoth>, table, a);
+  return e == cudaSuccess ? POOT_OK : cuda_fail(e);
+}
+
 int clip_grad_norm(const poot_grad_tensor* t, int64_t count, float max_norm, float* norm, cudaStream_t stream) {
   if (count < 0 || count > kMaxDim || norm == nullptr || (count > 0 && t == nullptr) || !(max_norm >= 0.0f))
     return POOT_ERR_INVALID_ARG;
@@ -729,7 +780,7 @@ int clip_grad_norm(const poot_grad_tensor* t, int64_t count, float max_norm, flo
   FfnDevice* d;
   const int st = ffn_device(&d);
   if (st != POOT_OK) return st;
-  const int max_blocks = d->sms * 4;
+  const int max_blocks = d->clip_blocks;
   const int64_t launches = std::max<int64_t>(1, ceil_div(count, kClipTable));
   WorkspaceLease lease = stream_workspace(d->dev, stream, size_t(launches) * max_blocks * sizeof(double));
   if (lease.ptr == nullptr) return cuda_fail(cudaErrorMemoryAllocation);
@@ -737,47 +788,23 @@ int clip_grad_norm(const poot_grad_tensor* t, int64_t count, float max_norm, flo
   a.partial = static_cast<double*>(lease.ptr);
   a.max_norm = max_norm;
   a.norm = norm;
-  a.write_norm = 0;
+  a.write_norm = 1;
   a.part0 = 0;
   a.parts = 0;
-  ClipTable table;
-  auto fill = [&](int64_t first) {
-    int64_t k = first;
-    table.count = 0;
-    table.first[0] = 0;
-    for (; k < count && table.count < kClipTable; ++k) {
-      const poot_grad_tensor& g = t[k];
-      if (g.n == 0) continue;
-      const int i = table.count++;
-      table.src[i] = g.src;
-      table.dst[i] = g.dst;
-      table.n[i] = g.n;
-      table.dtype[i] = static_cast<unsigned char>(g.dtype);
-      table.first[i + 1] =
-          table.first[i] + static_cast<int>(ceil_div(g.n, kClipPieceBytes / (g.dtype == POOT_GRAD_F32 ? 4 : 2)));
-    }
-    return k;
-  };
-  auto blocks_for = [&]() {
-    return static_cast<unsigned>(std::max(1, std::min(table.first[table.count], max_blocks)));
-  };
+  if (count <= kClipTableFew) return finish(lease, clip_fused<kClipTableFew>(t, count, a, max_blocks, stream));
+  if (count <= kClipTable) return finish(lease, clip_fused<kClipTable>(t, count, a, max_blocks, stream));
+  ClipTable<kClipTable> table;
   cudaError_t e = cudaSuccess;
-  bool more = true;
-  for (int64_t k = 0; more && e == cudaSuccess;) {
-    k = fill(k);
-    more = k < count;
-    const unsigned blocks = blocks_for();
+  for (int64_t k = 0; k < count && e == cudaSuccess; k += kClipTable) {
+    const int blocks = fill_clip(&table, t + k, std::min<int64_t>(kClipTable, count - k), max_blocks);
     a.part0 = a.parts;
-    e = launch(clip_sum_kernel, dim3(blocks), dim3(kClipThreads), 0, stream, table, a);
-    a.parts += static_cast<int>(blocks);
+    e = launch(clip_kernel<kClipTable, kClipSum>, dim3(blocks), dim3(kClipThreads), 0, stream, table, a);
+    a.parts += blocks;
   }
-  more = true;
-  for (int64_t k = 0; more && e == cudaSuccess;) {
-    const bool single = count <= kClipTable;  // the table still holds the one launch's tensors
+  for (int64_t k = 0; k < count && e == cudaSuccess; k += kClipTable) {
+    const int blocks = fill_clip(&table, t + k, std::min<int64_t>(kClipTable, count - k), max_blocks);
     a.write_norm = k == 0;
-    k = single ? count : fill(k);
-    more = k < count;
-    e = launch(clip_scale_kernel, dim3(blocks_for()), dim3(kClipThreads), 0, stream, table, a);
+    e = launch(clip_kernel<kClipTable, kClipScale>, dim3(blocks), dim3(kClipThreads), 0, stream, table, a);
   }
   return finish(lease, e == cudaSuccess ? POOT_OK : cuda_fail(e));
 }

@@ -213,10 +213,12 @@ def _stream(device, stream):
 def _empty(like, shape, other, dtype=None):
     """An output of the call: from its stream's memory, and kept from reuse
     while the caller's current stream may still read it."""
+    if dtype is None:
+        dtype = like.dtype
     if other is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(other):
-        t = like.new_empty(shape, dtype=dtype)
+        t = torch.empty(shape, dtype=dtype, device=like.device)
     t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
@@ -316,7 +318,8 @@ def _refuse_grad(g, d, i, device):
             raise TypeError(f"{name}[{i}] must be a float16, bfloat16 or float32 tensor")
         if t.get_device() != device or not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor on the device of the first")
-    raise ValueError(f"out[{i}] must have the shape and dtype of grads[{i}]")
+    if d.dtype != g.dtype or d.shape != g.shape:
+        raise ValueError(f"out[{i}] must have the shape and dtype of grads[{i}]")
 
 
 def clip_grad_norm(grads, max_norm: float, *, out=None, stream=None):
@@ -334,18 +337,30 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, stream=None):
         raise ValueError("grads must hold at least one tensor")
     if len(dsts) != len(grads):
         raise ValueError(f"out must hold {len(grads)} tensors, got {len(dsts)}")
-    first = grads[0]
-    device = first.get_device() if isinstance(first, torch.Tensor) and first.is_cuda else -1
-    pack, codes, rows = _PACK_GRAD.pack, _GRAD_CODES, []
-    for i, (g, d) in enumerate(zip(grads, dsts)):
-        if not (device >= 0 and isinstance(g, torch.Tensor) and g.dtype in codes and g.get_device() == device
-                and g.is_contiguous()):
+    # one pass per property over the whole list, in the interpreter's own loops
+    T = torch.Tensor
+    n = len(grads)
+    try:
+        dtypes, shapes = [g.dtype for g in grads], [g.shape for g in grads]
+        devices = list(map(T.get_device, grads))
+        codes = [_GRAD_CODES[t] for t in dtypes]
+        src, sizes = list(map(T.data_ptr, grads)), map(T.numel, grads)
+        ok = devices[0] >= 0 and devices.count(devices[0]) == n and all(map(T.is_contiguous, grads))
+        dst = src
+        if ok and out is not None:
+            dst = list(map(T.data_ptr, dsts))
+            ok = (shapes == [d.shape for d in dsts] and dtypes == [d.dtype for d in dsts]
+                  and devices == list(map(T.get_device, dsts)) and all(map(T.is_contiguous, dsts)))
+    except (TypeError, AttributeError, KeyError, RuntimeError):
+        ok = False
+    if not ok:
+        device = grads[0].get_device() if isinstance(grads[0], T) else -1
+        for i, (g, d) in enumerate(zip(grads, dsts)):
             _refuse_grad(g, d, i, device)
-        if d is not g and not (isinstance(d, torch.Tensor) and d.dtype is g.dtype and d.get_device() == device
-                               and d.shape == g.shape and d.is_contiguous()):
-            _refuse_grad(g, d, i, device)
-        rows.append(pack(g.data_ptr(), d.data_ptr(), g.numel(), codes[g.dtype]))
+    device = devices[0]
+    table = b"".join(map(_PACK_GRAD.pack, src, dst, sizes, codes))
     handle, other = _stream(device, stream)
+    first = grads[0]
     norm = _empty(first, (), other, torch.float32)
-    _call("poot_clip_grad_norm", device, b"".join(rows), len(grads), max_norm, norm.data_ptr(), handle)
+    _call("poot_clip_grad_norm", device, table, n, max_norm, norm.data_ptr(), handle)
     return norm
