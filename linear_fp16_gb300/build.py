@@ -1,7 +1,8 @@
-"""Build the CUDA library libpoot_linear.so (sm_103a) in-tree with nvcc.
+"""Build the CUDA library libpoot_linear.so (sm_103a) in-tree with nvcc, and
+the extension that calls it on torch tensors.
 
 Usage: python -m linear_fp16_gb300.build [--verbose]
-The library lands in linear_fp16_gb300/_build/ (git-ignored).
+Both land in linear_fp16_gb300/_build/ (git-ignored).
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -24,6 +26,9 @@ DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in (
     "mma.cuh", "ffn_gemm.cuh", "ffn_gemv.cuh", "ffn_elem.cuh", "clip.cuh")] + [
     os.path.join(INCLUDE, f) for f in ("poot_linear.h", "poot_ffn.h")]
 
+EXT_SOURCE = os.path.join(CSRC, "ffn_torch.cpp")
+EXT_DEPENDS = [EXT_SOURCE] + [os.path.join(INCLUDE, f) for f in ("poot_linear.h", "poot_ffn.h")]
+
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr"]
@@ -36,11 +41,20 @@ def nvcc() -> str:
     return cand
 
 
+def extension() -> str:
+    """Path of the tensor-level extension, built for this torch and interpreter."""
+    import torch
+    return os.path.join(BUILD, f"_ffn_torch.{sys.implementation.cache_tag}.{torch.__version__}.so")
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in DEPENDS)
+    for target, deps in ((LIB, DEPENDS), (extension(), EXT_DEPENDS)):
+        if not os.path.exists(target):
+            return False
+        t = os.path.getmtime(target)
+        if any(os.path.getmtime(p) > t for p in deps):
+            return False
+    return True
 
 
 def _run(cmd, verbose: bool) -> None:
@@ -57,23 +71,33 @@ def _run(cmd, verbose: bool) -> None:
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
+    import torch
     os.makedirs(BUILD, exist_ok=True)
     tag = f".tmp{os.getpid()}"
-    objs = [os.path.join(BUILD, os.path.basename(src) + tag + ".o") for src in SOURCES]
-    tmp = LIB + tag
+    objs = [os.path.join(BUILD, os.path.basename(src) + tag + ".o") for src in SOURCES + [EXT_SOURCE]]
+    lib, ext = LIB + tag, extension() + tag
+    tdir = os.path.dirname(torch.__file__)
+    includes = [INCLUDE, os.path.join(tdir, "include"), os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"],
+                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")]
     compiles = [[nvcc(), *ARCH, *FLAGS, "-Xptxas=-v", "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", o]
                 for src, o in zip(SOURCES, objs)]
-    link = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp]
+    compiles.append(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *[f"-I{p}" for p in includes], "-c",
+                     EXT_SOURCE, "-o", objs[-1]])
     try:
-        # the translation units side by side, then the link
+        # the translation units side by side, then the links
         with ThreadPoolExecutor(len(compiles)) as pool:
             list(pool.map(lambda cmd: _run(cmd, verbose), compiles))
-        _run(link, verbose)
+        _run([nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs[:-1], "-o", lib], verbose)
+        os.replace(lib, LIB)
+        # (the loader finds the library beside the extension; torch is loaded already)
+        _run(["g++", "-shared", objs[-1], "-L" + BUILD, "-l:" + os.path.basename(LIB), "-L" + os.path.join(tdir, "lib"),
+              "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-o", ext], verbose)
+        os.replace(ext, extension())
     finally:
         for o in objs:
             if os.path.exists(o):
                 os.remove(o)
-    os.replace(tmp, LIB)
     return LIB
 
 
