@@ -7,7 +7,8 @@
  * device, sizes in elements, status codes, work queued on `stream` without
  * synchronising; argument errors are found before any CUDA call and leave
  * everything untouched.  Matrices are row-major; a leading dimension (`ld*`,
- * elements between rows) of 0 means contiguous rows.  Weights are
+ * elements between rows) of 0 means contiguous rows.  Where ld is larger, the
+ * memory between two rows of an input may be read (never used).  Weights are
  * [out_features, in_features] and contiguous, read in place.
  *
  * Numerics: unlike poot_contract, whose steps round one by one, these

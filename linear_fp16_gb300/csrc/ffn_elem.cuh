@@ -10,26 +10,48 @@ namespace poot {
 struct FfnPackArgs {
   const uint16_t* src[4];
   uint16_t* dst[4];      // row pitch ldd (a multiple of 8), 16-byte aligned
-  long long ld[4], ldd[4], rows[4];
-  int cols[4];
+  long long ld[4], ldd[4];
+  int rows[4], cols[4];
   int count;
 };
 
-// Copies up to four matrices into rows of a 16-byte pitch: a warp takes a row,
-// 16 bytes a lane.  The pad columns are written as zeros and never read (the
-// tensor maps end at the matrix's own columns).  Blocks `block` of `blocks`.
+// Copies up to four matrices into rows of a 16-byte pitch.  A warp takes 1024
+// elements of a row, four chunks a lane in flight.  The pad columns are
+// written as zeros and never read (the tensor maps end at the matrix's own
+// columns).  Blocks `block` of `blocks`.
+constexpr int kPackSpan = 1024;
 __device__ __forceinline__ void ffn_pack_rows(const FfnPackArgs& a, int block, int blocks) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
+  const long long warps = (long long)blocks * 8;
+  long long skip = 0;  // this warp's first unit in the next matrix: units are dealt on over all of them
+  const long long me = (long long)block * 8 + (threadIdx.x >> 5);
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     if (t >= a.count) break;
-    for (long long r = (long long)block * 8 + warp; r < a.rows[t]; r += (long long)blocks * 8) {
+    const uint32_t spans = (uint32_t)(a.cols[t] + kPackSpan - 1) / kPackSpan;
+    const long long units = (long long)a.rows[t] * spans;
+    const uint16_t *lo = a.src[t], *hi = lo + (long long)(a.rows[t] - 1) * a.ld[t] + a.cols[t];
+    long long i = me - skip;
+    if (i < 0) i += warps;
+    for (; i < units; i += warps) {
+      // (a row index fits 32 bits; 64-bit division only where the units do not)
+      const long long r = units <= 0x7fffffffLL ? (long long)((uint32_t)i / spans) : i / spans;
+      const int c0 = (int)(i - r * spans) * kPackSpan + lane * 8;
       const uint16_t* s = a.src[t] + r * a.ld[t];
       uint16_t* d = a.dst[t] + r * a.ldd[t];
-#pragma unroll 4
-      for (int c = lane * 8; c < a.cols[t]; c += 256)
-        *reinterpret_cast<uint4*>(d + c) = ffn_load8(s + c, a.cols[t] - c);
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + j * 256;
+        if (c < a.cols[t]) v[j] = ffn_load8_any(s + c, a.cols[t] - c, lo, hi);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + j * 256;
+        if (c < a.cols[t]) *reinterpret_cast<uint4*>(d + c) = v[j];
+      }
     }
+    skip = (skip + units) % warps;
   }
 }
 
@@ -77,7 +99,11 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const __grid_co
   float sg[8], su[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sg[j] = su[j] = 0.0f;
-  auto load = [&](const uint16_t* p) { return VEC ? ldg_stream_16(p) : ffn_load8(p, n); };
+  const long long last = a.M - 1;
+  const uint16_t *eh = a.dh + last * a.ld_dh + a.N, *eg = a.g + last * a.ld_g + a.N, *eu = a.u + last * a.ld_u + a.N;
+  auto load = [&](const uint16_t* p, const uint16_t* lo, const uint16_t* hi) {
+    return VEC ? ldg_stream_16(p) : ffn_load8_any(p, n, lo, hi);
+  };
   auto grad = [&](auto act, const uint4& vh, const uint4& vg, const uint4& vu, long long row) {
     float dh[8], g[8], u[8], dg[8], du[8];
     ffn_unpack8<DT>(vh, dh);
@@ -102,12 +128,12 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const __grid_co
     for (long long row = (long long)rb * a.rows + warp; row < row_end; row += 16) {
       const bool two = row + 8 < row_end;
       const uint16_t *ph = a.dh + row * a.ld_dh + c, *pg = a.g + row * a.ld_g + c, *pu = a.u + row * a.ld_u + c;
-      const uint4 h0 = load(ph), g0 = load(pg), u0 = load(pu);
+      const uint4 h0 = load(ph, a.dh, eh), g0 = load(pg, a.g, eg), u0 = load(pu, a.u, eu);
       uint4 h1 = make_uint4(0, 0, 0, 0), g1 = h1, u1 = h1;
       if (two) {
-        h1 = load(ph + 8 * a.ld_dh);
-        g1 = load(pg + 8 * a.ld_g);
-        u1 = load(pu + 8 * a.ld_u);
+        h1 = load(ph + 8 * a.ld_dh, a.dh, eh);
+        g1 = load(pg + 8 * a.ld_g, a.g, eg);
+        u1 = load(pu + 8 * a.ld_u, a.u, eu);
       }
       grad(act, h0, g0, u0, row);
       if (two) grad(act, h1, g1, u1, row + 8);

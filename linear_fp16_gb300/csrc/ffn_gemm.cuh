@@ -63,6 +63,33 @@ __device__ __forceinline__ uint4 ffn_load8(const uint16_t* __restrict__ p, int n
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The same for rows that no wide load fits, where [lo, hi) is the memory the
+// matrix spans: the two 16-byte vectors around p, shifted into place, where
+// both lie inside that memory; element loads at its ends.  (Eight 2-byte
+// loads a lane made the copies below bound by their number.)
+__device__ __forceinline__ uint4 ffn_load8_any(const uint16_t* __restrict__ p, int n, const void* lo, const void* hi) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), a0 = a & ~uintptr_t(15);
+  if (n < 8 || a0 < reinterpret_cast<uintptr_t>(lo) || a0 + 32 > reinterpret_cast<uintptr_t>(hi)) return ffn_load8(p, n);
+  const uint4 u = __ldg(reinterpret_cast<const uint4*>(a0));
+  const uint32_t sh = (uint32_t)(a - a0);
+  if (sh == 0) return u;
+  const uint4 v = __ldg(reinterpret_cast<const uint4*>(a0) + 1);
+  uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  if (sh & 8u) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (sh & 4u) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  if (sh & 2u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 template <int DT>
 __device__ __forceinline__ void ffn_unpack8(const uint4& v, float (&f)[8]) {
   const float2 a = ep_unpack_t<DT>(v.x), b = ep_unpack_t<DT>(v.y), c = ep_unpack_t<DT>(v.z), d = ep_unpack_t<DT>(v.w);
@@ -306,7 +333,7 @@ __device__ __forceinline__ void ffn_bias_grad(const FfnBiasGrad& b, float* red, 
         const bool vec = nc == 8 && b.ld % 8 == 0 && (reinterpret_cast<uintptr_t>(b.d) & 15u) == 0;
 #pragma unroll 4
         for (long long r = part; r < b.rows; r += lanes) {
-          const uint4 v = vec ? __ldg(reinterpret_cast<const uint4*>(p + r * b.ld)) : ffn_load8(p + r * b.ld, nc);
+          const uint4 v = vec ? __ldg(reinterpret_cast<const uint4*>(p + r * b.ld)) : ffn_load8_any(p + r * b.ld, nc, b.d, b.d + (b.rows - 1) * b.ld + b.N);
           float f[8];
           ffn_unpack8<DT>(v, f);
 #pragma unroll

@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(WARPS * 32) gated_gemv_any_kernel(const GatedG
   const uint16_t* __restrict__ uB = a.wu + rowB;
   const uint16_t* __restrict__ x0 = a.x + (okx0 ? r : 0) * a.ldx;
   const uint16_t* __restrict__ x1 = a.x + (okx1 ? r + 8 : 0) * a.ldx;
+  const uint16_t *ge = a.wg + (size_t)N * K, *ue = a.wu + (size_t)N * K, *xe = a.x + (M - 1) * a.ldx + K;
   grid_dep_wait();
   grid_dep_launch();
 
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(WARPS * 32) gated_gemv_any_kernel(const GatedG
 #pragma unroll
     for (int i = 0; i < 4; ++i) dg[q][i] = du[q][i] = 0.0f;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  constexpr int U = 4;  // steps of 32 along K in flight
+  constexpr int U = NT == 1 ? 4 : 2;  // steps of 32 along K in flight
   for (int k0 = k_begin; k0 < k_end; k0 += 32 * U) {
     uint4 vga[U], vgb[U], vua[U], vub[U], vx[U][NT];
 #pragma unroll
@@ -248,13 +249,13 @@ __global__ void __launch_bounds__(WARPS * 32) gated_gemv_any_kernel(const GatedG
       const int k = k0 + 32 * s + 8 * t;
       const int n = k_end - k;
       const bool in = n > 0;
-      vga[s] = in && okA ? ffn_load8(gA + k, n) : zero;
-      vgb[s] = in && okB ? ffn_load8(gB + k, n) : zero;
-      vua[s] = in && okA ? ffn_load8(uA + k, n) : zero;
-      vub[s] = in && okB ? ffn_load8(uB + k, n) : zero;
-      vx[s][0] = in && okx0 ? ffn_load8(x0 + k, n) : zero;
+      vga[s] = in && okA ? ffn_load8_any(gA + k, n, a.wg, ge) : zero;
+      vgb[s] = in && okB ? ffn_load8_any(gB + k, n, a.wg, ge) : zero;
+      vua[s] = in && okA ? ffn_load8_any(uA + k, n, a.wu, ue) : zero;
+      vub[s] = in && okB ? ffn_load8_any(uB + k, n, a.wu, ue) : zero;
+      vx[s][0] = in && okx0 ? ffn_load8_any(x0 + k, n, a.x, xe) : zero;
       if (NT > 1)
-        vx[s][NT - 1] = in && okx1 ? ffn_load8(x1 + k, n) : zero;
+        vx[s][NT - 1] = in && okx1 ? ffn_load8_any(x1 + k, n, a.x, xe) : zero;
     }
 #pragma unroll
     for (int s = 0; s < U; ++s) {

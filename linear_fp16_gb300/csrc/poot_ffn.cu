@@ -148,7 +148,7 @@ struct Packer {
     a.src[t] = static_cast<const uint16_t*>(o->p);
     a.ld[t] = o->ld;
     a.ldd[t] = ceil8(o->cols);
-    a.rows[t] = o->rows;
+    a.rows[t] = static_cast<int>(o->rows);
     a.cols[t] = static_cast<int>(o->cols);
     bytes += round256(size_t(o->rows) * a.ldd[t] * 2);
   }
@@ -160,11 +160,11 @@ struct Packer {
       base += round256(size_t(a.rows[t]) * a.ldd[t] * 2);
     }
   }
-  // blocks that copy eight rows each, a few times over
+  // eight warps a block, a unit (see ffn_pack_rows) a warp while they last
   int blocks(int sms) const {
-    int64_t rows = 0;
-    for (int t = 0; t < a.count; ++t) rows = std::max<int64_t>(rows, a.rows[t]);
-    return static_cast<int>(std::min<int64_t>(ceil_div(rows, 8), int64_t(sms) * 6));
+    int64_t units = 0;
+    for (int t = 0; t < a.count; ++t) units += int64_t(a.rows[t]) * ceil_div(a.cols[t], kPackSpan);
+    return static_cast<int>(std::min<int64_t>(ceil_div(units, 8), int64_t(sms) * 8));
   }
   cudaError_t run(int sms, cudaStream_t stream) const {
     if (a.count == 0) return cudaSuccess;
