@@ -164,64 +164,62 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const __grid_co
 }
 
 struct FfnReduceArgs {
-  const float* ws;  // [outputs][S][M][N] (gated: outputs 2, gate and up)
+  const float* ws;  // [outputs][S][M][ldw] (gated: outputs 2, gate and up)
   uint16_t* y[3];   // gated: h, g, u (g and u may be nullptr); else the outputs
   const uint16_t* bias[2];
-  long long MN;
-  int S, N, outputs, dtype, act, gated;
+  long long M;
+  int S, N, ldw, outputs, dtype, act, gated;
 };
 
 // Second half of a split product: the S partial sums of an element are added
-// in order; then the gated epilogue or one rounding.
+// in order; then the gated epilogue or one rounding.  Four columns a thread
+// (the workspace's rows are padded to that).
 __global__ void __launch_bounds__(256) ffn_reduce_kernel(const FfnReduceArgs a) {
   grid_dep_wait();
   grid_dep_launch();
-  const int dt = a.dtype;
-  const long long total = a.gated ? a.MN : a.outputs * a.MN;
-  const bool vec = a.N % 4 == 0;  // then every 4 consecutive elements lie in one row
-  const long long units = vec ? total / 4 : total;
-  const int w = vec ? 4 : 1;
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < units; i += gridDim.x * 256LL) {
-    const long long e = i * w;
-    const int o = (int)(e / a.MN);
-    const long long off = e - o * a.MN;
+  const int dt = a.dtype, quads = a.ldw / 4;
+  const long long per = a.M * quads, total = a.gated ? per : a.outputs * per, slab = a.M * a.ldw;
+  const bool vec = a.N % 4 == 0;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
+    const int o = i >= per ? 1 : 0;  // (at most two outputs)
+    const long long e = i - o * per;
+    const long long row = e <= 0x7fffffffLL ? (long long)((uint32_t)e / (uint32_t)quads) : e / quads;
+    const int col = (int)(e - row * quads) * 4;
+    const int n = min(4, a.N - col);
     float s[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (h == 1 && !a.gated) break;
-      const float* p = a.ws + ((long long)(a.gated ? h : o) * a.S) * a.MN + off;
+      const float* p = a.ws + (long long)(a.gated ? h : o) * a.S * slab + row * a.ldw + col;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < a.S; ++k, p += a.MN) {
-        if (vec) {
-          const float4 t = __ldg(reinterpret_cast<const float4*>(p));
-          v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
-        } else {
-          v.x += __ldg(p);
-        }
+#pragma unroll 4
+      for (int k = 0; k < a.S; ++k) {
+        const float4 t = __ldg(reinterpret_cast<const float4*>(p + k * slab));
+        v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
       }
       s[h][0] = v.x; s[h][1] = v.y; s[h][2] = v.z; s[h][3] = v.w;
     }
+    const long long off = row * a.N + col;
     auto put = [&](uint16_t* y, const float (&f)[4]) {
       const uint32_t lo = ep_pack(f[0], f[1], dt), hi = ep_pack(f[2], f[3], dt);
-      if (!vec) {
-        y[off] = (uint16_t)(lo & 0xffffu);
-      } else if ((reinterpret_cast<uintptr_t>(y) & 7u) == 0) {
+      if (vec && (reinterpret_cast<uintptr_t>(y) & 7u) == 0) {
         *reinterpret_cast<uint2*>(y + off) = make_uint2(lo, hi);
       } else {
-        y[off] = (uint16_t)lo; y[off + 1] = (uint16_t)(lo >> 16);
-        y[off + 2] = (uint16_t)hi; y[off + 3] = (uint16_t)(hi >> 16);
+        const uint16_t w[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < n) y[off + j] = w[j];
       }
     };
     if (a.gated) {
-      const int col = (int)(off % a.N);
       float h[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (j < w) {
+        if (j < n) {
           if (a.bias[0] != nullptr) s[0][j] += ep_widen(__ldg(a.bias[0] + col + j), dt);
           if (a.bias[1] != nullptr) s[1][j] += ep_widen(__ldg(a.bias[1] + col + j), dt);
         }
-        h[j] = j < w ? act_value(a.act, s[0][j]) * s[1][j] : 0.0f;
+        h[j] = j < n ? act_value(a.act, s[0][j]) * s[1][j] : 0.0f;
       }
       if (a.y[1] != nullptr) { put(a.y[1], s[0]); put(a.y[2], s[1]); }
       put(a.y[0], h);
@@ -236,7 +234,7 @@ __global__ void __launch_bounds__(256) gated_bias_kernel(const FfnReduceArgs a) 
   grid_dep_wait();
   grid_dep_launch();
   const int dt = a.dtype;
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < a.MN; i += gridDim.x * 256LL) {
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < a.M * a.N; i += gridDim.x * 256LL) {
     const int col = (int)(i % a.N);
     const float g = a.bias[0] != nullptr ? ep_widen(__ldg(a.bias[0] + col), dt) : 0.0f;
     const float u = a.bias[1] != nullptr ? ep_widen(__ldg(a.bias[1] + col), dt) : 0.0f;

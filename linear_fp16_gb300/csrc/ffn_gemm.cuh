@@ -44,10 +44,10 @@ enum FfnAct : int { kActSilu = 0, kActGeluTanh = 1, kActGeluErf = 2 };
 
 constexpr int kFfnBM = 128;
 constexpr int kFfnBK = 64;  // one 128-byte swizzle row
-constexpr int kFfnEpiWarps = 8;
-constexpr int kFfnMmaWarp = 8;
-constexpr int kFfnProdWarp = 9;
-constexpr int kFfnThreads = 10 * 32;
+constexpr int kFfnEpiWarps = 16;
+constexpr int kFfnMmaWarp = 16;
+constexpr int kFfnProdWarp = 17;
+constexpr int kFfnThreads = 18 * 32;
 constexpr int kFfnMaxBN = 256;
 constexpr int kFfnMaxStages = 8;
 constexpr uint32_t kFfnTmemCols = 2 * kFfnMaxBN;
@@ -110,8 +110,37 @@ __device__ __forceinline__ uint4 ffn_pack8(const float (&f)[8]) {
 //   gelu_erf   t P(t), P = 0.5 (1 + erf(t / sqrt 2));  P + t p(t), p the
 //              normal density
 // Where s is 0 or 1 in FP32 the product s (1 - s) is 0 and z' may overflow:
-// the second term is then dropped, as in the limit.
-__device__ __forceinline__ float act_sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// the second term is then dropped, as in the limit.  Exponential and quotient
+// are the approximate instructions (2^-22 relative each), far below the one
+// rounding to 11 or 8 bits that follows.
+__device__ __forceinline__ float act_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float act_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float act_sigmoid(float z) { return act_rcp(1.0f + act_exp2(-kLog2e * z)); }
+
+// The normal distribution function P(t) and e = exp(-t^2 / 2), by formula
+// 7.1.26 of Abramowitz and Stegun's Handbook of Mathematical Functions
+// (|error| <= 1.5e-7): erfc(x) = (a1 k + .. + a5 k^5) exp(-x^2), k = 1 / (1 +
+// p x).  The negative tail is the product itself, so it keeps its relative
+// precision, and the density of the derivative shares the exponential.
+__device__ __forceinline__ float act_normal(float t, float& e) {
+  const float x = fabsf(t) * 0.70710678118654752f;
+  const float k = act_rcp(fmaf(0.3275911f, x, 1.0f));
+  e = act_exp2(-kLog2e * x * x);
+  float q = fmaf(0.5f * 1.061405429f, k, 0.5f * -1.453152027f);
+  q = fmaf(q, k, 0.5f * 1.421413741f);
+  q = fmaf(q, k, 0.5f * -0.284496736f);
+  q = fmaf(q, k, 0.5f * 0.254829592f) * k * e;
+  return t < 0.0f ? q : 1.0f - q;
+}
 
 template <int ACT>
 __device__ __forceinline__ float act_value_t(float t) {
@@ -120,7 +149,8 @@ __device__ __forceinline__ float act_value_t(float t) {
   } else if constexpr (ACT == kActGeluTanh) {
     return t * act_sigmoid(1.5957691216057308f * fmaf(0.044715f * t * t, t, t));
   } else {
-    return 0.5f * t * (1.0f + erff(t * 0.70710678118654752f));
+    float e;
+    return t * act_normal(t, e);
   }
 }
 __device__ __forceinline__ float act_value(int act, float t) {
@@ -132,9 +162,10 @@ __device__ __forceinline__ float act_value(int act, float t) {
 template <int ACT>
 __device__ __forceinline__ void act_both_t(float t, float& v, float& d) {
   if constexpr (ACT == kActGeluErf) {
-    const float p = 0.5f * (1.0f + erff(t * 0.70710678118654752f));
+    float e;
+    const float p = act_normal(t, e);
     v = t * p;
-    d = fmaf(t, 0.3989422804014327f * __expf(-0.5f * t * t), p);
+    d = e != 0.0f ? fmaf(t * 0.3989422804014327f, e, p) : p;
   } else {
     float z = t, dz = 1.0f;
     if constexpr (ACT == kActGeluTanh) {
@@ -176,11 +207,12 @@ struct FfnJob {
   int kb_split;      // K blocks of a range (the last may be shorter)
   int tma_store;     // outputs stored by TMA; 0: plain stores
   uint16_t* y[3];    // row pitch N
-  float* partial;    // split > 1: FP32 sums [outputs][split][M][N] (gated: gate, up)
+  float* partial;    // split > 1: FP32 sums [outputs][split][M][N rounded up to 4] (gated: gate, up)
 };
 
 struct FfnMaps {
   CUtensorMap a[2][2], b[2][2], y[2][3];  // [job][operand]
+  CUtensorMap partial[2];                 // FP32 [slabs][M][N], rows of a 16-byte pitch
 };
 
 // Bias gradients, done by the epilogue warps before their first tile: db[o] =
@@ -202,7 +234,7 @@ struct FfnGemmArgs {
   int cols;          // output columns of a tile
   int stages;
   int extra;         // see FfnSchedule
-  int dtype, act, save;
+  int act, save;
   const uint16_t* bias[2];  // gated: bg, bu or nullptr
 };
 
@@ -232,13 +264,15 @@ struct FfnSchedule {
   }
 };
 
-// Shared memory: operand ring, then per epilogue warp two 2 KB staging boxes,
-// then barriers.
+// Shared memory: operand ring, then per epilogue warp a 2 KB staging box and
+// the biases of a tile's columns, then barriers.  Sixteen epilogue warps: with
+// eight the epilogue, not the products, set the time where K is short.
 struct FfnLayout {
   static constexpr int RING_BYTES = 192 * 1024;
   static constexpr int STG_BYTES = 32 * 32 * 2;
   static constexpr int OFF_STG = RING_BYTES;
-  static constexpr int OFF_BAR = OFF_STG + kFfnEpiWarps * 2 * STG_BYTES;
+  static constexpr int OFF_BIAS = OFF_STG + kFfnEpiWarps * STG_BYTES;  // [accumulator][box][gate, up][32]
+  static constexpr int OFF_BAR = OFF_BIAS + 2 * 4 * 2 * 32 * 2;
   static constexpr int NUM_BARS = 2 * kFfnMaxStages + 5;  // full, empty, acc full x2, acc empty x2, drain
   static constexpr int OFF_TMEM_SLOT = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
@@ -358,7 +392,7 @@ __device__ __forceinline__ void ffn_bias_grad(const FfnBiasGrad& b, float* red, 
   }
 }
 
-template <int CL, bool GATED>
+template <int CL, bool GATED, int DT>
 __global__ void __launch_bounds__(kFfnThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemmArgs args) {
   using L = FfnLayout;
@@ -519,7 +553,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         constexpr uint32_t AK = A_MN ? 2048u >> 4 : 2u, BKS = B_MN ? 2048u >> 4 : 2u;
         const FfnJob& job = args.job[ji];
         const uint32_t idesc = idesc_f16_f32acc(PAIR ? 2 * kFfnBM : kFfnBM, (uint32_t)BN) |
-                               (args.dtype == kEpiBf16 ? ((1u << 7) | (1u << 10)) : 0u) |
+                               (DT == kEpiBf16 ? ((1u << 7) | (1u << 10)) : 0u) |
                                (A_MN ? (1u << 15) : 0u) | (B_MN ? (1u << 16) : 0u);
         const int tiles = sched.count(ji);
         for (int ti = 0; ti < tiles && ok; ++ti) {
@@ -565,146 +599,146 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;   // TMEM lanes 32q .. 32q+31
-    const int half = warp >> 2;
-    // output columns of this warp: 32-column boxes half, half + 2, ...
+    const int part = warp >> 2;
+    // this warp's 32-column boxes of a tile: part, part + 4, ...
     const int boxes = args.cols / 32;
-    uint8_t* stg = smem + L::OFF_STG + warp * 2 * L::STG_BYTES;
-    const uint32_t stg_addr = sbase + L::OFF_STG + warp * 2 * L::STG_BYTES;
-    int sbuf = 0;
+    uint8_t* stg = smem + L::OFF_STG + warp * L::STG_BYTES;
+    const uint32_t stg_addr = sbase + L::OFF_STG + warp * L::STG_BYTES;
     int buf = 0;
     uint32_t buf_phase = 0;
-    const int dt = args.dtype;
-    if (!GATED && args.bias_grad.outputs > 0) {
-      // 256 x 9 FP32 over the staging boxes of all epilogue warps
-      float* red = reinterpret_cast<float*>(smem + L::OFF_STG);
-      if (dt == kEpiBf16) ffn_bias_grad<kEpiBf16>(args.bias_grad, red, (int)blockIdx.x, (int)gridDim.x, threadIdx.x);
-      else ffn_bias_grad<kEpiF16>(args.bias_grad, red, (int)blockIdx.x, (int)gridDim.x, threadIdx.x);
-    }
+    if (!GATED && args.bias_grad.outputs > 0)
+      // 512 x 9 FP32 over the staging boxes of all epilogue warps
+      ffn_bias_grad<DT>(args.bias_grad, reinterpret_cast<float*>(smem + L::OFF_STG), (int)blockIdx.x, (int)gridDim.x,
+                        threadIdx.x);
     const int tiles0 = sched.count(0), tiles = tiles0 + (GATED ? 0 : sched.count(1));
     for (int ti = 0; ti < tiles; ++ti) {
       const int ji = ti < tiles0 ? 0 : 1, t = sched.tile(ji, ji == 0 ? ti : ti - tiles0);
       const FfnJob& job = args.job[ji];
       const int M = job.M, N = job.N;
+      int s, g, mb, nb;
+      tile_decode(job, t, s, g, mb, nb);
+      const int m0 = mb * tile_rows + (int)rank * kFfnBM + q * 32, n0 = nb * args.cols;
 
-      // 16 packed pairs (this lane's row of a 32 x 32 box) to output `o`
-      auto store_box = [&](const uint32_t (&packed)[16], int o, int row0, int nc) {
-        if (job.tma_store) {
-          if (lane == 0) bulk_wait_group_read<1>();
-          __syncwarp();
-        }
-        uint8_t* rowp = stg + sbuf * L::STG_BYTES + lane * 64;
+      // The 32 x 32 box at (m0, nc) of output `o`, this lane's row given as
+      // 16 packed pairs value(0) .. value(15), through the staging box: 64
+      // bytes a row, chunk j at j ^ ((row >> 1) & 3) (TMA's 64-byte swizzle).
+      auto store_box = [&](int o, int nc, auto&& value) {
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+        uint8_t* rowp = stg + lane * 64;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int pos = j ^ ((lane >> 1) & 3);
-          *reinterpret_cast<uint4*>(rowp + pos * 16) =
-              make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
-        }
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(rowp + (j ^ ((lane >> 1) & 3)) * 16) =
+              make_uint4(value(4 * j), value(4 * j + 1), value(4 * j + 2), value(4 * j + 3));
         if (job.tma_store) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&maps.y[ji][o], stg_addr + sbuf * L::STG_BYTES, nc, row0);
+            tma_store_2d(&maps.y[ji][o], stg_addr, nc, m0);
             bulk_commit_group();
           }
         } else {
           __syncwarp();
-          const uint8_t* box = stg + sbuf * L::STG_BYTES;
           uint16_t* const yo = o == 0 ? job.y[0] : (o == 1 ? job.y[1] : job.y[2]);
-          const int col = nc + lane;
-#pragma unroll 4
-          for (int rr = 0; rr < 32; ++rr) {
-            const int r = row0 + rr;
-            if (r < M && col < N) {
-              const int pos = (lane >> 3) ^ ((rr >> 1) & 3);
-              yo[(size_t)r * N + col] = *reinterpret_cast<const uint16_t*>(box + rr * 64 + pos * 16 + (lane & 7) * 2);
-            }
+          // lane: column of the box; rows advance by pointer
+          const bool in = nc + lane < N;
+          const int rows = min(32, M - m0);
+          uint16_t* dst = yo + (size_t)m0 * N + nc + lane;
+          const uint8_t* src = stg + (lane & 7) * 2;
+          if (in) {
+#pragma unroll 8
+            for (int rr = 0; rr < rows; ++rr, dst += N)
+              *dst = *reinterpret_cast<const uint16_t*>(src + rr * 64 + (((lane >> 3) ^ ((rr >> 1) & 3)) << 4));
           }
           __syncwarp();
         }
-        sbuf ^= 1;
       };
-      // this lane's row of FP32 sums of a 32 x 32 box to the partial sums
-      auto store_partial = [&](const uint32_t (&r)[32], int slab, int row, int nc) {
-        if (row >= M) return;
-        float* p = job.partial + ((size_t)slab * M + row) * N + nc;
-        if (N % 4 == 0) {
+      // a box of FP32 sums to the partial sums, as two 32 x 16 boxes (64 bytes
+      // a row, the same swizzle)
+      auto store_partial = [&](const uint32_t (&r)[32], int slab, int nc) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (nc + 4 * j < N)
-              *reinterpret_cast<uint4*>(p + 4 * j) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-        } else {
+        for (int h = 0; h < 2; ++h) {
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+          uint8_t* rowp = stg + lane * 64;
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (nc + j < N) p[j] = __uint_as_float(r[j]);
+          for (int j = 0; j < 4; ++j) {
+            const int c = 16 * h + 4 * j;
+            *reinterpret_cast<uint4*>(rowp + (j ^ ((lane >> 1) & 3)) * 16) = make_uint4(r[c], r[c + 1], r[c + 2], r[c + 3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&maps.partial[ji], stg_addr, nc + 16 * h, m0, slab);
+            bulk_commit_group();
+          }
         }
       };
-      int s, g, mb, nb;
-      tile_decode(job, t, s, g, mb, nb);
-      const int m0 = mb * tile_rows + (int)rank * kFfnBM + q * 32, n0 = nb * args.cols;
+
       const bool got = mbar_wait(bar_cfull(buf), buf_phase, abort_flag);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after_sync();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kFfnMaxBN);
+      const bool rows_in = m0 < M;  // warp-uniform
 #pragma unroll 1
-      for (int bx = half; bx < boxes; bx += 2) {
+      for (int bx = part; bx < boxes; bx += 4) {
         const int nc = n0 + bx * 32;
+        if (nc >= N || !rows_in) break;  // warp-uniform: nothing of the box is in the output
         uint32_t r[32];
         tmem_ld_32x32b_x32(taddr + (uint32_t)(bx * 32), r);
         if constexpr (GATED) {
           uint32_t r2[32];
           tmem_ld_32x32b_x32(taddr + (uint32_t)(BN / 2 + bx * 32), r2);
+          const bool biased = args.bias[0] != nullptr || args.bias[1] != nullptr;
+          uint16_t* const sbias = reinterpret_cast<uint16_t*>(smem + L::OFF_BIAS) + (buf * 4 + part) * 64;
+          static_assert(kFfnMaxBN / 2 / 32 <= 4, "a warp has one box of a gated tile");
+          if (biased && job.split == 1) {
+            // lane l fetches the biases of column nc + l.  The four warps of a
+            // box write the same values; the slot is this accumulator's, and
+            // no warp is two tiles ahead of another.
+            const int col = nc + lane;
+            sbias[lane] = (args.bias[0] != nullptr && col < N) ? __ldg(args.bias[0] + col) : (uint16_t)0;
+            sbias[32 + lane] = (args.bias[1] != nullptr && col < N) ? __ldg(args.bias[1] + col) : (uint16_t)0;
+            __syncwarp();
+          }
           tmem_ld_wait();
-          if (nc >= N) continue;  // warp-uniform
           if (job.split > 1) {
-            store_partial(r, s, m0 + lane, nc);
-            store_partial(r2, job.split + s, m0 + lane, nc);
+            store_partial(r, s, nc);
+            store_partial(r2, job.split + s, nc);
             continue;
           }
-          if (args.bias[0] != nullptr || args.bias[1] != nullptr) {
-            // lane l holds the biases of column nc + l
-            const int col = nc + lane;
-            const float bg = (args.bias[0] != nullptr && col < N) ? ep_widen(__ldg(args.bias[0] + col), dt) : 0.0f;
-            const float bu = (args.bias[1] != nullptr && col < N) ? ep_widen(__ldg(args.bias[1] + col), dt) : 0.0f;
+          if (biased) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              r[j] = __float_as_uint(__uint_as_float(r[j]) + __shfl_sync(0xffffffffu, bg, j));
-              r2[j] = __float_as_uint(__uint_as_float(r2[j]) + __shfl_sync(0xffffffffu, bu, j));
+            for (int j = 0; j < 4; ++j) {
+              float gv[8], uv[8];
+              ffn_unpack8<DT>(reinterpret_cast<const uint4*>(sbias)[j], gv);
+              ffn_unpack8<DT>(reinterpret_cast<const uint4*>(sbias)[4 + j], uv);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                r[8 * j + k] = __float_as_uint(__uint_as_float(r[8 * j + k]) + gv[k]);
+                r2[8 * j + k] = __float_as_uint(__uint_as_float(r2[8 * j + k]) + uv[k]);
+              }
             }
           }
-          uint32_t packed[16];
           if (args.save) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              packed[i] = ep_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), dt);
-            store_box(packed, 1, m0, nc);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              packed[i] = ep_pack(__uint_as_float(r2[2 * i]), __uint_as_float(r2[2 * i + 1]), dt);
-            store_box(packed, 2, m0, nc);
+            store_box(1, nc, [&](int i) { return ep_pack_t<DT>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])); });
+            store_box(2, nc, [&](int i) { return ep_pack_t<DT>(__uint_as_float(r2[2 * i]), __uint_as_float(r2[2 * i + 1])); });
           }
           auto gate = [&](auto act) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              packed[i] = ep_pack(act_value_t<decltype(act)::value>(__uint_as_float(r[2 * i])) * __uint_as_float(r2[2 * i]),
-                                  act_value_t<decltype(act)::value>(__uint_as_float(r[2 * i + 1])) * __uint_as_float(r2[2 * i + 1]),
-                                  dt);
+            constexpr int ACT = decltype(act)::value;
+            store_box(0, nc, [&](int i) {
+              return ep_pack_t<DT>(act_value_t<ACT>(__uint_as_float(r[2 * i])) * __uint_as_float(r2[2 * i]),
+                                   act_value_t<ACT>(__uint_as_float(r[2 * i + 1])) * __uint_as_float(r2[2 * i + 1]));
+            });
           };
           if (args.act == kActSilu) gate(std::integral_constant<int, kActSilu>{});
           else if (args.act == kActGeluTanh) gate(std::integral_constant<int, kActGeluTanh>{});
           else gate(std::integral_constant<int, kActGeluErf>{});
-          store_box(packed, 0, m0, nc);
         } else {
           tmem_ld_wait();
-          if (nc >= N) continue;
-          if (job.split > 1) {
-            store_partial(r, g * job.split + s, m0 + lane, nc);
-            continue;
-          }
-          uint32_t packed[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            packed[i] = ep_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), dt);
-          store_box(packed, g, m0, nc);
+          if (job.split > 1) store_partial(r, g * job.split + s, nc);
+          else
+            store_box(g, nc, [&](int i) { return ep_pack_t<DT>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])); });
         }
       }
       tc_fence_before_sync();

@@ -46,8 +46,11 @@ FfnDevice g_devices[kMaxDevices];
 
 template <int CL, bool GATED>
 cudaError_t set_attr() {
-  return cudaFuncSetAttribute(ffn_gemm_kernel<CL, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              FfnLayout::DYN_BYTES);
+  const cudaError_t e = cudaFuncSetAttribute(ffn_gemm_kernel<CL, GATED, kEpiF16>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, FfnLayout::DYN_BYTES);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(ffn_gemm_kernel<CL, GATED, kEpiBf16>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, FfnLayout::DYN_BYTES);
 }
 
 template <int NT, int DT>
@@ -187,54 +190,86 @@ struct FfnProduct {
   void* y[3] = {nullptr, nullptr, nullptr};
   int64_t kb() const { return ceil_div(kext, kFfnBK) * parts; }
   size_t partial_bytes(int split) const {
-    return split > 1 ? round256(size_t(split) * (gated ? 2 : outputs) * rows * cols * 4) : 0;
+    return split > 1 ? round256(size_t(split) * (gated ? 2 : outputs) * rows * ceil_div(cols, 4) * 16) : 0;
   }
 };
 
-// Cost model: a 64-element K block of a 128-row tile takes max(2 bn, 128 + bn)
-// cycles of MMA or operand reads, divided by the efficiency of the shape, plus
-// a fixed fill and drain per tile; the tiles of all products fill the CTA
-// (pair) slots together, the longest tile at least.  A split over K adds the
-// second kernel and its bytes.
+// Time of a plan, in microseconds, from a model fitted to GB300 timings of 240
+// single and paired products of 17 .. 8192 rows under every tile and split
+// (the plan it picks is within 2% of the best of them on average, 31% at
+// worst): a tile takes its K blocks at the shape's rate plus a fill, or its
+// epilogue where that is longer; the tiles fill the CTAs (pairs) as
+// FfnSchedule deals them; all of it takes at least the operands' time from
+// HBM; a split adds the second kernel and the partial sums' traffic.
+struct FfnShape {
+  int cl, bn;
+  double per_kb;  // 64 elements of K
+};
+constexpr FfnShape kFfnShapes[] = {{2, 256, 0.264}, {2, 128, 0.244}, {1, 256, 0.335}, {1, 128, 0.281}, {1, 64, 0.236}};
+
+double plan_time(const FfnProduct* const* ps, int count, const FfnShape& s, const int* split, int sms, double bytes) {
+  const int64_t slots = sms / s.cl;
+  int64_t tiles[2] = {0, 0}, kbs[2] = {1, 1};
+  double tile[2] = {0, 0}, last = 0, added = s.cl == 2 ? 0.39 : 0.0;
+  for (int i = 0; i < count; ++i) {
+    const FfnProduct& q = *ps[i];
+    const int64_t width = q.gated ? s.bn / 2 : s.bn;
+    const int64_t kb = ceil_div(q.kext, kFfnBK * s.cl) * q.parts;
+    kbs[i] = ceil_div(kb, split[i]);
+    const int64_t S = ceil_div(kb, kbs[i]);
+    const double main = double(kbs[i] * s.cl) * s.per_kb + 0.23;
+    const double epi = 0.137 * double(width) / 128.0;
+    tiles[i] = ceil_div(q.rows, kFfnBM * s.cl) * ceil_div(q.cols, width) * q.outputs * S;
+    tile[i] = std::max(main, epi);
+    last = std::max(last, std::min(main, epi));
+    if (S > 1) added += 1.7 + double(S) * double(q.rows) * double(q.cols) * q.outputs * (q.gated ? 2 : 1) * 1.75e-6;
+  }
+  double t;
+  if (count < 2) {
+    t = double(ceil_div(tiles[0], slots)) * tile[0];
+  } else {
+    const int64_t r = tiles[0] % slots, extra = r != 0 ? (2 * kbs[0] + kbs[1]) / (2 * kbs[1]) : 0;
+    const int64_t common = ceil_div(std::max<int64_t>(0, tiles[1] - extra * (slots - r)), slots);
+    const int64_t taken = r != 0 ? std::min(extra, ceil_div(tiles[1], slots - r)) : 0;
+    t = std::max(double(ceil_div(tiles[0], slots)) * tile[0], double(tiles[0] / slots) * tile[0] + double(taken) * tile[1]) +
+        double(common) * tile[1];
+  }
+  return std::max(t + last, bytes / 5.95e6) + added;
+}
+
 FfnPlan plan_ffn(const FfnProduct* const* ps, int count, int sms) {
-  static const struct { int cl, bn, eff; } shapes[] = {{2, 256, 100}, {2, 128, 80}, {1, 256, 85}, {1, 128, 70}, {1, 64, 55}};
+  double bytes = 0;
+  for (int i = 0; i < count; ++i) {
+    const FfnProduct& q = *ps[i];
+    const int na = q.mn_a ? q.outputs : q.parts, nb = q.gated ? 2 : q.parts;
+    bytes += 2.0 * (double(q.rows) * q.kext * na + double(q.cols) * q.kext * nb + double(q.rows) * q.cols * q.outputs);
+  }
   FfnPlan best;
-  int64_t best_cost = INT64_MAX;
-  for (const auto& s : shapes) {
-    const int64_t slots = s.cl == 2 ? sms / 2 : sms;
-    const int64_t per_kb = std::max<int64_t>(2 * s.bn, 128 + s.bn) * 100 / s.eff;
-    FfnPlan p;
-    p.cl = s.cl;
-    p.bn = s.bn;
-    // tiles and their times at a split; the best split of each product alone
-    int64_t work = 0, longest = 0, waves = 0, added = s.cl == 2 ? 1500 : 0;
+  double best_time = 1e300;
+  for (const FfnShape& s : kFfnShapes) {
+    int split[2] = {1, 1};
+    double t = plan_time(ps, count, s, split, sms, bytes);
+    // splits, one product after the other, while its tiles leave CTAs idle
     for (int i = 0; i < count; ++i) {
       const FfnProduct& q = *ps[i];
-      const int64_t tiles = ceil_div(q.rows, 128 * s.cl) * ceil_div(q.cols, q.gated ? s.bn / 2 : s.bn) * q.outputs;
-      const int64_t kb = q.kb();
-      int64_t alone = INT64_MAX, w = 0, l = 0, e = 0, t_of = 0;
-      for (int S = 1; S <= 16; ++S) {
-        if (S > 1 && (kb / S < 8 || tiles * S > 2 * slots)) break;
-        const int64_t t = ceil_div(kb, S) * per_kb + 1500;
-        const int64_t x = S > 1 ? 6000 + S * q.rows * q.cols * q.outputs * (q.gated ? 2 : 1) * 4 / 2048 : 0;
-        const int64_t cost = ceil_div(tiles * S, slots) * t + x;
-        if (cost < alone) {
-          alone = cost;
-          p.split[i] = S;
-          w = tiles * S * t;
-          l = ceil_div(tiles * S, slots) * t;
-          e = x;
-          t_of = t;
+      const int64_t tiles = ceil_div(q.rows, kFfnBM * s.cl) * ceil_div(q.cols, q.gated ? s.bn / 2 : s.bn) * q.outputs;
+      for (int S = 2; S <= 16 && tiles * S <= 2 * (sms / s.cl) && q.kb() >= 4 * S; S *= 2) {
+        int trial[2] = {split[0], split[1]};
+        trial[i] = S;
+        const double u = plan_time(ps, count, s, trial, sms, bytes);
+        if (u < t) {
+          t = u;
+          split[i] = S;
         }
       }
-      work += w;
-      longest = std::max(longest, t_of);
-      waves = l;
-      added += e;
     }
-    // one product runs in whole waves; two fill each other's gaps
-    const int64_t cost = (count == 1 ? waves : std::max(ceil_div(work, slots) + longest / 2, longest)) + added;
-    if (cost < best_cost) { best_cost = cost; best = p; }
+    if (t < best_time) {
+      best_time = t;
+      best.cl = s.cl;
+      best.bn = s.bn;
+      best.split[0] = split[0];
+      best.split[1] = split[1];
+    }
   }
   return best;
 }
@@ -245,9 +280,10 @@ struct FfnEpilogue {
 };
 
 template <int CL, bool GATED>
-cudaError_t launch_ffn(const FfnMaps& m, const FfnGemmArgs& a, int64_t units, cudaStream_t stream) {
-  return launch_clustered(ffn_gemm_kernel<CL, GATED>, dim3(static_cast<unsigned>(units * CL)), dim3(kFfnThreads),
-                          FfnLayout::DYN_BYTES, stream, unsigned(CL), m, a);
+cudaError_t launch_ffn(const FfnMaps& m, const FfnGemmArgs& a, bool bf16, int64_t units, cudaStream_t stream) {
+  return launch_clustered(bf16 ? ffn_gemm_kernel<CL, GATED, kEpiBf16> : ffn_gemm_kernel<CL, GATED, kEpiF16>,
+                          dim3(static_cast<unsigned>(units * CL)), dim3(kFfnThreads), FfnLayout::DYN_BYTES, stream,
+                          unsigned(CL), m, a);
 }
 
 // Runs up to two products (dx and dW) in one launch, with the
@@ -264,7 +300,6 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
   a.stages = ffn_stages(p.cl, p.bn);
   const bool gated = count > 0 && ps[0]->gated;
   a.cols = gated ? p.bn / 2 : p.bn;
-  a.dtype = ep.dtype;
   a.act = ep.act;
   a.save = ep.save;
   for (int i = 0; i < 2; ++i) a.bias[i] = static_cast<const uint16_t*>(ep.bias[i]);
@@ -315,6 +350,9 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
     if (j.tma_store)
       for (int o = 0; o < ny; ++o)
         ok = ok && encode_2d(&m.y[ji][o], q.y[o], q.cols, q.rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, bf16);
+    if (j.split > 1)
+      ok = ok && encode_3d_f32(&m.partial[ji], j.partial, ceil_div(q.cols, 4) * 4, q.rows,
+                               uint64_t(j.split) * (q.gated ? 2 : q.outputs), 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
     if (!ok) return cuda_fail(cudaErrorInvalidValue);
   }
   for (FfnJob& j : a.job) {
@@ -327,8 +365,8 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
   const int64_t units = a.bias_grad.outputs > 0 ? units_max : std::min<int64_t>(total, units_max);
   const bool pair = p.cl == 2;
   cudaError_t e;
-  if (gated) e = pair ? launch_ffn<2, true>(m, a, units, stream) : launch_ffn<1, true>(m, a, units, stream);
-  else e = pair ? launch_ffn<2, false>(m, a, units, stream) : launch_ffn<1, false>(m, a, units, stream);
+  if (gated) e = pair ? launch_ffn<2, true>(m, a, bf16, units, stream) : launch_ffn<1, true>(m, a, bf16, units, stream);
+  else e = pair ? launch_ffn<2, false>(m, a, bf16, units, stream) : launch_ffn<1, false>(m, a, bf16, units, stream);
   if (e != cudaSuccess) return cuda_fail(e);
   for (int i = 0; i < count; ++i) {
     const FfnProduct& q = *ps[i];
@@ -339,14 +377,15 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
     r.ws = j.partial;
     for (int o = 0; o < 3; ++o) r.y[o] = j.y[o];
     for (int o = 0; o < 2; ++o) r.bias[o] = a.bias[o];
-    r.MN = q.rows * q.cols;
+    r.M = q.rows;
     r.S = j.split;
     r.N = j.N;
+    r.ldw = static_cast<int>(ceil_div(q.cols, 4) * 4);
     r.outputs = q.outputs;
     r.dtype = ep.dtype;
     r.act = ep.act;
     r.gated = q.gated;
-    e = launch(ffn_reduce_kernel, dim3(grid_for(r.MN * q.outputs / (q.cols % 4 == 0 ? 4 : 1), d.sms)), dim3(256), 0,
+    e = launch(ffn_reduce_kernel, dim3(grid_for(r.M * (r.ldw / 4) * q.outputs, d.sms)), dim3(256), 0,
                stream, r);
     if (e != cudaSuccess) return cuda_fail(e);
   }
@@ -433,7 +472,7 @@ int gated_linear(const poot_gated_linear_args* ap, cudaStream_t stream) {
     r.y[2] = static_cast<uint16_t*>(p.u);
     r.bias[0] = static_cast<const uint16_t*>(p.bg);
     r.bias[1] = static_cast<const uint16_t*>(p.bu);
-    r.MN = M * N;
+    r.M = M;
     r.N = static_cast<int>(N);
     r.dtype = p.dtype;
     r.act = p.activation;
