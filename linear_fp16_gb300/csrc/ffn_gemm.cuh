@@ -327,32 +327,36 @@ constexpr int kFfnEpiThreads = kFfnEpiWarps * 32;
 __device__ __forceinline__ void ffn_epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kFfnEpiThreads) : "memory"); }
 
 // Bias gradients by the epilogue warps of all CTAs: a CTA takes consecutive
-// groups of 8 columns (of all outputs, side by side), a thread every
-// (256 / groups)-th row of one group; partial sums meet in shared memory in a
-// fixed order.  FP32 sums, one rounding.
+// groups of 8 columns (of all outputs, side by side), a lane every so-many-th
+// row of one group.  Lanes of a group meet by shuffles, warps in shared
+// memory, in a fixed order.  FP32 sums, one rounding.
 template <int DT>
-__device__ __forceinline__ void ffn_bias_grad(const FfnBiasGrad& b, float* red, int cta, int ctas, int tid) {
+__device__ __forceinline__ void ffn_bias_grad(const FfnBiasGrad& b, float* red, int cta, int ctas) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per_out = (b.N + 7) / 8;             // groups of one output
   const int groups = per_out * b.outputs;
   const int share = (groups + ctas - 1) / ctas;
   const int g0 = cta * share, g1 = min(groups, g0 + share);
   for (int base = g0; base < g1; base += 32) {
     const int n = min(32, g1 - base);            // groups of this round
-    const int lanes = kFfnEpiThreads / n;        // threads per group
-    const int g = tid % n, part = tid / n;
+    int width = 1;                               // lanes side by side on them
+    while (width < n) width *= 2;
+    const int g = lane & (width - 1);
+    const int step = kFfnEpiWarps * 32 / width;  // rows read at one time
+    const int o = (base + g) / per_out, c = ((base + g) - o * per_out) * 8, nc = min(8, b.N - c);
     float s[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] = 0.0f;
-    const int o = (base + g) / per_out, c = ((base + g) - o * per_out) * 8, nc = min(8, b.N - c);
-    if (part < lanes) {
+    if (g < n) {
+      const long long r0 = warp * (32 / width) + lane / width;
       if (b.sums != nullptr) {
         const float* p = b.sums + (size_t)o * b.N + c;
-        const size_t step = (size_t)b.outputs * b.N;
-        const bool vec = b.N % 4 == 0;
+        const size_t pitch = (size_t)b.outputs * b.N;
+        const bool vec = b.N % 4 == 0 && nc == 8;
 #pragma unroll 4
-        for (long long r = part; r < b.rows; r += lanes) {
-          const float* q = p + (size_t)r * step;
-          if (vec && nc == 8) {
+        for (long long r = r0; r < b.rows; r += step) {
+          const float* q = p + (size_t)r * pitch;
+          if (vec) {
             const float4 u = __ldg(reinterpret_cast<const float4*>(q)), v = __ldg(reinterpret_cast<const float4*>(q) + 1);
             s[0] += u.x; s[1] += u.y; s[2] += u.z; s[3] += u.w;
             s[4] += v.x; s[5] += v.y; s[6] += v.z; s[7] += v.w;
@@ -363,28 +367,36 @@ __device__ __forceinline__ void ffn_bias_grad(const FfnBiasGrad& b, float* red, 
           }
         }
       } else {
-        const uint16_t* p = b.d + c;
+        const uint16_t *p = b.d + c, *hi = b.d + (b.rows - 1) * b.ld + b.N;
         const bool vec = nc == 8 && b.ld % 8 == 0 && (reinterpret_cast<uintptr_t>(b.d) & 15u) == 0;
 #pragma unroll 4
-        for (long long r = part; r < b.rows; r += lanes) {
-          const uint4 v = vec ? __ldg(reinterpret_cast<const uint4*>(p + r * b.ld)) : ffn_load8_any(p + r * b.ld, nc, b.d, b.d + (b.rows - 1) * b.ld + b.N);
+        for (long long r = r0; r < b.rows; r += step) {
+          const uint4 v = vec ? __ldg(reinterpret_cast<const uint4*>(p + r * b.ld))
+                              : ffn_load8_any(p + r * b.ld, nc, b.d, hi);
           float f[8];
           ffn_unpack8<DT>(v, f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) s[j] += f[j];
         }
       }
+    }
+    for (int off = width; off < 32; off *= 2) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) red[(part * n + g) * 9 + j] = s[j];
+      for (int j = 0; j < 8; ++j) s[j] += __shfl_xor_sync(0xffffffffu, s[j], off);
+    }
+    if (lane < n) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) red[(warp * 32 + lane) * 9 + j] = s[j];
     }
     ffn_epi_sync();
-    if (tid < n * 8) {
-      const int gg = tid >> 3, j = tid & 7;
+    if ((int)threadIdx.x < n * 8) {
+      const int gg = threadIdx.x >> 3, j = threadIdx.x & 7;
       const int oo = (base + gg) / per_out, col = ((base + gg) - oo * per_out) * 8 + j;
       uint16_t* out = oo ? b.out[1] : b.out[0];
       if (col < b.N && out != nullptr) {
-        float t = red[gg * 9 + j];
-        for (int p = 1; p < lanes; ++p) t += red[(p * n + gg) * 9 + j];
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kFfnEpiWarps; ++w) t += red[(w * 32 + gg) * 9 + j];
         out[col] = (uint16_t)ep_pack_t<DT>(t, 0.0f);
       }
     }
@@ -607,9 +619,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     int buf = 0;
     uint32_t buf_phase = 0;
     if (!GATED && args.bias_grad.outputs > 0)
-      // 512 x 9 FP32 over the staging boxes of all epilogue warps
-      ffn_bias_grad<DT>(args.bias_grad, reinterpret_cast<float*>(smem + L::OFF_STG), (int)blockIdx.x, (int)gridDim.x,
-                        threadIdx.x);
+      // (16 x 32 x 9 FP32 over the staging boxes of all epilogue warps)
+      ffn_bias_grad<DT>(args.bias_grad, reinterpret_cast<float*>(smem + L::OFF_STG), (int)blockIdx.x, (int)gridDim.x);
     const int tiles0 = sched.count(0), tiles = tiles0 + (GATED ? 0 : sched.count(1));
     for (int ti = 0; ti < tiles; ++ti) {
       const int ji = ti < tiles0 ? 0 : 1, t = sched.tile(ji, ji == 0 ? ti : ti - tiles0);
@@ -675,7 +686,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         }
       };
 
-      const bool got = mbar_wait(bar_cfull(buf), buf_phase, abort_flag);
+      const bool got = mbar_wait_long(bar_cfull(buf), buf_phase, abort_flag);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after_sync();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kFfnMaxBN);

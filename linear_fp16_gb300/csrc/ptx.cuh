@@ -89,6 +89,30 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same for waits of microseconds by many warps: the suspend-time hint
+// (20 us) lets a warp sleep until the phase completes, instead of polling.
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_timer_ns();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (abort != nullptr && *abort) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      if (abort != nullptr) *abort = 1;
+      atomicOr(&g_device_error, kErrTimeout);
+      return false;
+    }
+  }
+}
+
 // ---- clusters (CTA pairs for the 2-SM MMA) --------------------------------
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
