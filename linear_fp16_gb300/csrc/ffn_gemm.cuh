@@ -12,7 +12,7 @@
 //              A = D_q [M,N] and B = x [M,K], both MN-major
 //
 // A persistent CTA (or a CTA pair on one 256-row tile, 2-SM MMA) per SM walks
-// output tiles.  Warp roles as in the linear's GEMM: eight epilogue warps, one
+// output tiles.  Warp roles as in the linear's GEMM: epilogue warps, one
 // thread that issues the MMAs, one that issues the TMA loads.  A sum stays
 // in TMEM over the whole K range (FP32 accumulators): unlike the linear's
 // kernel there is no promotion into registers every 1024 elements, because
@@ -44,10 +44,14 @@ enum FfnAct : int { kActSilu = 0, kActGeluTanh = 1, kActGeluErf = 2 };
 
 constexpr int kFfnBM = 128;
 constexpr int kFfnBK = 64;  // one 128-byte swizzle row
-constexpr int kFfnEpiWarps = 16;
-constexpr int kFfnMmaWarp = 16;
-constexpr int kFfnProdWarp = 17;
-constexpr int kFfnThreads = 18 * 32;
+// Epilogue warps; then the MMA issuer and the producer.  The gated kernel
+// takes eight with 168 registers and two staging boxes each, the gradients
+// sixteen with one
+// (GB300: gated 1417 x 520 x 1280 9.9 us with eight, 10.8 with sixteen, 4096 x
+// 4096 x 1024 with g and u 48.6 and 50.5; gradients 6 x 8320 x 470 29.8 and
+// 27.0, 112 x 4480 x 2531 61 and 55, 1024 x 1024 x 768 14.8 and 15.4).
+__host__ __device__ constexpr int ffn_epi_warps(bool gated) { return gated ? 8 : 16; }
+__host__ __device__ constexpr int ffn_threads(bool gated) { return (ffn_epi_warps(gated) + 2) * 32; }
 constexpr int kFfnMaxBN = 256;
 constexpr int kFfnMaxStages = 8;
 constexpr uint32_t kFfnTmemCols = 2 * kFfnMaxBN;
@@ -233,45 +237,46 @@ struct FfnGemmArgs {
   int bn;            // accumulator columns of a tile (gated: bn / 2 columns of h)
   int cols;          // output columns of a tile
   int stages;
-  int extra;         // see FfnSchedule
+  int first, extra;  // see FfnSchedule
   int act, save;
   const uint16_t* bias[2];  // gated: bg, bu or nullptr
 };
 
-// The tiles of one CTA (or pair): its round-robin share of job 0; then, where
-// job 0 leaves it one tile short of others, `extra` tiles of job 1 (as many
-// as take the time of a job 0 tile); then its round-robin share of the rest of
-// job 1.  count(job) tiles, the i-th is tile(job, i).
+// The tiles of one CTA (or pair): its round-robin share of the job with the
+// longer tiles (args.first); then, where that leaves it one tile short of
+// others, `extra` tiles of the other job (as many as take the time of one);
+// then its round-robin share of the rest of the other job.  count(job) tiles,
+// the i-th is tile(job, i).
 struct FfnSchedule {
-  int unit, units, t0, t1, r, extra, base;
+  int first, unit, units, t0, t1, r, extra, base;
   __device__ __forceinline__ FfnSchedule(const FfnGemmArgs& a, int unit_, int units_)
-      : unit(unit_), units(units_), t0(a.job[0].tiles), t1(a.job[1].tiles), r(a.job[0].tiles % units_) {
+      : first(a.first), unit(unit_), units(units_), t0(a.job[a.first].tiles), t1(a.job[1 - a.first].tiles), r(t0 % units_) {
     const bool is_short = r != 0 && unit >= r;
-    base = r != 0 ? a.extra * (units - r) : 0;  // tiles of job 1 handed out as extras
+    base = r != 0 ? a.extra * (units - r) : 0;  // tiles handed out as extras
     extra = is_short ? a.extra : 0;
     if (extra > 0) {  // those that exist
-      const int first = unit - r, step = units - r;
-      extra = first < t1 ? min(extra, (t1 - 1 - first) / step + 1) : 0;
+      const int start = unit - r, step = units - r;
+      extra = start < t1 ? min(extra, (t1 - 1 - start) / step + 1) : 0;
     }
   }
   __device__ __forceinline__ int count(int job) const {
-    if (job == 0) return unit < t0 ? (t0 - 1 - unit) / units + 1 : 0;
+    if (job == first) return unit < t0 ? (t0 - 1 - unit) / units + 1 : 0;
     return extra + (base + unit < t1 ? (t1 - 1 - base - unit) / units + 1 : 0);
   }
   __device__ __forceinline__ int tile(int job, int i) const {
-    if (job == 0) return i * units + unit;
+    if (job == first) return i * units + unit;
     return i < extra ? i * (units - r) + (unit - r) : base + (i - extra) * units + unit;
   }
 };
 
-// Shared memory: operand ring, then per epilogue warp a 2 KB staging box and
-// the biases of a tile's columns, then barriers.  Sixteen epilogue warps: with
-// eight the epilogue, not the products, set the time where K is short.
+// Shared memory: operand ring, then the epilogue warps' staging boxes and the
+// biases of a tile's columns, then barriers.
 struct FfnLayout {
   static constexpr int RING_BYTES = 192 * 1024;
   static constexpr int STG_BYTES = 32 * 32 * 2;
   static constexpr int OFF_STG = RING_BYTES;
-  static constexpr int OFF_BIAS = OFF_STG + kFfnEpiWarps * STG_BYTES;  // [accumulator][box][gate, up][32]
+  static constexpr int STG_BOXES = 16;  // 32 x 32 output boxes, shared out among the epilogue warps
+  static constexpr int OFF_BIAS = OFF_STG + STG_BOXES * STG_BYTES;  // [accumulator][box][gate, up][32]
   static constexpr int OFF_BAR = OFF_BIAS + 2 * 4 * 2 * 32 * 2;
   static constexpr int NUM_BARS = 2 * kFfnMaxStages + 5;  // full, empty, acc full x2, acc empty x2, drain
   static constexpr int OFF_TMEM_SLOT = OFF_BAR + NUM_BARS * 8;
@@ -323,8 +328,8 @@ __device__ __forceinline__ void ffn_load(bool mn, uint32_t dst, const CUtensorMa
   }
 }
 
-constexpr int kFfnEpiThreads = kFfnEpiWarps * 32;
-__device__ __forceinline__ void ffn_epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kFfnEpiThreads) : "memory"); }
+// the epilogue warps of a gradient kernel
+__device__ __forceinline__ void ffn_epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(ffn_epi_warps(false) * 32) : "memory"); }
 
 // Bias gradients by the epilogue warps of all CTAs: a CTA takes consecutive
 // groups of 8 columns (of all outputs, side by side), a lane every so-many-th
@@ -342,7 +347,8 @@ __device__ __forceinline__ void ffn_bias_grad(const FfnBiasGrad& b, float* red, 
     int width = 1;                               // lanes side by side on them
     while (width < n) width *= 2;
     const int g = lane & (width - 1);
-    const int step = kFfnEpiWarps * 32 / width;  // rows read at one time
+    constexpr int kWarps = ffn_epi_warps(false);
+    const int step = kWarps * 32 / width;  // rows read at one time
     const int o = (base + g) / per_out, c = ((base + g) - o * per_out) * 8, nc = min(8, b.N - c);
     float s[8];
 #pragma unroll
@@ -396,7 +402,7 @@ __device__ __forceinline__ void ffn_bias_grad(const FfnBiasGrad& b, float* red, 
       if (col < b.N && out != nullptr) {
         float t = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kFfnEpiWarps; ++w) t += red[(w * 32 + gg) * 9 + j];
+        for (int w = 0; w < kWarps; ++w) t += red[(w * 32 + gg) * 9 + j];
         out[col] = (uint16_t)ep_pack_t<DT>(t, 0.0f);
       }
     }
@@ -405,10 +411,12 @@ __device__ __forceinline__ void ffn_bias_grad(const FfnBiasGrad& b, float* red, 
 }
 
 template <int CL, bool GATED, int DT>
-__global__ void __launch_bounds__(kFfnThreads, 1)
+__global__ void __launch_bounds__(ffn_threads(GATED), 1)
     ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemmArgs args) {
   using L = FfnLayout;
   constexpr bool PAIR = CL == 2;
+  constexpr int EPI_WARPS = ffn_epi_warps(GATED), MMA_WARP = EPI_WARPS, PROD_WARP = EPI_WARPS + 1;
+  constexpr int STG = L::STG_BOXES / EPI_WARPS;  // staging boxes of a warp
   constexpr int SUB = ffn_sub(CL);
   constexpr int A_BYTES = ffn_a_bytes(CL);
   constexpr int A_SUB = A_BYTES / SUB;
@@ -457,13 +465,13 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(bar_cfull(a), 1u);
-      mbar_init(bar_cempty(a), (uint32_t)(CL * kFfnEpiWarps));
+      mbar_init(bar_cempty(a), (uint32_t)(CL * EPI_WARPS));
     }
     mbar_init(bar_drain, 1u);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kFfnMmaWarp) {
+  if (warp == MMA_WARP) {
     if constexpr (PAIR) {
       tmem_alloc_pair(smem_addr(tmem_slot), kFfnTmemCols);
       tmem_relinquish_alloc_permit_pair();
@@ -472,7 +480,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
       tmem_relinquish_alloc_permit();
     }
   }
-  if (warp == kFfnProdWarp && lane == 0 && args.job[0].tiles > 0) {
+  if (warp == PROD_WARP && lane == 0 && args.job[0].tiles > 0) {
     tma_prefetch_desc(&maps.a[0][0]);
     tma_prefetch_desc(&maps.b[0][0]);
   }
@@ -485,7 +493,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
   grid_dep_wait();
 
   const FfnSchedule sched(args, unit, units);
-  if (warp == kFfnProdWarp) {
+  if (warp == PROD_WARP) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       int stage = 0;
@@ -531,8 +539,13 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         }
       }
       };
-      load_job(std::integral_constant<int, 0>{});
-      if constexpr (!GATED) load_job(std::integral_constant<int, 1>{});
+      if (GATED || args.first == 0) {
+        load_job(std::integral_constant<int, 0>{});
+        if constexpr (!GATED) load_job(std::integral_constant<int, 1>{});
+      } else {
+        load_job(std::integral_constant<int, 1>{});
+        load_job(std::integral_constant<int, 0>{});
+      }
       // the last loads land before the CTA can exit (in a pair the odd CTA is
       // held by the closing cluster barrier)
       if (leader) {
@@ -545,7 +558,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == kFfnMmaWarp) {
+  } else if (warp == MMA_WARP) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && leader) {
       int stage = 0;
@@ -553,7 +566,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
       int buf = 0;
       uint32_t buf_phase = 0;
       bool ok = true;
-      // dx tiles, then dW tiles, each in a loop of their own whose operand
+      // dx tiles and dW tiles each have a loop of their own, whose operand
       // order and instruction descriptor are constants: with the order chosen
       // per tile the issuing thread leaves gaps in the tensor pipe (8192 x
       // 4096 x 14336, both gradients: 1073 us against 1006)
@@ -600,8 +613,13 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
           if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
         }
       };
-      issue_job(std::integral_constant<int, 0>{});
-      if constexpr (!GATED) issue_job(std::integral_constant<int, 1>{});
+      if (GATED || args.first == 0) {
+        issue_job(std::integral_constant<int, 0>{});
+        if constexpr (!GATED) issue_job(std::integral_constant<int, 1>{});
+      } else {
+        issue_job(std::integral_constant<int, 1>{});
+        issue_job(std::integral_constant<int, 0>{});
+      }
       // every MMA this thread issued has finished before TMEM is released
       if constexpr (PAIR) umma_commit_pair(bar_drain, 1);
       else umma_commit(bar_drain);
@@ -612,18 +630,18 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;   // TMEM lanes 32q .. 32q+31
     const int part = warp >> 2;
-    // this warp's 32-column boxes of a tile: part, part + 4, ...
+    // this warp's 32-column boxes of a tile: part, part + EPI_WARPS / 4, ...
     const int boxes = args.cols / 32;
-    uint8_t* stg = smem + L::OFF_STG + warp * L::STG_BYTES;
-    const uint32_t stg_addr = sbase + L::OFF_STG + warp * L::STG_BYTES;
+    uint8_t* const stg0 = smem + L::OFF_STG + warp * STG * L::STG_BYTES;
+    int sbox = 0;  // staging box to fill next
     int buf = 0;
     uint32_t buf_phase = 0;
     if (!GATED && args.bias_grad.outputs > 0)
       // (16 x 32 x 9 FP32 over the staging boxes of all epilogue warps)
       ffn_bias_grad<DT>(args.bias_grad, reinterpret_cast<float*>(smem + L::OFF_STG), (int)blockIdx.x, (int)gridDim.x);
-    const int tiles0 = sched.count(0), tiles = tiles0 + (GATED ? 0 : sched.count(1));
+    const int tiles0 = sched.count(sched.first), tiles = tiles0 + (GATED ? 0 : sched.count(1 - sched.first));
     for (int ti = 0; ti < tiles; ++ti) {
-      const int ji = ti < tiles0 ? 0 : 1, t = sched.tile(ji, ji == 0 ? ti : ti - tiles0);
+      const int ji = ti < tiles0 ? sched.first : 1 - sched.first, t = sched.tile(ji, ti < tiles0 ? ti : ti - tiles0);
       const FfnJob& job = args.job[ji];
       const int M = job.M, N = job.N;
       int s, g, mb, nb;
@@ -634,8 +652,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
       // 16 packed pairs value(0) .. value(15), through the staging box: 64
       // bytes a row, chunk j at j ^ ((row >> 1) & 3) (TMA's 64-byte swizzle).
       auto store_box = [&](int o, int nc, auto&& value) {
-        if (lane == 0) bulk_wait_group_read<0>();
+        if (lane == 0) bulk_wait_group_read<STG - 1>();  // the box's last store has read it
         __syncwarp();
+        uint8_t* const stg = stg0 + sbox * L::STG_BYTES;
+        sbox = sbox + 1 == STG ? 0 : sbox + 1;
         uint8_t* rowp = stg + lane * 64;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -645,7 +665,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&maps.y[ji][o], stg_addr, nc, m0);
+            tma_store_2d(&maps.y[ji][o], smem_addr(stg), nc, m0);
             bulk_commit_group();
           }
         } else {
@@ -669,8 +689,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
       auto store_partial = [&](const uint32_t (&r)[32], int slab, int nc) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (lane == 0) bulk_wait_group_read<0>();
+          if (lane == 0) bulk_wait_group_read<STG - 1>();
           __syncwarp();
+          uint8_t* const stg = stg0 + sbox * L::STG_BYTES;
+          sbox = sbox + 1 == STG ? 0 : sbox + 1;
           uint8_t* rowp = stg + lane * 64;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -680,7 +702,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d(&maps.partial[ji], stg_addr, nc + 16 * h, m0, slab);
+            tma_store_3d(&maps.partial[ji], smem_addr(stg), nc + 16 * h, m0, slab);
             bulk_commit_group();
           }
         }
@@ -692,7 +714,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kFfnMaxBN);
       const bool rows_in = m0 < M;  // warp-uniform
 #pragma unroll 1
-      for (int bx = part; bx < boxes; bx += 4) {
+      for (int bx = part; bx < boxes; bx += EPI_WARPS / 4) {
         const int nc = n0 + bx * 32;
         if (nc >= N || !rows_in) break;  // warp-uniform: nothing of the box is in the output
         uint32_t r[32];
@@ -701,8 +723,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
           uint32_t r2[32];
           tmem_ld_32x32b_x32(taddr + (uint32_t)(BN / 2 + bx * 32), r2);
           const bool biased = args.bias[0] != nullptr || args.bias[1] != nullptr;
-          uint16_t* const sbias = reinterpret_cast<uint16_t*>(smem + L::OFF_BIAS) + (buf * 4 + part) * 64;
-          static_assert(kFfnMaxBN / 2 / 32 <= 4, "a warp has one box of a gated tile");
+          uint16_t* const sbias = reinterpret_cast<uint16_t*>(smem + L::OFF_BIAS) + (buf * 4 + bx) * 64;
           if (biased && job.split == 1) {
             // lane l fetches the biases of column nc + l.  The four warps of a
             // box write the same values; the slot is this accumulator's, and
@@ -767,7 +788,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   if constexpr (PAIR) cluster_sync();
-  if (warp == kFfnMmaWarp) {
+  if (warp == MMA_WARP) {
     tc_fence_after_sync();
     if constexpr (PAIR) tmem_dealloc_pair(tmem_base, kFfnTmemCols);
     else tmem_dealloc(tmem_base, kFfnTmemCols);

@@ -207,6 +207,18 @@ struct FfnShape {
 };
 constexpr FfnShape kFfnShapes[] = {{2, 256, 0.264}, {2, 128, 0.244}, {1, 256, 0.335}, {1, 128, 0.281}, {1, 64, 0.236}};
 
+inline const FfnShape& shape_of(const FfnPlan& p) {
+  for (const FfnShape& s : kFfnShapes)
+    if (s.cl == p.cl && s.bn == p.bn) return s;
+  return kFfnShapes[0];
+}
+
+// Time of a tile of `kb` 64-element K blocks among others of its kind: its
+// products, or its share of HBM for 128 rows of output.
+inline double tile_time(const FfnShape& s, int64_t kb, int64_t cols) {
+  return std::max(double(kb) * s.per_kb + 0.23, double(cols) * 128 * 2 / 39.5e3);
+}
+
 double plan_time(const FfnProduct* const* ps, int count, const FfnShape& s, const int* split, int sms, double bytes) {
   const int64_t slots = sms / s.cl;
   int64_t tiles[2] = {0, 0}, kbs[2] = {1, 1};
@@ -228,11 +240,14 @@ double plan_time(const FfnProduct* const* ps, int count, const FfnShape& s, cons
   if (count < 2) {
     t = double(ceil_div(tiles[0], slots)) * tile[0];
   } else {
-    const int64_t r = tiles[0] % slots, extra = r != 0 ? (2 * kbs[0] + kbs[1]) / (2 * kbs[1]) : 0;
-    const int64_t common = ceil_div(std::max<int64_t>(0, tiles[1] - extra * (slots - r)), slots);
-    const int64_t taken = r != 0 ? std::min(extra, ceil_div(tiles[1], slots - r)) : 0;
-    t = std::max(double(ceil_div(tiles[0], slots)) * tile[0], double(tiles[0] / slots) * tile[0] + double(taken) * tile[1]) +
-        double(common) * tile[1];
+    double dealt[2];
+    for (int i = 0; i < 2; ++i) dealt[i] = tile_time(s, kbs[i] * s.cl, s.bn);
+    const int f = dealt[1] > dealt[0] ? 1 : 0, o = 1 - f;
+    const int64_t r = tiles[f] % slots, extra = r != 0 ? static_cast<int64_t>(dealt[f] / dealt[o] + 0.5) : 0;
+    const int64_t common = ceil_div(std::max<int64_t>(0, tiles[o] - extra * (slots - r)), slots);
+    const int64_t taken = r != 0 ? std::min(extra, ceil_div(tiles[o], slots - r)) : 0;
+    t = std::max(double(ceil_div(tiles[f], slots)) * tile[f], double(tiles[f] / slots) * tile[f] + double(taken) * tile[o]) +
+        double(common) * tile[o];
   }
   return std::max(t + last, bytes / 5.95e6) + added;
 }
@@ -282,7 +297,7 @@ struct FfnEpilogue {
 template <int CL, bool GATED>
 cudaError_t launch_ffn(const FfnMaps& m, const FfnGemmArgs& a, bool bf16, int64_t units, cudaStream_t stream) {
   return launch_clustered(bf16 ? ffn_gemm_kernel<CL, GATED, kEpiBf16> : ffn_gemm_kernel<CL, GATED, kEpiF16>,
-                          dim3(static_cast<unsigned>(units * CL)), dim3(kFfnThreads), FfnLayout::DYN_BYTES, stream,
+                          dim3(static_cast<unsigned>(units * CL)), dim3(ffn_threads(GATED)), FfnLayout::DYN_BYTES, stream,
                           unsigned(CL), m, a);
 }
 
@@ -360,7 +375,14 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
     j.tiles_per_out = 1;
     j.split = 1;
   }
-  if (count == 2) a.extra = (2 * a.job[0].kb_split + a.job[1].kb_split) / (2 * a.job[1].kb_split);
+  if (count == 2) {
+    double t[2];
+    for (int i = 0; i < 2; ++i) t[i] = tile_time(shape_of(p), int64_t(a.job[i].kb_split) * p.cl, a.cols);
+    a.first = t[1] > t[0] ? 1 : 0;
+    a.extra = static_cast<int>(t[a.first] / t[1 - a.first] + 0.5);
+  } else if (count == 1) {
+    a.first = ps[0]->mn_a ? 1 : 0;
+  }
   // without bias gradients no more CTAs than tiles
   const int64_t units = a.bias_grad.outputs > 0 ? units_max : std::min<int64_t>(total, units_max);
   const bool pair = p.cl == 2;
