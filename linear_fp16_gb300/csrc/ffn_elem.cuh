@@ -39,16 +39,16 @@ __device__ __forceinline__ void ffn_pack_rows(const FfnPackArgs& a, int block, i
       const int c0 = (int)(i - r * spans) * kPackSpan + lane * 8;
       const uint16_t* s = a.src[t] + r * a.ld[t];
       uint16_t* d = a.dst[t] + r * a.ldd[t];
-      uint4 v[4];
+      if (c0 + 3 * 256 + 8 <= a.cols[t] && ffn_wide_ok(s + c0, lo, hi) && ffn_wide_ok(s + c0 + 3 * 256, lo, hi)) {
+        FfnPair v[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = c0 + j * 256;
-        if (c < a.cols[t]) v[j] = ffn_load8_any(s + c, a.cols[t] - c, lo, hi);
-      }
+        for (int j = 0; j < 4; ++j) v[j] = ffn_wide_load(s + c0 + j * 256);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = c0 + j * 256;
-        if (c < a.cols[t]) *reinterpret_cast<uint4*>(d + c) = v[j];
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(d + c0 + j * 256) = ffn_wide_shift(s + c0 + j * 256, v[j]);
+      } else {
+        for (int c = c0; c < min(a.cols[t], c0 + kPackSpan); c += 256)
+          *reinterpret_cast<uint4*>(d + c) = ffn_load8_any(s + c, a.cols[t] - c, lo, hi);
       }
     }
     skip = (skip + units) % warps;
@@ -104,6 +104,11 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const __grid_co
   auto load = [&](const uint16_t* p, const uint16_t* lo, const uint16_t* hi) {
     return VEC ? ldg_stream_16(p) : ffn_load8_any(p, n, lo, hi);
   };
+  // rows no pair of vectors of which leaves the matrices
+  auto wide = [&](long long row) {
+    return n == 8 && ffn_wide_ok(a.dh + row * a.ld_dh + c, a.dh, eh) && ffn_wide_ok(a.g + row * a.ld_g + c, a.g, eg) &&
+           ffn_wide_ok(a.u + row * a.ld_u + c, a.u, eu);
+  };
   auto grad = [&](auto act, const uint4& vh, const uint4& vg, const uint4& vu, long long row) {
     float dh[8], g[8], u[8], dg[8], du[8];
     ffn_unpack8<DT>(vh, dh);
@@ -128,6 +133,14 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const __grid_co
     for (long long row = (long long)rb * a.rows + warp; row < row_end; row += 16) {
       const bool two = row + 8 < row_end;
       const uint16_t *ph = a.dh + row * a.ld_dh + c, *pg = a.g + row * a.ld_g + c, *pu = a.u + row * a.ld_u + c;
+      if (!VEC && two && wide(row) && wide(row + 8)) {
+        const uint16_t *qh = ph + 8 * a.ld_dh, *qg = pg + 8 * a.ld_g, *qu = pu + 8 * a.ld_u;
+        const FfnPair h0 = ffn_wide_load(ph), g0 = ffn_wide_load(pg), u0 = ffn_wide_load(pu);
+        const FfnPair h1 = ffn_wide_load(qh), g1 = ffn_wide_load(qg), u1 = ffn_wide_load(qu);
+        grad(act, ffn_wide_shift(ph, h0), ffn_wide_shift(pg, g0), ffn_wide_shift(pu, u0), row);
+        grad(act, ffn_wide_shift(qh, h1), ffn_wide_shift(qg, g1), ffn_wide_shift(qu, u1), row + 8);
+        continue;
+      }
       const uint4 h0 = load(ph, a.dh, eh), g0 = load(pg, a.g, eg), u0 = load(pu, a.u, eu);
       uint4 h1 = make_uint4(0, 0, 0, 0), g1 = h1, u1 = h1;
       if (two) {

@@ -67,31 +67,36 @@ __device__ __forceinline__ uint4 ffn_load8(const uint16_t* __restrict__ p, int n
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The same for rows that no wide load fits, where [lo, hi) is the memory the
-// matrix spans: the two 16-byte vectors around p, shifted into place, where
-// both lie inside that memory; element loads at its ends.  (Eight 2-byte
-// loads a lane made the copies below bound by their number.)
-__device__ __forceinline__ uint4 ffn_load8_any(const uint16_t* __restrict__ p, int n, const void* lo, const void* hi) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), a0 = a & ~uintptr_t(15);
-  if (n < 8 || a0 < reinterpret_cast<uintptr_t>(lo) || a0 + 32 > reinterpret_cast<uintptr_t>(hi)) return ffn_load8(p, n);
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(a0));
-  const uint32_t sh = (uint32_t)(a - a0);
-  if (sh == 0) return u;
-  const uint4 v = __ldg(reinterpret_cast<const uint4*>(a0) + 1);
-  uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-  if (sh & 8u) {
+// Rows that no wide load fits: the two 16-byte vectors around p, shifted into
+// place, where both lie inside the memory [lo, hi) that the matrix spans.
+// (Eight 2-byte loads a lane made such kernels bound by their number.)  In
+// three steps, so that a caller has several pairs on their way at a time.
+__device__ __forceinline__ bool ffn_wide_ok(const uint16_t* p, const void* lo, const void* hi) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
+  return a0 >= reinterpret_cast<uintptr_t>(lo) && a0 + 32 <= reinterpret_cast<uintptr_t>(hi);
+}
+struct FfnPair {
+  uint4 u, v;
+};
+__device__ __forceinline__ FfnPair ffn_wide_load(const uint16_t* p) {
+  const uint4* a0 = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
+  return {__ldg(a0), __ldg(a0 + 1)};
+}
+__device__ __forceinline__ uint4 ffn_wide_shift(const uint16_t* p, const FfnPair& r) {
+  const uint32_t sh = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+  uint32_t w[8] = {r.u.x, r.u.y, r.u.z, r.u.w, r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  }
-  if (sh & 4u) {
+  for (int i = 0; i < 6; ++i) w[i] = (sh & 8u) ? w[i + 2] : w[i];
 #pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  }
-  if (sh & 2u) {
+  for (int i = 0; i < 5; ++i) w[i] = (sh & 4u) ? w[i + 1] : w[i];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-  }
+  for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (sh & 2u) << 3);
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// eight elements p[0 .. n) at any alignment, the rest zero
+__device__ __forceinline__ uint4 ffn_load8_any(const uint16_t* __restrict__ p, int n, const void* lo, const void* hi) {
+  if (n < 8 || !ffn_wide_ok(p, lo, hi)) return ffn_load8(p, n);
+  return ffn_wide_shift(p, ffn_wide_load(p));
 }
 
 template <int DT>

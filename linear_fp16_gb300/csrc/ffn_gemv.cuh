@@ -241,21 +241,60 @@ __global__ void __launch_bounds__(WARPS * 32) gated_gemv_any_kernel(const GatedG
 #pragma unroll
     for (int i = 0; i < 4; ++i) dg[q][i] = du[q][i] = 0.0f;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  constexpr int U = NT == 1 ? 4 : 2;  // steps of 32 along K in flight
+  constexpr int U = 2;  // steps of 32 along K in flight
   for (int k0 = k_begin; k0 < k_end; k0 += 32 * U) {
     uint4 vga[U], vgb[U], vua[U], vub[U], vx[U][NT];
+    const int kf = k0 + 8 * t, kl = kf + 32 * (U - 1);  // this lane's first and last vector
+    if (okB && kl + 8 <= k_end && ffn_wide_ok(gA + kf, a.wg, ge) && ffn_wide_ok(gB + kl, a.wg, ge) &&
+        ffn_wide_ok(uA + kf, a.wu, ue) && ffn_wide_ok(uB + kl, a.wu, ue)) {
+      FfnPair p[U][4];
 #pragma unroll
-    for (int s = 0; s < U; ++s) {
-      const int k = k0 + 32 * s + 8 * t;
-      const int n = k_end - k;
-      const bool in = n > 0;
-      vga[s] = in && okA ? ffn_load8_any(gA + k, n, a.wg, ge) : zero;
-      vgb[s] = in && okB ? ffn_load8_any(gB + k, n, a.wg, ge) : zero;
-      vua[s] = in && okA ? ffn_load8_any(uA + k, n, a.wu, ue) : zero;
-      vub[s] = in && okB ? ffn_load8_any(uB + k, n, a.wu, ue) : zero;
-      vx[s][0] = in && okx0 ? ffn_load8_any(x0 + k, n, a.x, xe) : zero;
-      if (NT > 1)
-        vx[s][NT - 1] = in && okx1 ? ffn_load8_any(x1 + k, n, a.x, xe) : zero;
+      for (int s = 0; s < U; ++s) {
+        const int k = kf + 32 * s;
+        p[s][0] = ffn_wide_load(gA + k);
+        p[s][1] = ffn_wide_load(gB + k);
+        p[s][2] = ffn_wide_load(uA + k);
+        p[s][3] = ffn_wide_load(uB + k);
+      }
+#pragma unroll
+      for (int s = 0; s < U; ++s) {
+        const int k = kf + 32 * s;
+        vga[s] = ffn_wide_shift(gA + k, p[s][0]);
+        vgb[s] = ffn_wide_shift(gB + k, p[s][1]);
+        vua[s] = ffn_wide_shift(uA + k, p[s][2]);
+        vub[s] = ffn_wide_shift(uB + k, p[s][3]);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < U; ++s) {
+        const int k = kf + 32 * s, n = k_end - k;
+        vga[s] = n > 0 && okA ? ffn_load8(gA + k, n) : zero;
+        vgb[s] = n > 0 && okB ? ffn_load8(gB + k, n) : zero;
+        vua[s] = n > 0 && okA ? ffn_load8(uA + k, n) : zero;
+        vub[s] = n > 0 && okB ? ffn_load8(uB + k, n) : zero;
+      }
+    }
+    // (rows of x that are not there read the first one's, and give zeros)
+    if (kl + 8 <= k_end && ffn_wide_ok(x0 + kf, a.x, xe) && ffn_wide_ok(x0 + kl, a.x, xe) &&
+        (NT == 1 || (ffn_wide_ok(x1 + kf, a.x, xe) && ffn_wide_ok(x1 + kl, a.x, xe)))) {
+      FfnPair p[U][NT];
+#pragma unroll
+      for (int s = 0; s < U; ++s) {
+        p[s][0] = ffn_wide_load(x0 + kf + 32 * s);
+        if (NT > 1) p[s][NT - 1] = ffn_wide_load(x1 + kf + 32 * s);
+      }
+#pragma unroll
+      for (int s = 0; s < U; ++s) {
+        vx[s][0] = okx0 ? ffn_wide_shift(x0 + kf + 32 * s, p[s][0]) : zero;
+        if (NT > 1) vx[s][NT - 1] = okx1 ? ffn_wide_shift(x1 + kf + 32 * s, p[s][NT - 1]) : zero;
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < U; ++s) {
+        const int k = kf + 32 * s, n = k_end - k;
+        vx[s][0] = n > 0 && okx0 ? ffn_load8(x0 + k, n) : zero;
+        if (NT > 1) vx[s][NT - 1] = n > 0 && okx1 ? ffn_load8(x1 + k, n) : zero;
+      }
     }
 #pragma unroll
     for (int s = 0; s < U; ++s) {
