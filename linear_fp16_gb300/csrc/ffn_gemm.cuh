@@ -44,14 +44,15 @@ enum FfnAct : int { kActSilu = 0, kActGeluTanh = 1, kActGeluErf = 2 };
 
 constexpr int kFfnBM = 128;
 constexpr int kFfnBK = 64;  // one 128-byte swizzle row
-// Epilogue warps; then the MMA issuer and the producer.  The gated kernel
+// Epilogue warps; then the MMA issuer and two producers, one per operand (one
+// thread issuing both took 0.3 us a stage where the MMAs take 0.27).  The gated kernel
 // takes eight with 168 registers and two staging boxes each, the gradients
 // sixteen with one
 // (GB300: gated 1417 x 520 x 1280 9.9 us with eight, 10.8 with sixteen, 4096 x
 // 4096 x 1024 with g and u 48.6 and 50.5; gradients 6 x 8320 x 470 29.8 and
 // 27.0, 112 x 4480 x 2531 61 and 55, 1024 x 1024 x 768 14.8 and 15.4).
 __host__ __device__ constexpr int ffn_epi_warps(bool gated) { return gated ? 8 : 16; }
-__host__ __device__ constexpr int ffn_threads(bool gated) { return (ffn_epi_warps(gated) + 2) * 32; }
+__host__ __device__ constexpr int ffn_threads(bool gated) { return (ffn_epi_warps(gated) + (gated ? 3 : 2)) * 32; }
 constexpr int kFfnMaxBN = 256;
 constexpr int kFfnMaxStages = 8;
 constexpr uint32_t kFfnTmemCols = 2 * kFfnMaxBN;
@@ -189,34 +190,52 @@ __device__ __forceinline__ void act_both_t(float t, float& v, float& d) {
   }
 }
 
-// Tile index -> (M block, N block): groups of group_m M blocks walked column
-// by column, odd groups from the far end, so that CTAs running together share
-// rows of both operands in L2.
-__device__ __forceinline__ void ffn_tile_coords(int t, int num_m, int num_n, int group_m, int& mb, int& nb) {
-  const int span = group_m * num_n;
-  const int g = t / span;
-  const int first_m = g * group_m;
-  const int gsize = min(num_m - first_m, group_m);
-  const int local = t - g * span;
-  mb = first_m + local % gsize;
-  nb = local / gsize;
-  if (g & 1) nb = num_n - 1 - nb;
-}
+// Division of n < 2^31 by a divisor known on the host (Granlund and Montgomery,
+// "Division by invariant integers using multiplication"): a tile's
+// coordinates take six, and the first tile's stand before its first load.
+struct FfnDiv {
+  uint32_t d = 1, mul = 1, shift = 0;
+  FfnDiv() = default;
+  explicit FfnDiv(uint32_t d_) : d(d_) {
+    while ((uint64_t(1) << shift) < d) ++shift;
+    mul = static_cast<uint32_t>((((uint64_t(1) << shift) - d) << 32) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
 
 // One family of tiles: the products of one kind, with their operands.
 // gated: a[0] = x, b = Wg, Wu, y = h, g, u.  dx: a = D_p, b = W_p, y[0] = dx.
 // dW: a = D_q, b[0] = x, y = dW_q.
 struct FfnJob {
-  int M, N;          // rows and columns of one output (gated: of h)
-  int parts;         // products added into one sum
-  int num_m, num_n, group_m, tiles_per_out, tiles;
+  // the first tile's load needs these
+  int tiles_per_out, split, group_m, num_n, num_m;
   int kb_part;       // K blocks (SUB * 64 elements) of one part
   int kb_total;      // over all parts
-  int split;         // K ranges (tiles of their own), 1: none
-  int kb_split;      // K blocks of a range (the last may be shorter)
+  int kb_split;      // K blocks of a range (the last may be shorter); split ranges, tiles of their own
+  FfnDiv by_out, by_split, by_span, by_group, by_rest;  // tiles_per_out, split, group_m num_n, group_m, the last group's
+  // the epilogue these
+  int M, N;          // rows and columns of one output (gated: of h)
+  int tiles;
   int tma_store;     // outputs stored by TMA; 0: plain stores
   uint16_t* y[3];    // row pitch N
-  float* partial;    // split > 1: FP32 sums [outputs][split][M][N rounded up to 4] (gated: gate, up)
+};
+
+// tile t -> (K range, output, M block, N block).  Groups of group_m M blocks
+// are walked column by column, odd groups from the far end, so that CTAs
+// running together share rows of both operands in L2.
+struct FfnTile {
+  int s, g, mb, nb;
+  __device__ __forceinline__ FfnTile(const FfnJob& j, uint32_t t) {
+    const uint32_t q = j.by_out.div(t), tl = t - q * (uint32_t)j.tiles_per_out;
+    g = (int)j.by_split.div(q);
+    s = (int)q - g * j.split;
+    const int span = j.group_m * j.num_n, group = (int)j.by_span.div(tl), first_m = group * j.group_m;
+    const uint32_t local = tl - (uint32_t)(group * span);
+    const bool rest = j.num_m - first_m < j.group_m;
+    nb = (int)(rest ? j.by_rest.div(local) : j.by_group.div(local));
+    mb = first_m + (int)local - nb * (rest ? j.num_m - first_m : j.group_m);
+    if (group & 1) nb = j.num_n - 1 - nb;
+  }
 };
 
 struct FfnMaps {
@@ -236,38 +255,45 @@ struct FfnBiasGrad {
   uint16_t* out[2];    // either may be nullptr
 };
 
+struct FfnDeal {     // see FfnSchedule
+  int first;         // the job with the longer tiles
+  int rounds, rest;  // its tiles: full rounds over all CTAs (pairs), and what is left
+  int extra, base;   // tiles of the other job dealt to CTAs it leaves short: each, all
+  int rounds1, rest1;  // the other job's tiles after those
+  int tiles1;        // the other job's tiles
+};
+
+// (a kernel's first reads of its arguments miss every cache: what the first
+// tile needs stands together)
 struct FfnGemmArgs {
-  FfnJob job[2];     // gated: job 0; gradients: dx, dW (either may have no tiles)
-  FfnBiasGrad bias_grad;
+  FfnDeal deal;
   int bn;            // accumulator columns of a tile (gated: bn / 2 columns of h)
   int cols;          // output columns of a tile
   int stages;
-  int first, extra;  // see FfnSchedule
   int act, save;
+  FfnJob job[2];     // gated: job 0; gradients: dx, dW (either may have no tiles)
   const uint16_t* bias[2];  // gated: bg, bu or nullptr
+  FfnBiasGrad bias_grad;
 };
 
 // The tiles of one CTA (or pair): its round-robin share of the job with the
-// longer tiles (args.first); then, where that leaves it one tile short of
+// longer tiles (deal.first); then, where that leaves it one tile short of
 // others, `extra` tiles of the other job (as many as take the time of one);
 // then its round-robin share of the rest of the other job.  count(job) tiles,
 // the i-th is tile(job, i).
 struct FfnSchedule {
-  int first, unit, units, t0, t1, r, extra, base;
-  __device__ __forceinline__ FfnSchedule(const FfnGemmArgs& a, int unit_, int units_)
-      : first(a.first), unit(unit_), units(units_), t0(a.job[a.first].tiles), t1(a.job[1 - a.first].tiles), r(t0 % units_) {
-    const bool is_short = r != 0 && unit >= r;
-    base = r != 0 ? a.extra * (units - r) : 0;  // tiles handed out as extras
-    extra = is_short ? a.extra : 0;
-    if (extra > 0) {  // those that exist
+  int first, unit, units, r, extra, base, n0, n1;
+  __device__ __forceinline__ FfnSchedule(const FfnDeal& d, int unit_, int units_)
+      : first(d.first), unit(unit_), units(units_), r(d.rest), extra(0), base(d.base) {
+    if (r != 0 && unit >= r && d.extra > 0) {  // those that exist
       const int start = unit - r, step = units - r;
-      extra = start < t1 ? min(extra, (t1 - 1 - start) / step + 1) : 0;
+      extra = d.extra;
+      if (start + (extra - 1) * step >= d.tiles1) extra = start < d.tiles1 ? (d.tiles1 - 1 - start) / step + 1 : 0;
     }
+    n0 = d.rounds + (unit < r ? 1 : 0);
+    n1 = extra + d.rounds1 + (unit < d.rest1 ? 1 : 0);
   }
-  __device__ __forceinline__ int count(int job) const {
-    if (job == first) return unit < t0 ? (t0 - 1 - unit) / units + 1 : 0;
-    return extra + (base + unit < t1 ? (t1 - 1 - base - unit) / units + 1 : 0);
-  }
+  __device__ __forceinline__ int count(int job) const { return job == first ? n0 : n1; }
   __device__ __forceinline__ int tile(int job, int i) const {
     if (job == first) return i * units + unit;
     return i < extra ? i * (units - r) + (unit - r) : base + (i - extra) * units + unit;
@@ -420,7 +446,7 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
     ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemmArgs args) {
   using L = FfnLayout;
   constexpr bool PAIR = CL == 2;
-  constexpr int EPI_WARPS = ffn_epi_warps(GATED), MMA_WARP = EPI_WARPS, PROD_WARP = EPI_WARPS + 1;
+  constexpr int EPI_WARPS = ffn_epi_warps(GATED), MMA_WARP = EPI_WARPS, PROD_WARP = EPI_WARPS + 1;  // A's; then B's
   constexpr int STG = L::STG_BOXES / EPI_WARPS;  // staging boxes of a warp
   constexpr int SUB = ffn_sub(CL);
   constexpr int A_BYTES = ffn_a_bytes(CL);
@@ -436,14 +462,6 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
   const int unit = (int)(blockIdx.x / CL);
   const int units = (int)(gridDim.x / CL);
   const int tile_rows = CL * kFfnBM;
-
-  // tile t -> (K range, output, M block, N block)
-  auto tile_decode = [](const FfnJob& j, int t, int& s, int& g, int& mb, int& nb) {
-    const int q = t / j.tiles_per_out;
-    s = q % j.split;
-    g = q / j.split;
-    ffn_tile_coords(t - q * j.tiles_per_out, j.num_m, j.num_n, j.group_m, mb, nb);
-  };
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -485,72 +503,79 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
       tmem_relinquish_alloc_permit();
     }
   }
-  if (warp == PROD_WARP && lane == 0 && args.job[0].tiles > 0) {
-    tma_prefetch_desc(&maps.a[0][0]);
-    tma_prefetch_desc(&maps.b[0][0]);
-  }
   grid_dep_launch();
   tc_fence_before_sync();
   __syncthreads();
   if constexpr (PAIR) cluster_sync();  // both CTAs' barriers exist before any remote signal
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
-  grid_dep_wait();
 
-  const FfnSchedule sched(args, unit, units);
-  if (warp == PROD_WARP) {
+  // Each role waits for the previous grid itself, just before it touches
+  // global memory: the schedule and the first tile's coordinates (reads of
+  // arguments that miss every cache) are then done by the time it ends.
+  // (Prefetching the tensor maps in the prologue made it 1 us longer.)
+  const FfnSchedule sched(args.deal, unit, units);
+  if (warp >= PROD_WARP) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
       long long issued = 0;
       bool ok = true;
-      // JI: 0 dx (or the gated block), 1 dW
-      auto load_job = [&](auto ji_tag) {
-      constexpr int ji = decltype(ji_tag)::value;
-      constexpr bool mn_a = !GATED && ji == 1;
-      const FfnJob& job = args.job[ji];
-      const int tiles = sched.count(ji);
-      for (int ti = 0; ti < tiles && ok; ++ti) {
-        int s, g, mb, nb;
-        tile_decode(job, sched.tile(ji, ti), s, g, mb, nb);
-        const int kb0 = s * job.kb_split, kb1 = min(job.kb_total, kb0 + job.kb_split);
-        const int arow = mb * tile_rows + (int)rank * kFfnBM;
-        const int brow = nb * args.cols + (GATED ? 0 : (int)rank * (BN / CL));
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (issued >= STAGES && !mbar_wait(bar_empty(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
-          const uint32_t fb = bar_full(stage);
-          const uint32_t fbl = PAIR ? map_to_cta(fb, 0u) : fb;  // both CTAs' bytes complete on the even CTA's barrier
-          if (leader) mbar_arrive_expect_tx(fb, (uint32_t)(CL * STAGE_BYTES));
-          const int part = kb >= job.kb_part ? 1 : 0;  // (one part: kb never gets there)
-          const int kc = (kb - part * job.kb_part) * (SUB * kFfnBK);
-          const CUtensorMap* ma = &maps.a[ji][GATED ? 0 : (mn_a ? g : part)];
-          const CUtensorMap* mbp = &maps.b[ji][GATED ? (PAIR ? (int)rank : 0) : (mn_a ? 0 : part)];
+      // JI: 0 dx (or the gated block), 1 dW.  A's producer arms the stage's
+      // barrier for both operands' bytes; B's may land before that (the
+      // phase stays open until the arrival).
+      auto load_job = [&](auto ji_tag, auto op_tag) {
+        constexpr int ji = decltype(ji_tag)::value;
+        constexpr bool IS_A = (decltype(op_tag)::value & 1) != 0, IS_B = (decltype(op_tag)::value & 2) != 0;
+        const FfnJob& job = args.job[ji];
+        const int tiles = sched.count(ji);
+        for (int ti = 0; ti < tiles && ok; ++ti) {
+          const FfnTile tile(job, (uint32_t)sched.tile(ji, ti));
+          const int kb0 = tile.s * job.kb_split, kb1 = min(job.kb_total, kb0 + job.kb_split);
+          const int arow = tile.mb * tile_rows + (int)rank * kFfnBM;
+          const int brow = tile.nb * args.cols + (GATED ? 0 : (int)rank * (BN / CL));
+          for (int kb = kb0; kb < kb1; ++kb) {
+            if (issued == 0) grid_dep_wait();
+            if (issued >= STAGES && !mbar_wait(bar_empty(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
+            const uint32_t fb = bar_full(stage);
+            const uint32_t fbl = PAIR ? map_to_cta(fb, 0u) : fb;  // both CTAs' bytes complete on the even CTA's barrier
+            if (IS_A && leader) mbar_arrive_expect_tx(fb, (uint32_t)(CL * STAGE_BYTES));
+            const int part = kb >= job.kb_part ? 1 : 0;  // (one part: kb never gets there)
+            const int kc = (kb - part * job.kb_part) * (SUB * kFfnBK);
 #pragma unroll
-          for (int h = 0; h < SUB; ++h) {
-            const uint32_t da = stage_a(stage) + (uint32_t)(h * A_SUB), db = stage_b(stage) + (uint32_t)(h * B_SUB);
-            const int k0 = kc + h * kFfnBK;
-            ffn_load<CL>(mn_a, da, ma, fbl, arow, kFfnBM, k0);
-            if constexpr (GATED) {
-              ffn_load<CL>(false, db, mbp, fbl, brow, BN / 2, k0);
-              if constexpr (!PAIR)
-                ffn_load<CL>(false, db + (uint32_t)(BN / 2) * 128u, &maps.b[0][1], fbl, brow, BN / 2, k0);
-            } else {
-              ffn_load<CL>(true, db, mbp, fbl, brow, BN / CL, k0);
+            for (int h = 0; h < SUB; ++h) {
+              const int k0 = kc + h * kFfnBK;
+              if constexpr (IS_A)
+                ffn_load<CL>(!GATED && ji == 1, stage_a(stage) + (uint32_t)(h * A_SUB),
+                             &maps.a[ji][GATED ? 0 : (ji == 1 ? tile.g : part)], fbl, arow, kFfnBM, k0);
+              if constexpr (IS_B) {
+                const uint32_t db = stage_b(stage) + (uint32_t)(h * B_SUB);
+                ffn_load<CL>(!GATED, db, &maps.b[ji][GATED ? (PAIR ? (int)rank : 0) : (ji == 1 ? 0 : part)], fbl, brow,
+                             GATED ? BN / 2 : BN / CL, k0);
+                if constexpr (GATED && !PAIR)
+                  ffn_load<CL>(false, db + (uint32_t)(BN / 2) * 128u, &maps.b[0][1], fbl, brow, BN / 2, k0);
+              }
             }
+            ++issued;
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           }
-          ++issued;
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
-      }
       };
-      if (GATED || args.first == 0) {
-        load_job(std::integral_constant<int, 0>{});
-        if constexpr (!GATED) load_job(std::integral_constant<int, 1>{});
-      } else {
-        load_job(std::integral_constant<int, 1>{});
-        load_job(std::integral_constant<int, 0>{});
-      }
+      auto load_jobs = [&](auto op) {
+        const std::integral_constant<int, 0> j0;
+        const std::integral_constant<int, 1> j1;
+        if (GATED || args.deal.first == 0) {
+          load_job(j0, op);
+          if constexpr (!GATED) load_job(j1, op);
+        } else {
+          load_job(j1, op);
+          load_job(j0, op);
+        }
+      };
+      if constexpr (!GATED) load_jobs(std::integral_constant<int, 3>{});
+      else if (warp == PROD_WARP) load_jobs(std::integral_constant<int, 1>{});
+      else load_jobs(std::integral_constant<int, 2>{});
       // the last loads land before the CTA can exit (in a pair the odd CTA is
       // held by the closing cluster barrier)
       if (leader) {
@@ -587,7 +612,8 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
                                (A_MN ? (1u << 15) : 0u) | (B_MN ? (1u << 16) : 0u);
         const int tiles = sched.count(ji);
         for (int ti = 0; ti < tiles && ok; ++ti) {
-          const int s = (sched.tile(ji, ti) / job.tiles_per_out) % job.split;
+          const uint32_t q = job.by_out.div((uint32_t)sched.tile(ji, ti));
+          const int s = (int)(q - job.by_split.div(q) * (uint32_t)job.split);
           const int kb0 = s * job.kb_split, kb1 = min(job.kb_total, kb0 + job.kb_split);
           if (!mbar_wait(bar_cempty(buf), buf_phase ^ 1u, abort_flag)) { ok = false; break; }
           tc_fence_after_sync();
@@ -618,7 +644,7 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
           if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
         }
       };
-      if (GATED || args.first == 0) {
+      if (GATED || args.deal.first == 0) {
         issue_job(std::integral_constant<int, 0>{});
         if constexpr (!GATED) issue_job(std::integral_constant<int, 1>{});
       } else {
@@ -641,6 +667,7 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
     int sbox = 0;  // staging box to fill next
     int buf = 0;
     uint32_t buf_phase = 0;
+    grid_dep_wait();
     if (!GATED && args.bias_grad.outputs > 0)
       // (16 x 32 x 9 FP32 over the staging boxes of all epilogue warps)
       ffn_bias_grad<DT>(args.bias_grad, reinterpret_cast<float*>(smem + L::OFF_STG), (int)blockIdx.x, (int)gridDim.x);
@@ -649,9 +676,9 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
       const int ji = ti < tiles0 ? sched.first : 1 - sched.first, t = sched.tile(ji, ti < tiles0 ? ti : ti - tiles0);
       const FfnJob& job = args.job[ji];
       const int M = job.M, N = job.N;
-      int s, g, mb, nb;
-      tile_decode(job, t, s, g, mb, nb);
-      const int m0 = mb * tile_rows + (int)rank * kFfnBM + q * 32, n0 = nb * args.cols;
+      const FfnTile tile(job, (uint32_t)t);
+      const int s = tile.s, g = tile.g, nb = tile.nb;
+      const int m0 = tile.mb * tile_rows + (int)rank * kFfnBM + q * 32, n0 = nb * args.cols;
 
       // The 32 x 32 box at (m0, nc) of output `o`, this lane's row given as
       // 16 packed pairs value(0) .. value(15), through the staging box: 64
@@ -718,6 +745,16 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
       tc_fence_after_sync();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kFfnMaxBN);
       const bool rows_in = m0 < M;  // warp-uniform
+      // this warp is done with the accumulator: its sums are in registers
+      auto release = [&]() {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR) mbar_arrive_cluster(map_to_cta(bar_cempty(buf), 0u));
+          else mbar_arrive(bar_cempty(buf));
+        }
+      };
+      bool held = true;
 #pragma unroll 1
       for (int bx = part; bx < boxes; bx += EPI_WARPS / 4) {
         const int nc = n0 + bx * 32;
@@ -731,15 +768,18 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
           uint16_t* const sbias = reinterpret_cast<uint16_t*>(smem + L::OFF_BIAS) + (buf * 4 + bx) * 64;
           if (biased && job.split == 1) {
             // lane l fetches the biases of column nc + l.  The four warps of a
-            // box write the same values; the slot is this accumulator's, and
-            // no warp is two tiles ahead of another.
+            // box write the same values; the slot is this accumulator's, whose
+            // next tile starts only after all warps have released it.
             const int col = nc + lane;
             sbias[lane] = (args.bias[0] != nullptr && col < N) ? __ldg(args.bias[0] + col) : (uint16_t)0;
             sbias[32 + lane] = (args.bias[1] != nullptr && col < N) ? __ldg(args.bias[1] + col) : (uint16_t)0;
             __syncwarp();
           }
           tmem_ld_wait();
+          const bool last_box = bx + EPI_WARPS / 4 >= boxes;
           if (job.split > 1) {
+            if (last_box) release();
+            held = !last_box;
             store_partial(r, s, nc);
             store_partial(r2, job.split + s, nc);
             continue;
@@ -757,6 +797,9 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
               }
             }
           }
+          // (after the biases: their slot is the accumulator's)
+          if (last_box) release();
+          held = !last_box;
           if (args.save) {
             store_box(1, nc, [&](int i) { return ep_pack_t<DT>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])); });
             store_box(2, nc, [&](int i) { return ep_pack_t<DT>(__uint_as_float(r2[2 * i]), __uint_as_float(r2[2 * i + 1])); });
@@ -773,17 +816,16 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
           else gate(std::integral_constant<int, kActGeluErf>{});
         } else {
           tmem_ld_wait();
+          if (bx + EPI_WARPS / 4 >= boxes) {
+            release();
+            held = false;
+          }
           if (job.split > 1) store_partial(r, g * job.split + s, nc);
           else
             store_box(g, nc, [&](int i) { return ep_pack_t<DT>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])); });
         }
       }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (PAIR) mbar_arrive_cluster(map_to_cta(bar_cempty(buf), 0u));
-        else mbar_arrive(bar_cempty(buf));
-      }
+      if (held) release();
       if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
     }
     if (lane == 0) bulk_wait_group_read<0>();

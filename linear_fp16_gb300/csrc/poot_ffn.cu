@@ -327,7 +327,6 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
     FfnJob& j = a.job[ji];
     j.M = static_cast<int>(q.rows);
     j.N = static_cast<int>(q.cols);
-    j.parts = q.parts;
     j.num_m = static_cast<int>(ceil_div(q.rows, kFfnBM * p.cl));
     j.num_n = static_cast<int>(ceil_div(q.cols, a.cols));
     const int64_t kb_part = ceil_div(q.kext, bk);
@@ -347,7 +346,11 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
     if (total > INT32_MAX / 4) return POOT_ERR_INVALID_ARG;
     j.tiles_per_out = static_cast<int>(tpo);
     j.tiles = static_cast<int>(tiles);
-    j.partial = j.split > 1 ? partial[i] : nullptr;
+    j.by_out = FfnDiv(static_cast<uint32_t>(tpo));
+    j.by_split = FfnDiv(static_cast<uint32_t>(j.split));
+    j.by_span = FfnDiv(static_cast<uint32_t>(j.group_m) * static_cast<uint32_t>(j.num_n));
+    j.by_group = FfnDiv(static_cast<uint32_t>(j.group_m));
+    j.by_rest = FfnDiv(static_cast<uint32_t>((j.num_m - 1) % j.group_m + 1));
     const int ny = q.gated ? (ep.save ? 3 : 1) : q.outputs;
     j.tma_store = j.split == 1 && q.cols % 8 == 0;
     for (int o = 0; o < ny; ++o) {
@@ -366,7 +369,7 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
       for (int o = 0; o < ny; ++o)
         ok = ok && encode_2d(&m.y[ji][o], q.y[o], q.cols, q.rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, bf16);
     if (j.split > 1)
-      ok = ok && encode_3d_f32(&m.partial[ji], j.partial, ceil_div(q.cols, 4) * 4, q.rows,
+      ok = ok && encode_3d_f32(&m.partial[ji], partial[i], ceil_div(q.cols, 4) * 4, q.rows,
                                uint64_t(j.split) * (q.gated ? 2 : q.outputs), 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
     if (!ok) return cuda_fail(cudaErrorInvalidValue);
   }
@@ -375,16 +378,24 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
     j.tiles_per_out = 1;
     j.split = 1;
   }
+  // without bias gradients no more CTAs than tiles
+  const int64_t units = a.bias_grad.outputs > 0 ? units_max : std::min<int64_t>(total, units_max);
+  FfnDeal& deal = a.deal;
   if (count == 2) {
     double t[2];
     for (int i = 0; i < 2; ++i) t[i] = tile_time(shape_of(p), int64_t(a.job[i].kb_split) * p.cl, a.cols);
-    a.first = t[1] > t[0] ? 1 : 0;
-    a.extra = static_cast<int>(t[a.first] / t[1 - a.first] + 0.5);
+    deal.first = t[1] > t[0] ? 1 : 0;
+    deal.extra = static_cast<int>(std::min(t[deal.first] / t[1 - deal.first] + 0.5, 1e6));
   } else if (count == 1) {
-    a.first = ps[0]->mn_a ? 1 : 0;
+    deal.first = ps[0]->mn_a ? 1 : 0;
   }
-  // without bias gradients no more CTAs than tiles
-  const int64_t units = a.bias_grad.outputs > 0 ? units_max : std::min<int64_t>(total, units_max);
+  deal.rounds = static_cast<int>(a.job[deal.first].tiles / units);
+  deal.rest = static_cast<int>(a.job[deal.first].tiles % units);
+  deal.tiles1 = a.job[1 - deal.first].tiles;
+  const int64_t dealt = deal.rest != 0 ? std::min<int64_t>(int64_t(deal.extra) * (units - deal.rest), deal.tiles1) : 0;
+  deal.base = static_cast<int>(dealt);
+  deal.rounds1 = static_cast<int>((deal.tiles1 - dealt) / units);
+  deal.rest1 = static_cast<int>((deal.tiles1 - dealt) % units);
   const bool pair = p.cl == 2;
   cudaError_t e;
   if (gated) e = pair ? launch_ffn<2, true>(m, a, bf16, units, stream) : launch_ffn<1, true>(m, a, bf16, units, stream);
@@ -396,7 +407,7 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
     if (j.split == 1) continue;
     FfnReduceArgs r;
     std::memset(&r, 0, sizeof(r));
-    r.ws = j.partial;
+    r.ws = partial[i];
     for (int o = 0; o < 3; ++o) r.y[o] = j.y[o];
     for (int o = 0; o < 2; ++o) r.bias[o] = a.bias[o];
     r.M = q.rows;
