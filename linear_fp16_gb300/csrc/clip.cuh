@@ -4,14 +4,14 @@
 //   scale = min(1, max_norm / (norm + 1e-6))
 //   out   = RN(g * scale)          (in place where dst == src)
 //
-// One cooperative launch for up to kClipTable tensors: every block sums the
-// squares of its 32 KB pieces into one FP64 partial; after a grid barrier it
-// adds all partials in the same order (so all blocks see the same scale, and
-// the result does not depend on which block comes first) and scales its
-// pieces, the last one first and straight from the registers it was summed
-// from: up to one piece per resident block (10 MB) the tensors are read from
-// memory once.  Beyond that the second read is from L2 as far as L2 holds
-// them.  Longer lists take several launches of each half.  Bound by HBM.
+// Every block sums the squares of its 32 KB pieces into one FP64 partial; then,
+// in a second launch or after the grid barrier of a cooperative one, it adds
+// all partials in the same order (so all blocks see the same scale, and the
+// result does not depend on which block comes first) and scales its pieces,
+// the last one first: those are what L2, or in the cooperative form the
+// registers, still hold.  Bound by HBM: the tensors are read for the norm, read
+// again, from L2 as far as it holds them, and written.  Lists beyond kClipTable
+// tensors take several launches of each half.
 #pragma once
 
 #include <cooperative_groups.h>

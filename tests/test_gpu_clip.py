@@ -107,3 +107,27 @@ def test_equal_calls_give_equal_bits():
     norms = [L.clip_grad_norm(dev, 1.0, out=o) for o in outs]
     torch.cuda.synchronize()
     assert torch.equal(*norms) and all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_beyond_the_cooperative_threshold_and_31_bits(in_place):
+    """One tensor of more than 2^31 elements beside a small one (the norm by
+    64-bit sums of slices; results compared on slices at both ends)."""
+    n = (1 << 31) + 12345
+    big = torch.full((n,), 1.0 / 1024, dtype=BF16, device=DEV)
+    small = torch.randn(1000, generator=torch.Generator().manual_seed(3)).to(F32)
+    big[::4097] = 0.5
+    dev = small.to(DEV)
+    total = float(small.double().square().sum())
+    for i in range(0, n, 1 << 28):
+        total += float(big[i:i + (1 << 28)].double().square().sum())
+    ref = math.sqrt(total)
+    ends = [big[:5000].cpu(), big[-5000:].cpu(), small]
+    out = None if in_place else [torch.empty_like(big), torch.empty_like(dev)]
+    norm = L.clip_grad_norm([big, dev], 1.0, out=out)
+    torch.cuda.synchronize()
+    assert abs(float(norm) - ref) <= 2.0 ** -18 * ref
+    rb, rs = (big, dev) if in_place else out
+    for src, got in zip(ends, (rb[:5000], rb[-5000:], rs)):
+        want = src.double() / (ref + 1e-6)
+        R.check(got, want, (2.0 ** -18 + 2.0 ** -23) * want.abs(), "ends")

@@ -353,3 +353,32 @@ def test_on_another_stream_and_in_a_graph():
     assert torch.equal(gb[0], want_b[0])
     ref = torch.sqrt(sum(t.double().square().sum() for t in want_b[1:]))
     assert abs(float(norm) - float(ref)) <= 1e-6 * float(ref)
+
+
+def test_outputs_and_inputs_beyond_31_bits_of_elements():
+    """M * N above 2^31: rows at both ends and in the middle against the
+    64-bit form (N odd: rows of every alignment, no TMA stores)."""
+    M, N, K = 66000, 32769, 16
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    rnd = lambda *s: torch.randn(s, generator=gen, device=DEV, dtype=torch.float32)
+    x, wg, wu = rnd(M, K).to(BF16), (rnd(N, K) * 0.3).to(BF16), (rnd(N, K) * 0.3).to(BF16)
+    h, g, u = L.gated_linear(x, wg, wu, save=True)
+    rows = [0, 1, M // 2, 65534, 65535, M - 2, M - 1]
+    pick = lambda t: t[rows].cpu()
+    _check_gated(pick(x), wg.cpu(), wu.cpu(), None, None, "silu", True, (pick(h), pick(g), pick(u)))
+    dx = L.gated_linear_backward(h, x, wg, wu, g, u, need_dw=False)[0]
+    _ok()
+    ins = (pick(h), pick(x), wg.cpu(), wu.cpu(), pick(g), pick(u))
+    _check_gated_bwd(ins, "silu", (pick(dx), None, None, None, None))
+
+
+def test_gradients_over_many_rows():
+    """dW and db over more rows than one row block or K range holds."""
+    M, N, K = 70000, 24, 40
+    gen = _gen(M, N, K, 6)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=gen).to(F16)
+    dy, x, w = ints(M, N), ints(M, K), ints(N, K)
+    dx, dw, db = L.linear_backward(*_dev(dy, x, w))
+    _ok()
+    for o, r in ((dx, dy.double() @ w.double()), (dw, dy.double().T @ x.double()), (db, dy.double().sum(0))):
+        assert torch.equal(o.cpu(), r.float().to(F16))
