@@ -1,10 +1,10 @@
 // The gated block for up to 16 rows of x (a decode step): a stream of both
 // weights, bound by HBM (4 K bytes per output column).
 //
-// gated_gemv_kernel: operands on 16-byte boundaries.  One block per SM owns
-// an equal share of consecutive output columns, whatever their number (its
-// last columns may fill only part of an MMA: what is not there is not loaded),
-// and walks it in passes of up to 16 columns; sixteen warps split K.  Lane
+// gated_gemv_kernel: operands on 16-byte boundaries.  A block, one or two per
+// SM, owns an equal share of consecutive output columns, whatever their number
+// (its last columns may fill only part of an MMA: what is not there is not
+// loaded), and walks it in passes of up to 16 columns; its warps split K.  Lane
 // (r = lane / 4, t = lane % 4) takes, per step of 32 along K and group of 8
 // columns, the vectors Wg[n + r][k + 8t ..) and Wu[n + r][k + 8t ..) and
 // x[r][k + 8t ..) (x[r + 8] too when M > 8).  The summation order is free, so
@@ -13,7 +13,7 @@
 // MMAs, without shuffles, and a thread ends up with g and u of the same
 // output.  The weights pass through a ring of cp.async copies whose slots a
 // lane fills and reads alone (no barriers): the bytes in flight per SM are
-// the ring's 192 KB, not what registers can hold, and they keep flowing over
+// the ring's 192 KB, whatever registers can hold, and they keep flowing over
 // the ends of passes.  Warps meet in shared memory in a fixed order.
 //
 // gated_gemv_any_kernel: any alignment (rows gathered by smaller loads).
@@ -33,15 +33,19 @@ struct GatedGemvArgs {
   int kw;  // warps that split K
 };
 
-constexpr int kGgWarps = 16;
+// Two blocks of eight warps per SM, beside which the next launch's blocks find
+// room to start; where those would have fewer than a group of 8 columns each,
+// one block of sixteen warps (GB300, two blocks against one: 1 x 14336 x 4096
+// 38.2 and 39.1 us, 16 x 14336 x 4096 41.5 and 45.2, 8 x 4096 x 4096 13.0 and
+// 14.4; 16 x 1024 x 4096 10.1 and 7.7, 1 x 1024 x 768 3.1 and 2.7).
 constexpr int kGgSub = 2;    // groups of 8 columns per pass
 constexpr int kGgSteps = 2;  // steps of 32 along K per ring slot
 constexpr int kGgRing = 3;   // slots
 constexpr int kGgSlot = kGgSteps * kGgSub * 2 * 512;  // bytes of a warp's slot
-constexpr int kGgRingBytes = kGgWarps * kGgRing * kGgSlot;
-__host__ __device__ constexpr int gg_red_floats(int nt) { return kGgWarps * kGgSub * 16 * (8 * nt + 1); }
-__host__ __device__ constexpr int gg_smem_bytes(int nt) { return kGgRingBytes + gg_red_floats(nt) * 4; }
-static_assert(gg_smem_bytes(2) <= 232448, "more shared memory than a CTA can have");
+__host__ __device__ constexpr int gg_ring_bytes(int warps) { return warps * kGgRing * kGgSlot; }
+__host__ __device__ constexpr int gg_red_floats(int nt, int warps) { return warps * kGgSub * 16 * (8 * nt + 1); }
+__host__ __device__ constexpr int gg_smem_bytes(int nt, int warps) { return gg_ring_bytes(warps) + gg_red_floats(nt, warps) * 4; }
+static_assert(gg_smem_bytes(2, 16) <= 232448 && 2 * (gg_smem_bytes(2, 8) + 1024) <= 233472, "shared memory of an SM");
 
 // biases, then one rounding of each result
 template <int DT>
@@ -58,11 +62,11 @@ __device__ __forceinline__ void gg_finish(const GatedGemvArgs& a, float g, float
 }
 
 // NT: 8-column blocks of tokens (1: M <= 8, 2: M <= 16)
-template <int NT, int DT>
-__global__ void __launch_bounds__(kGgWarps * 32, 1) gated_gemv_kernel(const GatedGemvArgs a) {
+template <int NT, int DT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) gated_gemv_kernel(const GatedGemvArgs a) {
   constexpr int MT = 8 * NT;
   extern __shared__ __align__(16) uint8_t gg_smem[];
-  float* red = reinterpret_cast<float*>(gg_smem + kGgRingBytes);
+  float* red = reinterpret_cast<float*>(gg_smem + gg_ring_bytes(WARPS));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, t = lane & 3;
   const int K = a.K, N = a.N, M = a.M;
@@ -73,7 +77,7 @@ __global__ void __launch_bounds__(kGgWarps * 32, 1) gated_gemv_kernel(const Gate
   constexpr int KS = 32 * kGgSteps;
   // K is split over a.kw warps (as many as have a slot's worth of it, a power
   // of two); the warps are 16 / kw teams, each with every (16 / kw)-th pass
-  const int kw = a.kw, teams = kGgWarps / kw, team = warp / kw;
+  const int kw = a.kw, teams = WARPS / kw, team = warp / kw;
   const int slice = ((K + kw * KS - 1) / (kw * KS)) * KS;
   const int k_begin = min(K, (warp & (kw - 1)) * slice), k_end = min(K, k_begin + slice);
   const int kchunks = (k_end - k_begin + KS - 1) / KS;
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(kGgWarps * 32, 1) gated_gemv_kernel(const Gate
         for (int i = 0; i < 4; ++i)
           red[((warp * kGgSub + g) * 16 + r + (i < 2 ? 0 : 8)) * (MT + 1) + 8 * q + 2 * t + (i & 1)] = d[g][q][i];
     __syncthreads();
-    for (int o = threadIdx.x; o < teams * 8 * kGgSub * M; o += kGgWarps * 32) {
+    for (int o = threadIdx.x; o < teams * 8 * kGgSub * M; o += WARPS * 32) {
       const int n = o & (8 * kGgSub - 1), j = (o / (8 * kGgSub)) & (teams - 1), m = o / (8 * kGgSub * teams);
       const int col = c_begin + (rd * teams + j) * 8 * kGgSub + n;
       if (col >= c_end) continue;

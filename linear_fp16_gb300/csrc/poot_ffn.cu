@@ -55,8 +55,11 @@ cudaError_t set_attr() {
 
 template <int NT, int DT>
 cudaError_t set_gemv_attr() {
-  return cudaFuncSetAttribute(gated_gemv_kernel<NT, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              gg_smem_bytes(NT));
+  const cudaError_t e = cudaFuncSetAttribute(gated_gemv_kernel<NT, DT, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             gg_smem_bytes(NT, 16));
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(gated_gemv_kernel<NT, DT, 8>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, gg_smem_bytes(NT, 8));
 }
 
 int ffn_device(FfnDevice** out) {
@@ -432,12 +435,29 @@ int finish(WorkspaceLease& lease, int rc) {
 }
 
 // ---- the gated block ------------------------------------------------------------
+template <int NT, int WARPS>
+cudaError_t launch_gated_gemv_vec(const GatedGemvArgs& a, bool bf16, unsigned blocks, cudaStream_t stream) {
+  return launch(bf16 ? gated_gemv_kernel<NT, kEpiBf16, WARPS> : gated_gemv_kernel<NT, kEpiF16, WARPS>, dim3(blocks),
+                dim3(WARPS * 32), gg_smem_bytes(NT, WARPS), stream, a);
+}
+
 template <int NT>
-cudaError_t launch_gated_gemv(const GatedGemvArgs& a, bool bf16, bool vec, int sms, cudaStream_t stream) {
+cudaError_t launch_gated_gemv(GatedGemvArgs a, bool bf16, bool vec, int sms, cudaStream_t stream) {
   if (vec) {
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(sms, a.N)));
-    return launch(bf16 ? gated_gemv_kernel<NT, kEpiBf16> : gated_gemv_kernel<NT, kEpiF16>, grid, dim3(kGgWarps * 32),
-                  gg_smem_bytes(NT), stream, a);
+    const bool two = a.N >= 8 * 2 * sms;
+    const int warps = two ? 8 : 16;
+    const int64_t blocks = std::min<int64_t>(two ? 2 * sms : sms, a.N);
+    // Warps that split K: never more than there are ring slots of K; and, as
+    // far as the block has a pass for each team, so few that a warp's share of a
+    // pass is four slots (8 x 8192 x 2048 on GB300: 16.3 us with two slots, 14.1
+    // with four)
+    const int64_t passes = ceil_div(ceil_div(a.N, blocks), 8 * kGgSub);
+    a.kw = warps;
+    while (a.kw > 1 && (a.kw / 2 * 32 * kGgSteps >= a.K ||
+                        (a.K < a.kw * 128 * kGgSteps && 2 * warps / a.kw <= passes)))
+      a.kw /= 2;
+    return two ? launch_gated_gemv_vec<NT, 8>(a, bf16, static_cast<unsigned>(blocks), stream)
+               : launch_gated_gemv_vec<NT, 16>(a, bf16, static_cast<unsigned>(blocks), stream);
   }
   const int64_t tiles = ceil_div(a.N, 16);
   const dim3 grid(static_cast<unsigned>(tiles));
@@ -465,15 +485,6 @@ int gated_gemv(const poot_gated_linear_args& p, int64_t ldx, const FfnDevice& d,
   a.K = static_cast<int>(p.K);
   a.act = p.activation;
   a.save = p.g != nullptr;
-  // Warps that split K: never more than there are ring slots of K; and, as
-  // far as the block has a pass for each team, so few that a warp's share of a
-  // pass is four slots (8 x 8192 x 2048 on GB300: 16.3 us with two slots, 14.1
-  // with four)
-  const int64_t passes = ceil_div(ceil_div(p.N, std::min<int64_t>(d.sms, p.N)), 8 * kGgSub);
-  a.kw = kGgWarps;
-  while (a.kw > 1 && (a.kw / 2 * 32 * kGgSteps >= p.K ||
-                      (p.K < a.kw * 128 * kGgSteps && 2 * kGgWarps / a.kw <= passes)))
-    a.kw /= 2;
   const bool bf16 = p.dtype == POOT_DTYPE_BF16;
   const bool vec = p.K % 8 == 0 && ldx % 8 == 0 && aligned(p.x, 16) && aligned(p.wg, 16) && aligned(p.wu, 16);
   const cudaError_t e = p.M <= 8 ? launch_gated_gemv<1>(a, bf16, vec, d.sms, stream)
