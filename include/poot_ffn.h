@@ -43,9 +43,9 @@ enum poot_ffn_act {
  * poot_gated_linear_backward reads.  h is computed from the FP32 values.
  * M <= 16 streams the weights once (GEMV kernels, HBM-bound; 16-byte loads
  * with 16-byte aligned x and weights, K % 8 == 0 and ldx % 8 == 0); larger M
- * runs on the tcgen05 GEMM, whose operands, where TMA cannot read them in place (base
- * not 16-byte aligned, row pitch not a multiple of 8), are first copied to
- * 16-byte-pitched rows in the library's workspace.
+ * runs on the tcgen05 GEMM, whose operands, where TMA cannot read them in
+ * place (base not 16-byte aligned, row pitch not a multiple of 8), are first
+ * copied to 16-byte-pitched rows in the library's workspace.
  * M == 0 or N == 0 does nothing; K == 0 gives g = bg, u = bu.
  * Errors: POOT_ERR_INVALID_ARG (sizes outside [0, 2^31), NULL, ldx < K, an
  * unknown dtype or activation, only one of g and u, an output overlapping an

@@ -13,12 +13,16 @@
 //
 // A persistent CTA (or a CTA pair on one 256-row tile, 2-SM MMA) per SM walks
 // output tiles.  Warp roles as in the linear's GEMM: epilogue warps, one
-// thread that issues the MMAs, one that issues the TMA loads.  A sum stays
+// thread that issues the MMAs, one or two that issue the TMA loads.  A sum stays
 // in TMEM over the whole K range (FP32 accumulators): unlike the linear's
 // kernel there is no promotion into registers every 1024 elements, because
 // these operators' outputs are rounded once from the FP32 value to 11 or 8
 // bits and carry no 2-ulp rule; the accumulators of two tiles fit TMEM, so
-// the epilogue of a tile runs under the main loop of the next.
+// the epilogue of a tile runs under the main loop of the next.  Bound by the
+// tensor pipe under the power cap where K is long (GB300, bfloat16, 8192 x
+// 14336 x 4096: gated with g and u 1.13 ms, 1.70 PFLOP/s; dx and both dW 2.24
+// ms, 1.72 PFLOP/s), by operand loads from L2 (about 80 GB/s per SM) and the
+// start-up where one wave of tiles holds the problem.
 //
 // The gated tile: half of the tile's BN accumulator columns hold gate
 // columns and half the same columns of up, so that one thread has g and u
@@ -44,13 +48,12 @@ enum FfnAct : int { kActSilu = 0, kActGeluTanh = 1, kActGeluErf = 2 };
 
 constexpr int kFfnBM = 128;
 constexpr int kFfnBK = 64;  // one 128-byte swizzle row
-// Epilogue warps; then the MMA issuer and two producers, one per operand (one
-// thread issuing both took 0.3 us a stage where the MMAs take 0.27).  The gated kernel
-// takes eight with 168 registers and two staging boxes each, the gradients
-// sixteen with one
-// (GB300: gated 1417 x 520 x 1280 9.9 us with eight, 10.8 with sixteen, 4096 x
-// 4096 x 1024 with g and u 48.6 and 50.5; gradients 6 x 8320 x 470 29.8 and
-// 27.0, 112 x 4480 x 2531 61 and 55, 1024 x 1024 x 768 14.8 and 15.4).
+// Epilogue warps; then the MMA issuer; then the TMA producer, in the gated
+// kernel one per operand.  The gated kernel takes eight epilogue warps with 168
+// registers and two staging boxes each, the gradients sixteen with one (GB300:
+// gated 1417 x 520 x 1280 9.9 us with eight, 10.8 with sixteen, 4096 x 4096 x
+// 1024 with g and u 48.6 and 50.5; gradients 6 x 8320 x 470 29.8 and 27.0, 112
+// x 4480 x 2531 61 and 55, 1024 x 1024 x 768 14.8 and 15.4).
 __host__ __device__ constexpr int ffn_epi_warps(bool gated) { return gated ? 8 : 16; }
 __host__ __device__ constexpr int ffn_threads(bool gated) { return (ffn_epi_warps(gated) + (gated ? 3 : 2)) * 32; }
 constexpr int kFfnMaxBN = 256;
