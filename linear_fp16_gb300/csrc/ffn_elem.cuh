@@ -69,7 +69,7 @@ struct GateGradArgs {
   long long ld_dh, ld_g, ld_u;
   uint16_t *dg, *du;  // row pitch ldo, 16-byte aligned rows
   long long ldo;
-  float* sums;        // [row blocks][2][N] FP32 column sums, or nullptr
+  float* sums;        // [row blocks][2][N rounded up to 8] FP32 column sums, or nullptr
   int M, N, act;
   int rows;           // rows of a block, a multiple of 16
   int blocks;         // blocks of the gradient; the grid's others repack
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const __grid_co
         float s = red[0][threadIdx.x];
 #pragma unroll
         for (int w = 1; w < 8; ++w) s += red[w][threadIdx.x];
-        a.sums[((size_t)rb * 2 + o) * a.N + col] = s;
+        a.sums[((size_t)rb * 2 + o) * ((a.N + 7) / 8 * 8) + col] = s;
       }
     }
   }

@@ -250,7 +250,7 @@ struct FfnMaps {
 // sum over rows of either FP32 row-block sums (the gate's gradient leaves
 // them) or the rows of D itself.
 struct FfnBiasGrad {
-  const float* sums;   // [rows][outputs][N], or nullptr
+  const float* sums;   // [rows][outputs][pitch], pitch = N rounded up to 8, or nullptr
   const uint16_t* d;   // [rows][N] head dtype, rows ld apart, or nullptr
   long long ld;
   long long rows;
@@ -390,28 +390,24 @@ __device__ __forceinline__ void ffn_bias_grad(const FfnBiasGrad& b, float* red, 
     if (g < n) {
       const long long r0 = warp * (32 / width) + lane / width;
       if (b.sums != nullptr) {
-        const float* p = b.sums + (size_t)o * b.N + c;
-        const size_t pitch = (size_t)b.outputs * b.N;
-        const bool vec = b.N % 4 == 0 && nc == 8;
+        const int pitch = per_out * 8;
+        const float* p = b.sums + (size_t)o * pitch + c;
+        const size_t stride = (size_t)b.outputs * pitch;
 #pragma unroll 4
         for (long long r = r0; r < b.rows; r += step) {
-          const float* q = p + (size_t)r * pitch;
-          if (vec) {
-            const float4 u = __ldg(reinterpret_cast<const float4*>(q)), v = __ldg(reinterpret_cast<const float4*>(q) + 1);
-            s[0] += u.x; s[1] += u.y; s[2] += u.z; s[3] += u.w;
-            s[4] += v.x; s[5] += v.y; s[6] += v.z; s[7] += v.w;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (j < nc) s[j] += __ldg(q + j);
-          }
+          const float4* q = reinterpret_cast<const float4*>(p + (size_t)r * stride);
+          const float4 u = __ldg(q), v = __ldg(q + 1);
+          s[0] += u.x; s[1] += u.y; s[2] += u.z; s[3] += u.w;
+          s[4] += v.x; s[5] += v.y; s[6] += v.z; s[7] += v.w;
         }
       } else {
         const uint16_t *p = b.d + c, *hi = b.d + (b.rows - 1) * b.ld + b.N;
-        const bool vec = nc == 8 && b.ld % 8 == 0 && (reinterpret_cast<uintptr_t>(b.d) & 15u) == 0;
+        // (columns past N, inside the row's pitch, are added up and not stored;
+        // the last row's may not be there)
+        const bool vec = c + 8 <= b.ld && b.ld % 8 == 0 && (reinterpret_cast<uintptr_t>(b.d) & 15u) == 0;
 #pragma unroll 4
         for (long long r = r0; r < b.rows; r += step) {
-          const uint4 v = vec ? __ldg(reinterpret_cast<const uint4*>(p + r * b.ld))
+          const uint4 v = vec && (nc == 8 || r + 1 < b.rows) ? __ldg(reinterpret_cast<const uint4*>(p + r * b.ld))
                               : ffn_load8_any(p + r * b.ld, nc, b.d, hi);
           float f[8];
           ffn_unpack8<DT>(v, f);

@@ -671,7 +671,7 @@ int gated_linear_backward(const poot_gated_linear_backward_args* ap, cudaStream_
   void* const dwp[2] = {p.dwg, p.dwu};
   g.make(2, dmat, w, {p.x, M, K, ldx}, p.dx, dwp, M, N, K, d->sms, &pk);
   const size_t dbytes = round256(size_t(M) * Np * 2), partial = g.partial_bytes();
-  const size_t sbytes = want_db ? round256(size_t(row_blocks) * 2 * N * 4) : 0;
+  const size_t sbytes = want_db ? round256(size_t(row_blocks) * 2 * Np * 4) : 0;
   WorkspaceLease lease = stream_workspace(d->dev, stream, 2 * dbytes + partial + sbytes + pk.bytes);
   if (lease.ptr == nullptr) return cuda_fail(cudaErrorMemoryAllocation);
   char* const ws = static_cast<char*>(lease.ptr);
@@ -773,8 +773,8 @@ int linear_backward(const poot_linear_backward_args* ap, cudaStream_t stream) {
   FfnBiasGrad bg;
   std::memset(&bg, 0, sizeof(bg));
   if (p.db != nullptr) {
-    bg.d = static_cast<const uint16_t*>(p.dy);
-    bg.ld = ld_dy;
+    bg.d = static_cast<const uint16_t*>(dy.p);  // the repacked rows where there are any
+    bg.ld = dy.ld;
     bg.rows = M;
     bg.outputs = 1;
     bg.N = static_cast<int>(N);

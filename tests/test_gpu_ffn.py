@@ -382,3 +382,20 @@ def test_gradients_over_many_rows():
     _ok()
     for o, r in ((dx, dy.double() @ w.double()), (dw, dy.double().T @ x.double()), (db, dy.double().sum(0))):
         assert torch.equal(o.cpu(), r.float().to(F16))
+
+
+@pytest.mark.parametrize("M,N,ld", [(1, 3, 8), (5, 11, 16), (300, 230, 230), (300, 230, 232), (1000, 1001, 1008), (70, 8, 8)])
+def test_bias_gradients_of_ragged_columns(M, N, ld):
+    """Column counts that end inside a group of eight, alone and beside the
+    products, at several pitches; what lies between rows is never used."""
+    gen = _gen(M, N, ld, 7)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=gen).to(BF16)
+    wide = torch.full((M, ld), float("nan"), dtype=BF16, device=DEV)
+    dy, x, w = ints(M, N), ints(M, 24), ints(N, 24)
+    wide[:, :N] = dy.to(DEV)
+    want = dy.double().sum(0).float().to(BF16)
+    db = L.linear_backward(wide[:, :N], *_dev(x, w), need_dx=False, need_dw=False)[2]
+    both = L.linear_backward(wide[:, :N], *_dev(x, w))
+    _ok()
+    assert torch.equal(db.cpu(), want) and torch.equal(both[2].cpu(), want)
+    assert torch.equal(both[0].cpu(), (dy.double() @ w.double()).float().to(BF16))
