@@ -111,7 +111,8 @@ def poot_clip_grad_norm(tensors, count: int, max_norm: float, norm: int, stream:
 _ext = None
 
 
-def _tensor_calls():
+def load_tensor_calls():
+    """The extension behind the tensor-level calls (built first if needed)."""
     global _ext
     if _ext is None:
         load_library()  # builds what is missing, and comes first: the extension links to it
@@ -145,7 +146,7 @@ def gated_linear(x, wg, wu, bg=None, bu=None, *, activation: str = "silu", save:
     Runs on ``stream`` (default: the current stream of x's device).  Raises
     PootLinearError on a status other than POOT_OK.
     """
-    r = (_ext or _tensor_calls()).gated_linear(x, wg, wu, bg, bu, out, _act(activation), save, _stream(stream))
+    r = (_ext or load_tensor_calls()).gated_linear(x, wg, wu, bg, bu, out, _act(activation), save, _stream(stream))
     if r.__class__ is int:
         raise _b.PootLinearError(r, "poot_gated_linear")
     return r
@@ -158,7 +159,7 @@ def gated_linear_backward(dh, x, wg, wu, g, u, *, activation: str = "silu", need
     dh, g and u [M,N] and x [M,K] may have rows further apart than their
     columns; g and u are what gated_linear returned with ``save``.
     """
-    r = (_ext or _tensor_calls()).gated_linear_backward(dh, x, wg, wu, g, u, _act(activation), need_dx, need_dw,
+    r = (_ext or load_tensor_calls()).gated_linear_backward(dh, x, wg, wu, g, u, _act(activation), need_dx, need_dw,
                                                         need_db, _stream(stream))
     if r.__class__ is int:
         raise _b.PootLinearError(r, "poot_gated_linear_backward")
@@ -167,7 +168,7 @@ def gated_linear_backward(dh, x, wg, wu, g, u, *, activation: str = "silu", need
 
 def linear_backward(dy, x, w, *, need_dx: bool = True, need_dw: bool = True, need_db: bool = True, stream=None):
     """Gradients (dx, dw, db) of y = x W^T + b for dy [M,N]; None where not needed."""
-    r = (_ext or _tensor_calls()).linear_backward(dy, x, w, need_dx, need_dw, need_db, _stream(stream))
+    r = (_ext or load_tensor_calls()).linear_backward(dy, x, w, need_dx, need_dw, need_db, _stream(stream))
     if r.__class__ is int:
         raise _b.PootLinearError(r, "poot_linear_backward")
     return r
@@ -182,7 +183,7 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, stream=None):
     instead.  The norm, over all tensors together, is a float32 scalar tensor
     on the device (the call does not synchronise).
     """
-    r = (_ext or _tensor_calls()).clip_grad_norm(list(grads), None if out is None else list(out), max_norm,
+    r = (_ext or load_tensor_calls()).clip_grad_norm(list(grads), None if out is None else list(out), max_norm,
                                                  _stream(stream))
     if r.__class__ is int:
         raise _b.PootLinearError(r, "poot_clip_grad_norm")
