@@ -399,3 +399,20 @@ def test_bias_gradients_of_ragged_columns(M, N, ld):
     _ok()
     assert torch.equal(db.cpu(), want) and torch.equal(both[2].cpu(), want)
     assert torch.equal(both[0].cpu(), (dy.double() @ w.double()).float().to(BF16))
+
+
+@pytest.mark.parametrize("N", [202, 204, 201, 200, 34, 36])
+@pytest.mark.parametrize("off", [0, 1, 2, 4])
+def test_output_rows_at_any_alignment(N, off):
+    """Rows and bases of 2, 4, 8 and 16 bytes' alignment; nothing outside the
+    output is written."""
+    M, K, pad = 150, 72, 64
+    x, wg, wu, bg, bu = _gated_inputs(M, N, K, BF16, True, seed=8)
+    flat = torch.full((M * N + 2 * pad,), -7.0, dtype=BF16, device=DEV)
+    out = flat[pad + off:pad + off + M * N].view(M, N)
+    h = L.gated_linear(*_dev(x, wg, wu, bg, bu), out=out)
+    saved = L.gated_linear(*_dev(x, wg, wu, bg, bu), save=True)
+    _ok()
+    _check_gated(x, wg, wu, bg, bu, "silu", True, saved)
+    assert h is out and torch.equal(h, saved[0])
+    assert (flat[:pad + off] == -7).all() and (flat[pad + off + M * N:] == -7).all()
