@@ -35,9 +35,10 @@ struct GatedGemvArgs {
 
 // Two blocks of eight warps per SM, beside which the next launch's blocks find
 // room to start; where those would have fewer than a group of 8 columns each,
-// one block of sixteen warps (GB300, two blocks against one: 1 x 14336 x 4096
-// 38.2 and 39.1 us, 16 x 14336 x 4096 41.5 and 45.2, 8 x 4096 x 4096 13.0 and
-// 14.4; 16 x 1024 x 4096 10.1 and 7.7, 1 x 1024 x 768 3.1 and 2.7).
+// one block of sixteen warps (GB300, two blocks against one: 16 x 14336 x 4096
+// 41.5 and 45.2 us, 8 x 4096 x 4096 13.7 and 15.3; 1 x 14336 x 4096 38.2 and
+// 39.1 in a loop on one set of weights, 40.3 and 39.9 where they change from
+// call to call; 16 x 1024 x 4096 10.1 and 7.7, 1 x 1024 x 768 3.1 and 2.7).
 constexpr int kGgSub = 2;    // groups of 8 columns per pass
 constexpr int kGgSteps = 2;  // steps of 32 along K per ring slot
 constexpr int kGgRing = 3;   // slots
