@@ -143,12 +143,13 @@ inline bool encode_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64
   return r == CUDA_SUCCESS;
 }
 
-// ---- split-K workspace ------------------------------------------------------
+// ---- workspaces -------------------------------------------------------------
 struct Workspace {
+  std::mutex mu;  // held by the call that uses the buffer, see WorkspaceLease
   void* ptr = nullptr;
   size_t bytes = 0;
 };
-inline std::mutex g_ws_mu;
+inline std::mutex g_ws_mu;  // guards the map and the retired list, never held while a buffer's is taken
 // key: (device, stream, thread): the thread is part of the key only for
 // cudaStreamPerThread, one handle that names a different stream in each thread
 struct WorkspaceKey {
@@ -161,7 +162,7 @@ struct WorkspaceKey {
     return thread < o.thread;
   }
 };
-inline std::map<WorkspaceKey, Workspace> g_ws;
+inline std::map<WorkspaceKey, Workspace> g_ws;  // (its elements never move)
 inline std::vector<void*> g_ws_retired;
 
 struct WorkspaceRelease {
@@ -173,30 +174,37 @@ struct WorkspaceRelease {
 };
 inline WorkspaceRelease g_ws_release;
 
-// Workspace of a call (split-K partial sums, packed operands).  Outside
-// stream capture: one buffer per (device, stream; thread for
-// cudaStreamPerThread), grown by doubling and kept for the life of the process
-// (calls on one stream are ordered, so they can share it; a buffer outgrown
-// is kept too, as work queued earlier may still read it).  Under capture:
-// a graph-owned allocation (cudaMallocAsync / cudaFreeAsync on the capturing
+// Workspace of a call (split-K partial sums, packed operands, dg and du, the
+// clip's partial sums).  Outside stream capture: one buffer per (device,
+// stream; thread for cudaStreamPerThread), grown by doubling and kept for the
+// life of the process (a buffer outgrown is kept too, as work queued earlier
+// may still read it).  A call writes the buffer with one launch and reads it
+// with a later one, so the order of a stream's launches alone does not make it
+// safe to share: two host threads could queue A1 B1 A2 B2.  The lease holds
+// the buffer's lock until the call has queued its last launch; calls of other
+// threads on that stream wait on the host meanwhile.  Under capture: a
+// graph-owned allocation (cudaMallocAsync / cudaFreeAsync on the capturing
 // stream become memory nodes of the graph), so that a graph never shares a
-// buffer with calls made outside it.  nullptr: no workspace, no split.
+// buffer with calls made outside it.  nullptr: no workspace (and no lock).
 struct WorkspaceLease {
   void* ptr = nullptr;
   bool graph_owned = false;
   cudaStream_t stream = nullptr;
-  // a graph-owned workspace is freed on its stream after the last kernel
-  // that reads it (or on any early return before those launches)
+  std::unique_lock<std::mutex> lock;
+  // After the call's last launch, or on any early return before it: a
+  // graph-owned workspace is freed on its stream, a buffer's lock is given up.
   cudaError_t release() {
     cudaError_t e = cudaSuccess;
     if (graph_owned) e = cudaFreeAsync(ptr, stream);
     graph_owned = false;
+    if (lock.owns_lock()) lock.unlock();
     return e;
   }
   WorkspaceLease() = default;
   WorkspaceLease(const WorkspaceLease&) = delete;
   WorkspaceLease& operator=(const WorkspaceLease&) = delete;
-  WorkspaceLease(WorkspaceLease&& o) noexcept : ptr(o.ptr), graph_owned(o.graph_owned), stream(o.stream) {
+  WorkspaceLease(WorkspaceLease&& o) noexcept
+      : ptr(o.ptr), graph_owned(o.graph_owned), stream(o.stream), lock(std::move(o.lock)) {
     o.graph_owned = false;
   }
   WorkspaceLease& operator=(WorkspaceLease&& o) noexcept {
@@ -205,6 +213,7 @@ struct WorkspaceLease {
       ptr = o.ptr;
       graph_owned = o.graph_owned;
       stream = o.stream;
+      lock = std::move(o.lock);
       o.graph_owned = false;
     }
     return *this;
@@ -229,24 +238,30 @@ inline WorkspaceLease stream_workspace(int dev, cudaStream_t stream, size_t byte
     lease.stream = stream;
     return lease;
   }
-  std::lock_guard<std::mutex> lock(g_ws_mu);
   const std::thread::id tid = stream == cudaStreamPerThread ? std::this_thread::get_id() : std::thread::id();
-  Workspace& ws = g_ws[WorkspaceKey{dev, stream, tid}];
-  if (ws.bytes >= bytes) {
-    lease.ptr = ws.ptr;
-    return lease;
+  Workspace* ws;
+  {
+    std::lock_guard<std::mutex> lock(g_ws_mu);
+    ws = &g_ws[WorkspaceKey{dev, stream, tid}];
   }
-  size_t want = bytes > 2 * ws.bytes ? bytes : 2 * ws.bytes;
-  want = (want + (size_t(1) << 20) - 1) & ~((size_t(1) << 20) - 1);
-  void* p = nullptr;
-  if (cudaMalloc(&p, want) != cudaSuccess) {
-    (void)cudaGetLastError();  // no split-K then; not an error of the call
-    return lease;
+  std::unique_lock<std::mutex> held(ws->mu);
+  if (ws->bytes < bytes) {
+    size_t want = bytes > 2 * ws->bytes ? bytes : 2 * ws->bytes;
+    want = (want + (size_t(1) << 20) - 1) & ~((size_t(1) << 20) - 1);
+    void* p = nullptr;
+    if (cudaMalloc(&p, want) != cudaSuccess) {
+      (void)cudaGetLastError();  // no split-K then; not an error of the call
+      return lease;
+    }
+    if (ws->ptr != nullptr) {
+      std::lock_guard<std::mutex> lock(g_ws_mu);
+      g_ws_retired.push_back(ws->ptr);
+    }
+    ws->ptr = p;
+    ws->bytes = want;
   }
-  if (ws.ptr != nullptr) g_ws_retired.push_back(ws.ptr);
-  ws.ptr = p;
-  ws.bytes = want;
-  lease.ptr = p;
+  lease.ptr = ws->ptr;
+  lease.lock = std::move(held);
   return lease;
 }
 
