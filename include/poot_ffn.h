@@ -77,7 +77,7 @@ POOT_API int poot_gated_linear(const poot_gated_linear_args* args, poot_stream_t
  * Any output pointer may be NULL (not wanted); the inputs it alone needs may
  * then be NULL too (x only for dwg / dwu, wg and wu only for dx).  Outputs are
  * contiguous.  M == 0 writes zeros to dwg, dwu, dbg and dbu; N == 0 zeros to
- * dx.  dg and du live in the library's workspace (4 * M * ceil8(N) bytes).
+ * dx; K == 0 leaves dx, dwg and dwu without elements.  dg and du live in the library's workspace (4 * M * ceil8(N) bytes).
  * Errors as poot_gated_linear; POOT_ERR_CUDA when no workspace can be had.
  */
 typedef struct poot_gated_linear_backward_args {

@@ -648,7 +648,8 @@ int gated_linear_backward(const poot_gated_linear_backward_args* ap, cudaStream_
                               {p.u, span_bytes(M, N, ld_u)}},
                              {{p.dx, span_bytes(M, K, K)}, {p.dwg, wb}, {p.dwu, wb}, {p.dbg, 2 * N}, {p.dbu, 2 * N}});
   if (rc != POOT_OK) return rc;
-  if (p.dx == nullptr && !want_dw && !want_db) return POOT_OK;
+  // without columns dx, dwg and dwu have no elements: a launch needs a product or a bias gradient
+  if (((p.dx == nullptr && !want_dw) || K == 0) && !want_db) return POOT_OK;
   FfnDevice* d;
   const int st = ffn_device(&d);
   if (st != POOT_OK) return st;
@@ -742,7 +743,7 @@ int linear_backward(const poot_linear_backward_args* ap, cudaStream_t stream) {
   const int rc = check_spans({{p.dy, span_bytes(M, N, ld_dy)}, {p.x, span_bytes(M, K, ldx)}, {p.w, wb}},
                              {{p.dx, span_bytes(M, K, K)}, {p.dw, wb}, {p.db, 2 * N}});
   if (rc != POOT_OK) return rc;
-  if (p.dx == nullptr && p.dw == nullptr && p.db == nullptr) return POOT_OK;
+  if (((p.dx == nullptr && p.dw == nullptr) || K == 0) && p.db == nullptr) return POOT_OK;
   FfnDevice* d;
   const int st = ffn_device(&d);
   if (st != POOT_OK) return st;
@@ -780,7 +781,6 @@ int linear_backward(const poot_linear_backward_args* ap, cudaStream_t stream) {
     bg.N = static_cast<int>(N);
     bg.out[0] = static_cast<uint16_t*>(p.db);
   }
-  if (g.count == 0 && p.db == nullptr) return finish(lease, POOT_OK);
   return finish(lease, g.run(ep, &bg, ws, *d, stream));
 }
 
