@@ -2,12 +2,14 @@
 the extension that calls it on torch tensors.
 
 Usage: python -m linear_fp16_gb300.build [--verbose]
-Both land in linear_fp16_gb300/_build/ (git-ignored).
+builds the library, and the extension where torch is installed.  Both land in
+linear_fp16_gb300/_build/ (git-ignored).  The library needs neither torch nor
+Python's headers, to be built or to be loaded.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
-import re
 import shutil
 import subprocess
 import sys
@@ -47,14 +49,20 @@ def extension() -> str:
     return os.path.join(BUILD, f"_ffn_torch.{sys.implementation.cache_tag}.{torch.__version__}.so")
 
 
+def _newer(target: str, deps) -> bool:
+    if not os.path.exists(target):
+        return False
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(p) <= t for p in deps)
+
+
 def up_to_date() -> bool:
-    for target, deps in ((LIB, DEPENDS), (extension(), EXT_DEPENDS)):
-        if not os.path.exists(target):
-            return False
-        t = os.path.getmtime(target)
-        if any(os.path.getmtime(p) > t for p in deps):
-            return False
-    return True
+    """Whether the library is built from the present sources (torch plays no part in it)."""
+    return _newer(LIB, DEPENDS)
+
+
+def extension_up_to_date() -> bool:
+    return _newer(extension(), EXT_DEPENDS)
 
 
 def _run(cmd, verbose: bool) -> None:
@@ -69,31 +77,21 @@ def _run(cmd, verbose: bool) -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """The C library: nvcc alone, no torch and no Python headers."""
     if not force and up_to_date():
         return LIB
-    import torch
     os.makedirs(BUILD, exist_ok=True)
     tag = f".tmp{os.getpid()}"
-    objs = [os.path.join(BUILD, os.path.basename(src) + tag + ".o") for src in SOURCES + [EXT_SOURCE]]
-    lib, ext = LIB + tag, extension() + tag
-    tdir = os.path.dirname(torch.__file__)
-    includes = [INCLUDE, os.path.join(tdir, "include"), os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
-                sysconfig.get_paths()["include"],
-                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")]
+    objs = [os.path.join(BUILD, os.path.basename(src) + tag + ".o") for src in SOURCES]
+    lib = LIB + tag
     compiles = [[nvcc(), *ARCH, *FLAGS, "-Xptxas=-v", "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", o]
                 for src, o in zip(SOURCES, objs)]
-    compiles.append(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *[f"-I{p}" for p in includes], "-c",
-                     EXT_SOURCE, "-o", objs[-1]])
     try:
-        # the translation units side by side, then the links
+        # the translation units side by side, then the link
         with ThreadPoolExecutor(len(compiles)) as pool:
             list(pool.map(lambda cmd: _run(cmd, verbose), compiles))
-        _run([nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs[:-1], "-o", lib], verbose)
+        _run([nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", lib], verbose)
         os.replace(lib, LIB)
-        # (the loader finds the library beside the extension; torch is loaded already)
-        _run(["g++", "-shared", objs[-1], "-L" + BUILD, "-l:" + os.path.basename(LIB), "-L" + os.path.join(tdir, "lib"),
-              "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-o", ext], verbose)
-        os.replace(ext, extension())
     finally:
         for o in objs:
             if os.path.exists(o):
@@ -101,5 +99,37 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def build_extension(force: bool = False, verbose: bool = False) -> str:
+    """The extension for torch tensors, and the library it links to (side by side)."""
+    ext = extension()
+    if not force and up_to_date() and extension_up_to_date():
+        return ext
+    import torch
+    os.makedirs(BUILD, exist_ok=True)
+    tag = f".tmp{os.getpid()}"
+    obj, out = os.path.join(BUILD, os.path.basename(EXT_SOURCE) + tag + ".o"), ext + tag
+    tdir = os.path.dirname(torch.__file__)
+    includes = [INCLUDE, os.path.join(tdir, "include"), os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"],
+                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")]
+    try:
+        with ThreadPoolExecutor(2) as pool:
+            jobs = [pool.submit(build, force, verbose),
+                    pool.submit(_run, ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+                                       *[f"-I{p}" for p in includes], "-c", EXT_SOURCE, "-o", obj], verbose)]
+            for job in jobs:
+                job.result()
+        # (the loader finds the library beside the extension; torch is loaded already)
+        _run(["g++", "-shared", obj, "-L" + BUILD, "-l:" + os.path.basename(LIB), "-L" + os.path.join(tdir, "lib"),
+              "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-o", out], verbose)
+        os.replace(out, ext)
+    finally:
+        if os.path.exists(obj):
+            os.remove(obj)
+    return ext
+
+
 if __name__ == "__main__":
     print(build(force=True, verbose="--verbose" in sys.argv))
+    if importlib.util.find_spec("torch") is not None:
+        print(build_extension(force=not extension_up_to_date(), verbose="--verbose" in sys.argv))

@@ -112,11 +112,15 @@ _ext = None
 
 
 def load_tensor_calls():
-    """The extension behind the tensor-level calls (built first if needed)."""
+    """The extension behind the tensor-level calls (built first if needed).
+
+    The C entry points above need the library alone, neither this nor torch.
+    """
     global _ext
     if _ext is None:
-        load_library()  # builds what is missing, and comes first: the extension links to it
-        loader = importlib.machinery.ExtensionFileLoader("_ffn_torch", _build.extension())
+        path = _build.build_extension()
+        load_library()  # comes first: the extension links to it
+        loader = importlib.machinery.ExtensionFileLoader("_ffn_torch", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_ffn_torch", loader))
         loader.exec_module(module)
         _ext = module
