@@ -27,6 +27,10 @@
 extern "C" {
 #endif
 
+/* Largest M, N and K of these operators (2^31 - 4096: tiles and vectors that
+ * start inside a matrix end below 2^31). */
+#define POOT_FFN_MAX_SIZE 2147479552
+
 /* Activation of the gate. */
 enum poot_ffn_act {
     POOT_ACT_SILU = 0,       /* t / (1 + exp(-t)) */
@@ -47,8 +51,8 @@ enum poot_ffn_act {
  * place (base not 16-byte aligned, row pitch not a multiple of 8), are first
  * copied to 16-byte-pitched rows in the library's workspace.
  * M == 0 or N == 0 does nothing; K == 0 gives g = bg, u = bu.
- * Errors: POOT_ERR_INVALID_ARG (sizes outside [0, 2^31), NULL, ldx < K, an
- * unknown dtype or activation, only one of g and u, an output overlapping an
+ * Errors: POOT_ERR_INVALID_ARG (sizes outside [0, POOT_FFN_MAX_SIZE], NULL,
+ * ldx < K, an unknown dtype or activation, only one of g and u, an output overlapping an
  * input or another output); POOT_ERR_MISALIGNED (a pointer not 2-byte
  * aligned); otherwise as poot_linear_f16.
  */

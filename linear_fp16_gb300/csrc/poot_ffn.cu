@@ -31,7 +31,10 @@ namespace {
 using namespace poot;
 using namespace poot_host;
 
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+// Sizes: the kernels round them up to tiles, vectors and warps' shares of K (at
+// most 2304 more, the repacking's two spans of a row) in 32 bits
+constexpr int64_t kMaxDim = POOT_FFN_MAX_SIZE;
+static_assert(kMaxDim + 2304 < (int64_t(1) << 31), "32-bit index arithmetic");
 constexpr int kMaxDevices = 64;
 
 struct FfnDevice {
