@@ -8,8 +8,9 @@
  * synchronising; argument errors are found before any CUDA call and leave
  * everything untouched.  Matrices are row-major; a leading dimension (`ld*`,
  * elements between rows) of 0 means contiguous rows.  Where ld is larger, the
- * memory between two rows of an input may be read (never used).  Weights are
- * [out_features, in_features] and contiguous, read in place.
+ * memory between two rows of an input may be read (never used).  The ld of a
+ * single row is not used.  Weights are [out_features, in_features] and
+ * contiguous, read in place.
  *
  * Numerics: unlike poot_contract, whose steps round one by one, these
  * operators keep every value in FP32 from the sums to the result and round
@@ -52,7 +53,7 @@ enum poot_ffn_act {
  * copied to 16-byte-pitched rows in the library's workspace.
  * M == 0 or N == 0 does nothing; K == 0 gives g = bg, u = bu.
  * Errors: POOT_ERR_INVALID_ARG (sizes outside [0, POOT_FFN_MAX_SIZE], NULL,
- * ldx < K, an unknown dtype or activation, only one of g and u, an output overlapping an
+ * ldx < K, a matrix that spans more than 2^50 elements, an unknown dtype or activation, only one of g and u, an output overlapping an
  * input or another output); POOT_ERR_MISALIGNED (a pointer not 2-byte
  * aligned); otherwise as poot_linear_f16.
  */
@@ -81,7 +82,8 @@ POOT_API int poot_gated_linear(const poot_gated_linear_args* args, poot_stream_t
  * Any output pointer may be NULL (not wanted); the inputs it alone needs may
  * then be NULL too (x only for dwg / dwu, wg and wu only for dx).  Outputs are
  * contiguous.  M == 0 writes zeros to dwg, dwu, dbg and dbu; N == 0 zeros to
- * dx; K == 0 leaves dx, dwg and dwu without elements.  dg and du live in the library's workspace (4 * M * ceil8(N) bytes).
+ * dx; K == 0 leaves dx, dwg and dwu without elements.  dg and du live in the
+ * library's workspace (4 * M * ceil8(N) bytes).
  * Errors as poot_gated_linear; POOT_ERR_CUDA when no workspace can be had.
  */
 typedef struct poot_gated_linear_backward_args {

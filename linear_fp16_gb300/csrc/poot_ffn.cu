@@ -112,8 +112,23 @@ struct Span {
   int64_t bytes;
 };
 
+// Elements that a matrix spans, gaps between its rows included: no more than any
+// address space holds, so that byte counts and end addresses stay in 64 bits.
+constexpr int64_t kMaxSpan = int64_t(1) << 50;
+
 bool sizes_ok(int64_t M, int64_t N, int64_t K) {
-  return M >= 0 && N >= 0 && K >= 0 && M <= kMaxDim && N <= kMaxDim && K <= kMaxDim;
+  return M >= 0 && N >= 0 && K >= 0 && M <= kMaxDim && N <= kMaxDim && K <= kMaxDim && M * N <= kMaxSpan &&
+         M * K <= kMaxSpan && N * K <= kMaxSpan;
+}
+
+// The row pitch `ld` of an argument (0: contiguous rows) into *out; false: none
+// that a [rows, cols] matrix can have.  A single row has no pitch, whatever ld
+// says: it gets one that suits TMA.
+bool row_pitch(int64_t rows, int64_t cols, int64_t ld, int64_t* out) {
+  if (ld == 0) ld = cols;
+  if (ld < cols || (rows > 1 && ld > kMaxSpan / rows)) return false;
+  *out = rows > 1 ? ld : (cols + 7) / 8 * 8;
+  return true;
 }
 
 // bytes of a [rows, cols] matrix of 2-byte elements, rows ld apart
@@ -498,8 +513,10 @@ int gated_gemv(const poot_gated_linear_args& p, int64_t ldx, const FfnDevice& d,
 int gated_linear(const poot_gated_linear_args* ap, cudaStream_t stream) {
   if (ap == nullptr) return POOT_ERR_INVALID_ARG;
   const poot_gated_linear_args& p = *ap;
-  const int64_t M = p.M, N = p.N, K = p.K, ldx = p.ldx != 0 ? p.ldx : K;
-  if (!sizes_ok(M, N, K) || ldx < K || (p.dtype != POOT_DTYPE_F16 && p.dtype != POOT_DTYPE_BF16) ||
+  const int64_t M = p.M, N = p.N, K = p.K;
+  int64_t ldx;
+  if (!sizes_ok(M, N, K) || !row_pitch(M, K, p.ldx, &ldx) ||
+      (p.dtype != POOT_DTYPE_F16 && p.dtype != POOT_DTYPE_BF16) ||
       p.activation < POOT_ACT_SILU || p.activation > POOT_ACT_GELU_ERF || (p.g == nullptr) != (p.u == nullptr))
     return POOT_ERR_INVALID_ARG;
   if (M == 0 || N == 0) return POOT_OK;
@@ -630,9 +647,9 @@ int gated_linear_backward(const poot_gated_linear_backward_args* ap, cudaStream_
   if (ap == nullptr) return POOT_ERR_INVALID_ARG;
   const poot_gated_linear_backward_args& p = *ap;
   const int64_t M = p.M, N = p.N, K = p.K;
-  const int64_t ldx = p.ldx != 0 ? p.ldx : K, ld_dh = p.ld_dh != 0 ? p.ld_dh : N, ld_g = p.ld_g != 0 ? p.ld_g : N,
-                ld_u = p.ld_u != 0 ? p.ld_u : N;
-  if (!sizes_ok(M, N, K) || ldx < K || ld_dh < N || ld_g < N || ld_u < N ||
+  int64_t ldx, ld_dh, ld_g, ld_u;
+  if (!sizes_ok(M, N, K) || !row_pitch(M, K, p.ldx, &ldx) || !row_pitch(M, N, p.ld_dh, &ld_dh) ||
+      !row_pitch(M, N, p.ld_g, &ld_g) || !row_pitch(M, N, p.ld_u, &ld_u) ||
       (p.dtype != POOT_DTYPE_F16 && p.dtype != POOT_DTYPE_BF16) || p.activation < POOT_ACT_SILU ||
       p.activation > POOT_ACT_GELU_ERF)
     return POOT_ERR_INVALID_ARG;
@@ -735,8 +752,9 @@ int linear_backward(const poot_linear_backward_args* ap, cudaStream_t stream) {
   if (ap == nullptr) return POOT_ERR_INVALID_ARG;
   const poot_linear_backward_args& p = *ap;
   const int64_t M = p.M, N = p.N, K = p.K;
-  const int64_t ldx = p.ldx != 0 ? p.ldx : K, ld_dy = p.ld_dy != 0 ? p.ld_dy : N;
-  if (!sizes_ok(M, N, K) || ldx < K || ld_dy < N || (p.dtype != POOT_DTYPE_F16 && p.dtype != POOT_DTYPE_BF16))
+  int64_t ldx, ld_dy;
+  if (!sizes_ok(M, N, K) || !row_pitch(M, K, p.ldx, &ldx) || !row_pitch(M, N, p.ld_dy, &ld_dy) ||
+      (p.dtype != POOT_DTYPE_F16 && p.dtype != POOT_DTYPE_BF16))
     return POOT_ERR_INVALID_ARG;
   if (M > 0 && N > 0 && (p.dx != nullptr || p.dw != nullptr || p.db != nullptr)) {
     if (p.dy == nullptr || (K > 0 && p.dx != nullptr && p.w == nullptr) || (K > 0 && p.dw != nullptr && p.x == nullptr))

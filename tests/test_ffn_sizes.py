@@ -75,3 +75,48 @@ def test_rows_of_nearly_31_bits(K):
     n = len(at)
     for j, got in enumerate((g, u)):
         assert got.tolist() == [[float((j + 1) * n * (n + 1) // 2), float(sum((i + 1) * (i % 3 - 1 + j) for i in range(n)))]]
+
+
+PITCHES = [(gated, "ldx"), (gated_bwd, "ldx"), (gated_bwd, "ld_dh"), (gated_bwd, "ld_g"), (gated_bwd, "ld_u"),
+           (linear_bwd, "ldx"), (linear_bwd, "ld_dy")]
+
+
+@pytest.mark.parametrize("call,ld", PITCHES)
+def test_pitches_that_no_matrix_has(call, ld):
+    """Byte counts of such rows wrapped, and with them the overlap checks."""
+    for v in (1 << 50, 1 << 61, 1 << 62, (1 << 63) - 1):
+        assert call(**{ld: v}) == INV, v
+    assert call(**{ld: -1}) == INV
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("big", ["MN", "MK", "NK"])
+def test_matrices_beyond_any_address_space(call, big):
+    assert call(**{d: TOP if d in big else 1 for d in "MNK"}) == INV
+
+
+@no_gpu
+@pytest.mark.parametrize("call,ld", PITCHES)
+def test_a_single_row_has_no_pitch(call, ld):
+    assert call(**{"M": 1, ld: (1 << 63) - 1}) == L.POOT_ERR_CUDA
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,K", [(48, 40), (45, 37)])
+def test_gradients_of_a_single_row_at_any_pitch(N, K):
+    dev = "cuda:0"
+    g = torch.Generator().manual_seed(N)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g).half()
+    dy, x, w = ints(1, N), ints(1, K), ints(N, K)
+    t = [v.to(dev) for v in (dy, x, w)]
+    out = [torch.empty(s, dtype=torch.float16, device=dev) for s in ((1, K), (N, K), (N,))]
+    for ld in (0, 1 << 20, (1 << 20) + 1, 1 << 45):
+        for o in out:
+            o.fill_(float("nan"))
+        rc = L.poot_linear_backward(L.LinearBackwardArgs(
+            dy=t[0].data_ptr(), x=t[1].data_ptr(), w=t[2].data_ptr(), dx=out[0].data_ptr(), dw=out[1].data_ptr(),
+            db=out[2].data_ptr(), M=1, N=N, K=K, ld_dy=ld, ldx=ld), 0)
+        torch.cuda.synchronize()
+        assert rc == L.POOT_OK and L.poot_linear_device_status(0) == L.POOT_OK, ld
+        for o, r in zip(out, (dy.double() @ w.double(), dy.double().T @ x.double(), dy.double()[0])):
+            assert torch.equal(o.cpu(), r.half()), ld
