@@ -87,8 +87,9 @@ __global__ void __launch_bounds__(kGemvThreads) gemv_f16_kernel(const GemvArgs a
 #pragma unroll
   for (int m = 0; m < MT; ++m) acc[m] = 0.0f;
 
-  for (int kc0 = 0; kc0 < K; kc0 += kc) {
-    const int len = min(kc, K - kc0);
+  // (unsigned: the last chunk may end past 2^31)
+  for (uint32_t kc0 = 0; kc0 < (uint32_t)K; kc0 += (uint32_t)kc) {
+    const int len = (int)min((uint32_t)kc, (uint32_t)K - kc0);
     __syncthreads();  // the previous chunk has been consumed
     if constexpr (VEC) {
       const int vpr = kc / 8;  // 16-byte vectors per staged row
@@ -348,14 +349,15 @@ __global__ void __launch_bounds__(WARPS * 32) gemv_f16_mma_kernel(const GemvArgs
     n0 = ((int)blockIdx.x - grp * tpg) * 16;
   }
   const int nA = n0 + g, nB = n0 + g + 8;
-  // this warp's K slice, a multiple of 32
-  const int slice = ((K + WARPS * 32 - 1) / (WARPS * 32)) * 32;
-  const int k_begin = min(K, warp * slice);
-  const int k_end = min(K, k_begin + slice);
-  const __half* __restrict__ wa = a.w + (size_t)(nA < N ? nA : 0) * K;
-  const __half* __restrict__ wb = a.w + (size_t)(nB < N ? nB : 0) * K;
-  const __half* __restrict__ x0 = a.x + (size_t)(g < M ? g : 0) * K;
-  const __half* __restrict__ x1 = a.x + (size_t)(g + 8 < M ? g + 8 : 0) * K;
+  // this warp's K slice, a multiple of 32 (K rounded up may pass 2^31; from
+  // here on k counts from the slice's start)
+  const uint32_t slice = (((uint32_t)K + WARPS * 32 - 1) / (WARPS * 32)) * 32;
+  const uint32_t k_begin = min((uint32_t)K, (uint32_t)warp * slice);
+  const int k_end = (int)min((uint32_t)K - k_begin, slice);
+  const __half* __restrict__ wa = a.w + (size_t)(nA < N ? nA : 0) * K + k_begin;
+  const __half* __restrict__ wb = a.w + (size_t)(nB < N ? nB : 0) * K + k_begin;
+  const __half* __restrict__ x0 = a.x + (size_t)(g < M ? g : 0) * K + k_begin;
+  const __half* __restrict__ x1 = a.x + (size_t)(g + 8 < M ? g + 8 : 0) * K + k_begin;
   if constexpr (WIDE) {
     // this group's W rows and x rows
     wa += (size_t)grp * N * K;
@@ -366,9 +368,9 @@ __global__ void __launch_bounds__(WARPS * 32) gemv_f16_mma_kernel(const GemvArgs
   const bool okA = nA < N, okB = nB < N, okx0 = g < M, okx1 = (NT > 1) && (g + 8 < M);
   // start this warp's K slice of its 16 W rows towards L2 while the
   // previous grid drains (lane 4g prefetches rows nA and nB)
-  if (a.prefetch && t == 0 && k_end > k_begin) {
-    if (okA) prefetch_l2_bulk(wa + k_begin, (uint32_t)(k_end - k_begin) * 2u);
-    if (okB) prefetch_l2_bulk(wb + k_begin, (uint32_t)(k_end - k_begin) * 2u);
+  if (a.prefetch && t == 0 && k_end > 0) {
+    if (okA) prefetch_l2_bulk(wa, (uint32_t)k_end * 2u);
+    if (okB) prefetch_l2_bulk(wb, (uint32_t)k_end * 2u);
   }
   grid_dep_wait();
   grid_dep_launch();
@@ -389,7 +391,7 @@ __global__ void __launch_bounds__(WARPS * 32) gemv_f16_mma_kernel(const GemvArgs
   const uint4 zero = make_uint4(0, 0, 0, 0);
 
   constexpr int U = NT == 1 ? 8 : 4;  // steps of 32 along K per batch
-  for (int k0 = k_begin; k0 < k_end; k0 += 32 * U) {
+  for (int k0 = 0; k0 < k_end; k0 += 32 * U) {
     uint4 va[U], vb[U], vx[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
