@@ -604,7 +604,7 @@ int launch_gemv(int variant, const DeviceState& st, const void* x, const void* w
       e = launch(gemv_f16_rows_kernel<1>, rgrid, dim3(kGemvRowThreads), 0, stream, a);
     else
       e = launch(gemv_f16_rows_kernel<2>, rgrid, dim3(kGemvRowThreads), 0, stream, a);
-  } else if (variant == POOT_VARIANT_GEMV && wpr_req == 0) {
+  } else if (variant == POOT_VARIANT_GEMV && wpr_req == 0 && K <= kGemvMmaMaxK) {
     // 3 <= M <= 16 on the tensor cores, 16 rows of W per block; 16 warps
     // along K below two such blocks per SM, the L2 prefetch up to two
     // blocks for every three SMs
@@ -806,7 +806,7 @@ int contract(const void* x, const void* w, const void* b, void* y, int64_t G, in
   }
   // M <= 16 (operands readable by 16-byte loads, no GEMM split asked for):
   // the GEMV kernels with the per-element epilogue, any number of groups
-  const bool gemv_ok = M <= POOT_GEMV_MAX_M && xw_tma_ok(x, w, K);
+  const bool gemv_ok = M <= POOT_GEMV_MAX_M && xw_tma_ok(x, w, K) && (M <= 2 || K <= kGemvMmaMaxK);
   if (o.variant == POOT_VARIANT_GEMV && !gemv_ok) return POOT_ERR_INVALID_ARG;
   if (o.variant == POOT_VARIANT_GEMV || (o.variant == POOT_VARIANT_AUTO && gemv_ok && o.gemm_split_k <= 1)) {
     int dev = 0;
