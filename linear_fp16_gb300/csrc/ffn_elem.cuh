@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kGateThreads, 4) gate_grad_kernel(const __grid
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float v, d;
-      act_both_t<decltype(act)::value>(g[j], v, d);
+      act_both_t<decltype(act)::value, DT>(g[j], v, d);
       dg[j] = dh[j] * u[j] * d;
       du[j] = dh[j] * v;
       if constexpr (SUMS) {
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(256) ffn_reduce_kernel(const FfnReduceArgs a) 
           if (a.bias[0] != nullptr) s[0][j] += ep_widen(__ldg(a.bias[0] + col + j), dt);
           if (a.bias[1] != nullptr) s[1][j] += ep_widen(__ldg(a.bias[1] + col + j), dt);
         }
-        h[j] = j < n ? act_value(a.act, s[0][j]) * s[1][j] : 0.0f;
+        h[j] = j < n ? act_value<kEpiBf16>(a.act, s[0][j]) * s[1][j] : 0.0f;
       }
       if (a.y[1] != nullptr) { put(a.y[1], s[0]); put(a.y[2], s[1]); }
       put(a.y[0], h);
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(256) gated_bias_kernel(const FfnReduceArgs a) 
       a.y[1][i] = (uint16_t)gu;
       a.y[2][i] = (uint16_t)(gu >> 16);
     }
-    a.y[0][i] = (uint16_t)ep_pack(act_value(a.act, g) * u, 0.0f, dt);
+    a.y[0][i] = (uint16_t)ep_pack(act_value<kEpiBf16>(a.act, g) * u, 0.0f, dt);
   }
 }
 

@@ -59,7 +59,7 @@ __device__ __forceinline__ void gg_finish(const GatedGemvArgs& a, float g, float
     a.y[1][at] = (uint16_t)gu;
     a.y[2][at] = (uint16_t)(gu >> 16);
   }
-  a.y[0][at] = (uint16_t)ep_pack_t<DT>(act_value(a.act, g) * u, 0.0f);
+  a.y[0][at] = (uint16_t)ep_pack_t<DT>(act_value<DT>(a.act, g) * u, 0.0f);
 }
 
 // NT: 8-column blocks of tokens (1: M <= 8, 2: M <= 16)
