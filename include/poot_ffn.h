@@ -17,7 +17,10 @@
  * once to the head dtype (binary16 or bfloat16).  The one exception: the
  * gradients of gate and up (dg, du below) are rounded to the head dtype
  * before they are multiplied with the weights and x, as operands of 16-bit
- * products.  Sums are FP32 in a fixed order: equal calls give equal bits.
+ * products.  Sums are FP32 in a fixed order: equal calls give equal bits.  The
+ * tensor core truncates towards zero where it adds products to a sum, so sums of
+ * many terms of one sign come out low, whatever their length by less than an
+ * eighth of the result's rounding (M > 16).
  */
 #ifndef POOT_FFN_H
 #define POOT_FFN_H

@@ -14,11 +14,11 @@
 // A persistent CTA (or a CTA pair on one 256-row tile, 2-SM MMA) per SM walks
 // output tiles.  Warp roles as in the linear's GEMM: epilogue warps, one
 // thread that issues the MMAs, one or two that issue the TMA loads.  A sum stays
-// in TMEM over the whole K range (FP32 accumulators): unlike the linear's
-// kernel there is no promotion into registers every 1024 elements, because
-// these operators' outputs are rounded once from the FP32 value to 11 or 8
-// bits and carry no 2-ulp rule; the accumulators of two tiles fit TMEM, so
-// the epilogue of a tile runs under the main loop of the next.  Bound by the
+// in TMEM (FP32 accumulators) over a chunk of K, unlike in the linear's kernel,
+// which promotes every 1024 elements: these operators' outputs are rounded once
+// from the FP32 value to 11 or 8 bits and carry no 2-ulp rule (chunks: see
+// ffn_chunk_k).  The accumulators of two tiles fit TMEM, so the epilogue of a
+// tile runs under the main loop of the next.  Bound by the
 // tensor pipe under the power cap where K is long (GB300, bfloat16, 8192 x
 // 14336 x 4096: gated with g and u 1.13 ms, 1.70 PFLOP/s; dx and both dW 2.24
 // ms, 1.72 PFLOP/s), by operand loads from L2 (about 80 GB/s per SM) and the
@@ -57,6 +57,17 @@ constexpr int kFfnBK = 64;  // one 128-byte swizzle row
 __host__ __device__ constexpr int ffn_epi_warps(bool gated) { return gated ? 8 : 16; }
 __host__ __device__ constexpr int ffn_threads(bool gated) { return (ffn_epi_warps(gated) + (gated ? 3 : 2)) * 32; }
 constexpr int kFfnMaxBN = 256;
+// Elements of K summed in TMEM.  An MMA truncates where it adds 16 products to
+// the running sum, always towards zero: sums of one sign come out low by 6.3e-9
+// of themselves per term (mean over many outputs on GB300: 5.4e-5 over 8192 terms,
+// 1.7e-3 over 262144, where one rounding is 4.9e-4 in binary16 and 3.9e-3 in
+// bfloat16).  Chunks keep that at an eighth of the rounding in binary16 and at a
+// twentieth in bfloat16 (measured: 5e-5 and 2e-4 at any length).  Longer sums
+// are added up over chunks in FP32, rounded to nearest, in a scratch of the CTA
+// (128 KB, from L2) by the epilogue warps under the main loop of the next chunk.
+// (8192 for bfloat16 too: 2480 -> 2560 us for the gradients of 8192 x 14336 x
+// 4096, whose dx sums 28672 terms.)
+__host__ __device__ constexpr int ffn_chunk_k(int dtype) { return dtype == kEpiBf16 ? 32768 : 8192; }
 constexpr int kFfnMaxStages = 8;
 constexpr uint32_t kFfnTmemCols = 2 * kFfnMaxBN;
 
@@ -305,7 +316,9 @@ struct FfnGemmArgs {
   FfnJob job[2];     // gated: job 0; gradients: dx, dW (either may have no tiles)
   const uint16_t* bias[2];  // gated: bg, bu or nullptr
   FfnBiasGrad bias_grad;
+  float4* scratch;   // sums of earlier chunks, kFfnScratchBytes a CTA; nullptr: no sum has two
 };
+constexpr int kFfnScratchBytes = kFfnBM * kFfnMaxBN * 4;
 
 // The tiles of one CTA (or pair): its round-robin share of the job with the
 // longer tiles (deal.first); then, where that leaves it one tile short of
@@ -353,6 +366,8 @@ struct FfnLayout {
 // per four leaves gaps in the tensor pipe); a single CTA takes one, for a
 // deeper ring on the small problems it serves.
 __host__ __device__ constexpr int ffn_sub(int cl) { return cl == 2 ? 2 : 1; }
+// K blocks of a chunk
+__host__ __device__ constexpr int ffn_chunk_kb(int cl, int dtype) { return ffn_chunk_k(dtype) / (kFfnBK * ffn_sub(cl)); }
 __host__ __device__ constexpr int ffn_a_bytes(int cl) { return kFfnBM * kFfnBK * 2 * ffn_sub(cl); }
 __host__ __device__ constexpr int ffn_b_bytes(int cl, int bn) { return bn / cl * kFfnBK * 2 * ffn_sub(cl); }
 __host__ __device__ constexpr int ffn_stages(int cl, int bn) {
@@ -468,7 +483,30 @@ __device__ __forceinline__ void ffn_bias_grad(const FfnBiasGrad& b, float* red, 
   }
 }
 
-template <int CL, bool GATED, int DT>
+// A lane's 32 sums of a box in the scratch of FfnGemmArgs: `p` is its first
+// float4, the next ones follow 32 apart (a warp's lanes side by side).
+__device__ __forceinline__ void ffn_store_scratch(float4* p, const uint32_t (&r)[32]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    p[j * 32] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
+                            __uint_as_float(r[4 * j + 3]));
+}
+// r += what stands there
+__device__ __forceinline__ void ffn_add_scratch(const float4* p, uint32_t (&r)[32]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float4 v = p[j * 32];
+    r[4 * j] = __float_as_uint(v.x + __uint_as_float(r[4 * j]));
+    r[4 * j + 1] = __float_as_uint(v.y + __uint_as_float(r[4 * j + 1]));
+    r[4 * j + 2] = __float_as_uint(v.z + __uint_as_float(r[4 * j + 2]));
+    r[4 * j + 3] = __float_as_uint(v.w + __uint_as_float(r[4 * j + 3]));
+  }
+}
+
+// CHUNKS: some sum has more than one chunk (host: FfnSpace).  A form of its own,
+// because the code for it costs the others 2 - 3% (1024 x 1024 x 768 gradients
+// 16.4 -> 17.0 us).
+template <int CL, bool GATED, int DT, bool CHUNKS>
 __global__ void __launch_bounds__(ffn_threads(GATED), 1)
     ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemmArgs args) {
   using L = FfnLayout;
@@ -642,33 +680,38 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
           const uint32_t q = job.by_out.div((uint32_t)sched.tile(ji, ti));
           const int s = (int)(q - job.by_split.div(q) * (uint32_t)job.split);
           const int kb0 = s * job.kb_split, kb1 = min(job.kb_total, kb0 + job.kb_split);
-          if (!mbar_wait(bar_cempty(buf), buf_phase ^ 1u, abort_flag)) { ok = false; break; }
-          tc_fence_after_sync();
-          const uint32_t d_tmem = tmem_base + (uint32_t)(buf * kFfnMaxBN);
-          uint32_t acc = 0;
-          for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait(bar_full(stage), phase, abort_flag)) { ok = false; break; }
+          for (int kc = kb0;;) {  // chunks
+            const int kend = CHUNKS ? min(kb1, kc + ffn_chunk_kb(CL, DT)) : kb1;
+            if (!mbar_wait(bar_cempty(buf), buf_phase ^ 1u, abort_flag)) { ok = false; break; }
             tc_fence_after_sync();
+            const uint32_t d_tmem = tmem_base + (uint32_t)(buf * kFfnMaxBN);
+            uint32_t acc = 0;
+            for (int kb = kc; kb < kend; ++kb) {
+              if (!mbar_wait(bar_full(stage), phase, abort_flag)) { ok = false; break; }
+              tc_fence_after_sync();
 #pragma unroll
-            for (int h = 0; h < SUB; ++h) {
-              const uint32_t sa = stage_a(stage) + (uint32_t)(h * A_SUB), sb = stage_b(stage) + (uint32_t)(h * B_SUB);
-              const uint64_t ad = A_MN ? sdesc_mnmajor_sw128(sa) : sdesc_kmajor_sw128(sa);
-              const uint64_t bd = B_MN ? sdesc_mnmajor_sw128(sb) : sdesc_kmajor_sw128(sb);
+              for (int h = 0; h < SUB; ++h) {
+                const uint32_t sa = stage_a(stage) + (uint32_t)(h * A_SUB), sb = stage_b(stage) + (uint32_t)(h * B_SUB);
+                const uint64_t ad = A_MN ? sdesc_mnmajor_sw128(sa) : sdesc_kmajor_sw128(sa);
+                const uint64_t bd = B_MN ? sdesc_mnmajor_sw128(sb) : sdesc_kmajor_sw128(sb);
 #pragma unroll
-              for (int k = 0; k < kFfnBK / 16; ++k) {
-                if constexpr (PAIR) umma_f16_pair(d_tmem, ad + AK * k, bd + BKS * k, idesc, acc);
-                else umma_f16(d_tmem, ad + AK * k, bd + BKS * k, idesc, acc);
-                acc = 1u;
+                for (int k = 0; k < kFfnBK / 16; ++k) {
+                  if constexpr (PAIR) umma_f16_pair(d_tmem, ad + AK * k, bd + BKS * k, idesc, acc);
+                  else umma_f16(d_tmem, ad + AK * k, bd + BKS * k, idesc, acc);
+                  acc = 1u;
+                }
               }
+              if constexpr (PAIR) umma_commit_pair(bar_empty(stage), 3);
+              else umma_commit(bar_empty(stage));
+              if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
-            if constexpr (PAIR) umma_commit_pair(bar_empty(stage), 3);
-            else umma_commit(bar_empty(stage));
-            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            if (!ok) break;
+            if constexpr (PAIR) umma_commit_pair(bar_cfull(buf), 3);
+            else umma_commit(bar_cfull(buf));
+            if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+            if (!CHUNKS || (kc = kend) >= kb1) break;
           }
           if (!ok) break;
-          if constexpr (PAIR) umma_commit_pair(bar_cfull(buf), 3);
-          else umma_commit(bar_cfull(buf));
-          if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
         }
       };
       if (GATED || args.deal.first == 0) {
@@ -792,11 +835,22 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
         }
       };
 
-      const bool got = mbar_wait_long(bar_cfull(buf), buf_phase, abort_flag);
-      if (!__all_sync(0xffffffffu, got)) break;
-      tc_fence_after_sync();
-      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kFfnMaxBN);
+      const int sum_kb = CHUNKS ? min(job.kb_split, job.kb_total - s * job.kb_split) : 0;
+      const bool chunked = CHUNKS && sum_kb > ffn_chunk_kb(CL, DT);
+      uint32_t taddr;
+      auto wait_sums = [&] {
+        const bool got = mbar_wait_long(bar_cfull(buf), buf_phase, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) return false;
+        tc_fence_after_sync();
+        taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kFfnMaxBN);
+        return true;
+      };
       const bool rows_in = m0 < M;  // warp-uniform
+      // The scratch of accumulator columns 32 b .. 32 b + 31, this warp's rows: a
+      // lane writes and reads its own row's 32 sums there.  (Gated: gate columns, then up.)
+      auto scratch = [&](int b) {
+        return args.scratch + (size_t)blockIdx.x * (kFfnScratchBytes / 16) + ((b * 4 + q) * 8) * 32 + lane;
+      };
       // this warp is done with the accumulator: its sums are in registers
       auto release = [&]() {
         tc_fence_before_sync();
@@ -806,6 +860,29 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
           else mbar_arrive(bar_cempty(buf));
         }
       };
+      bool ok = true;
+      if constexpr (CHUNKS) {
+        // all chunks but the last: added up in the scratch
+#pragma unroll 1
+        for (int c = 0; c < (sum_kb - 1) / ffn_chunk_kb(CL, DT); ++c) {
+          ok = wait_sums();
+          if (!ok) break;
+#pragma unroll 1
+          for (int bx = part; bx < boxes && rows_in && n0 + bx * 32 < N; bx += EPI_WARPS / 4) {
+#pragma unroll 1
+            for (int b = bx; b < (GATED ? BN / 32 : bx + 1); b += BN / 64) {
+              uint32_t r[32];
+              tmem_ld_32x32b_x32(taddr + (uint32_t)(b * 32), r);
+              tmem_ld_wait();
+              if (c > 0) ffn_add_scratch(scratch(b), r);
+              ffn_store_scratch(scratch(b), r);
+            }
+          }
+          release();
+          if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+        }
+      }
+      if (!ok || !wait_sums()) break;
       bool held = true;
 #pragma unroll 1
       for (int bx = part; bx < boxes; bx += EPI_WARPS / 4) {
@@ -828,6 +905,10 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
             __syncwarp();
           }
           tmem_ld_wait();
+          if (chunked) {
+            ffn_add_scratch(scratch(bx), r);
+            ffn_add_scratch(scratch(BN / 64 + bx), r2);
+          }
           const bool last_box = bx + EPI_WARPS / 4 >= boxes;
           if (job.split > 1) {
             if (last_box) release();
@@ -868,6 +949,7 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
           else gate(std::integral_constant<int, kActGeluErf>{});
         } else {
           tmem_ld_wait();
+          if (chunked) ffn_add_scratch(scratch(bx), r);
           if (bx + EPI_WARPS / 4 >= boxes) {
             release();
             held = false;

@@ -49,11 +49,13 @@ FfnDevice g_devices[kMaxDevices];
 
 template <int CL, bool GATED>
 cudaError_t set_attr() {
-  const cudaError_t e = cudaFuncSetAttribute(ffn_gemm_kernel<CL, GATED, kEpiF16>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, FfnLayout::DYN_BYTES);
-  return e != cudaSuccess ? e
-                          : cudaFuncSetAttribute(ffn_gemm_kernel<CL, GATED, kEpiBf16>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, FfnLayout::DYN_BYTES);
+  for (auto kernel : {ffn_gemm_kernel<CL, GATED, kEpiF16, false>, ffn_gemm_kernel<CL, GATED, kEpiF16, true>,
+                      ffn_gemm_kernel<CL, GATED, kEpiBf16, false>, ffn_gemm_kernel<CL, GATED, kEpiBf16, true>}) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FfnLayout::DYN_BYTES);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 template <int NT, int DT>
@@ -317,16 +319,42 @@ struct FfnEpilogue {
 
 template <int CL, bool GATED>
 cudaError_t launch_ffn(const FfnMaps& m, const FfnGemmArgs& a, bool bf16, int64_t units, cudaStream_t stream) {
-  return launch_clustered(bf16 ? ffn_gemm_kernel<CL, GATED, kEpiBf16> : ffn_gemm_kernel<CL, GATED, kEpiF16>,
+  auto pick = [&](auto chunks) {
+    constexpr bool C = decltype(chunks)::value;
+    return bf16 ? ffn_gemm_kernel<CL, GATED, kEpiBf16, C> : ffn_gemm_kernel<CL, GATED, kEpiF16, C>;
+  };
+  return launch_clustered(a.scratch != nullptr ? pick(std::true_type{}) : pick(std::false_type{}),
                           dim3(static_cast<unsigned>(units * CL)), dim3(ffn_threads(GATED)), FfnLayout::DYN_BYTES, stream,
                           unsigned(CL), m, a);
 }
 
+// K blocks of product `q` under plan `p`: of one part, of a range (its split's
+// ranges but the last)
+inline int64_t plan_kb_part(const FfnProduct& q, const FfnPlan& p) { return ceil_div(q.kext, kFfnBK * ffn_sub(p.cl)); }
+inline int64_t plan_kb_split(const FfnProduct& q, const FfnPlan& p, int i) {
+  return ceil_div(plan_kb_part(q, p) * q.parts, p.split[i]);
+}
+
+// Workspace of products under plan `p`: each one's partial sums, then the
+// CTAs' scratch where a sum has more than one chunk (see FfnGemmArgs).
+struct FfnSpace {
+  size_t partial[2] = {0, 0}, scratch = 0;
+  size_t bytes() const { return partial[0] + partial[1] + scratch; }
+  FfnSpace(const FfnProduct* const* ps, int count, const FfnPlan& p, int dtype, int sms) {
+    for (int i = 0; i < count; ++i) {
+      partial[i] = ps[i]->partial_bytes(p.split[i]);
+      if (plan_kb_split(*ps[i], p, i) > ffn_chunk_kb(p.cl, dtype)) scratch = size_t(sms) * kFfnScratchBytes;
+    }
+  }
+};
+
 // Runs up to two products (dx and dW) in one launch, with the
 // bias gradients `bg` (may be nullptr) beside them, then the second halves of
-// split products.  `partial[i]`: workspace of product i.
+// split products.  `ws`: workspace as FfnSpace lays it out.
 int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const FfnEpilogue& ep,
-                 const FfnBiasGrad* bg, float* const* partial, const FfnDevice& d, cudaStream_t stream) {
+                 const FfnBiasGrad* bg, char* ws, const FfnDevice& d, cudaStream_t stream) {
+  const FfnSpace space(ps, count, p, ep.dtype, d.sms);
+  float* const partial[2] = {reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + space.partial[0])};
   const bool bf16 = ep.dtype == POOT_DTYPE_BF16;
   FfnGemmArgs a;
   FfnMaps m;
@@ -340,7 +368,8 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
   a.save = ep.save;
   for (int i = 0; i < 2; ++i) a.bias[i] = static_cast<const uint16_t*>(ep.bias[i]);
   if (bg != nullptr) a.bias_grad = *bg;
-  const int64_t units_max = d.sms / p.cl, bk = kFfnBK * ffn_sub(p.cl);
+  if (space.scratch != 0) a.scratch = reinterpret_cast<float4*>(ws + space.partial[0] + space.partial[1]);
+  const int64_t units_max = d.sms / p.cl;
   int64_t total = 0;
   for (int i = 0; i < count; ++i) {
     const FfnProduct& q = *ps[i];
@@ -350,12 +379,12 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
     j.N = static_cast<int>(q.cols);
     j.num_m = static_cast<int>(ceil_div(q.rows, kFfnBM * p.cl));
     j.num_n = static_cast<int>(ceil_div(q.cols, a.cols));
-    const int64_t kb_part = ceil_div(q.kext, bk);
+    const int64_t kb_part = plan_kb_part(q, p);
     if (kb_part * q.parts > INT32_MAX) return POOT_ERR_INVALID_ARG;
     // (one part: the part index never advances)
     j.kb_part = q.parts > 1 ? static_cast<int>(kb_part) : INT32_MAX;
     j.kb_total = static_cast<int>(kb_part * q.parts);
-    j.kb_split = static_cast<int>(ceil_div(j.kb_total, p.split[i]));
+    j.kb_split = static_cast<int>(plan_kb_split(q, p, i));
     j.split = static_cast<int>(ceil_div(j.kb_total, j.kb_split));  // no empty range
     // M blocks walked together: their A rows within 32 MB of L2, and at least
     // eight, about the square of tiles that run at one time
@@ -567,18 +596,17 @@ int gated_linear(const poot_gated_linear_args* ap, cudaStream_t stream) {
   pk.need(&q.a[0]);
   pk.need(&q.b[0]);
   pk.need(&q.b[1]);
-  const size_t partial = q.partial_bytes(plan.split[0]);
+  const size_t space = FfnSpace(ps, 1, plan, p.dtype, d->sms).bytes();
   WorkspaceLease lease;
-  if (partial + pk.bytes > 0) {
-    lease = stream_workspace(d->dev, stream, partial + pk.bytes);
+  if (space + pk.bytes > 0) {
+    lease = stream_workspace(d->dev, stream, space + pk.bytes);
     if (lease.ptr == nullptr) return cuda_fail(cudaErrorMemoryAllocation);
   }
   char* ws = static_cast<char*>(lease.ptr);
-  pk.place(ws + partial);
+  pk.place(ws + space);
   const cudaError_t e = pk.run(d->sms, stream);
   if (e != cudaSuccess) return finish(lease, cuda_fail(e));
-  float* const part[1] = {reinterpret_cast<float*>(ws)};
-  return finish(lease, run_products(ps, 1, plan, ep, nullptr, part, *d, stream));
+  return finish(lease, run_products(ps, 1, plan, ep, nullptr, ws, *d, stream));
 }
 
 int zero(void* p, int64_t bytes, cudaStream_t stream) {
@@ -628,18 +656,9 @@ struct Grads {
     }
     plan = plan_ffn(ps, count, sms);
   }
-  size_t partial_bytes() const {
-    size_t b = 0;
-    for (int i = 0; i < count; ++i) b += ps[i]->partial_bytes(plan.split[i]);
-    return b;
-  }
+  size_t space(int dtype, int sms) const { return FfnSpace(ps, count, plan, dtype, sms).bytes(); }
   int run(const FfnEpilogue& ep, const FfnBiasGrad* bg, char* ws, const FfnDevice& dev, cudaStream_t stream) const {
-    float* part[2] = {nullptr, nullptr};
-    for (int i = 0; i < count; ++i) {
-      part[i] = reinterpret_cast<float*>(ws);
-      ws += ps[i]->partial_bytes(plan.split[i]);
-    }
-    return run_products(ps, count, plan, ep, bg, part, dev, stream);
+    return run_products(ps, count, plan, ep, bg, ws, dev, stream);
   }
 };
 
@@ -691,15 +710,15 @@ int gated_linear_backward(const poot_gated_linear_backward_args* ap, cudaStream_
   const Operand dmat[2] = {{nullptr, M, N, Np}, {nullptr, M, N, Np}}, w[2] = {{p.wg, N, K, K}, {p.wu, N, K, K}};
   void* const dwp[2] = {p.dwg, p.dwu};
   g.make(2, dmat, w, {p.x, M, K, ldx}, p.dx, dwp, M, N, K, d->sms, &pk);
-  const size_t dbytes = round256(size_t(M) * Np * 2), partial = g.partial_bytes();
+  const size_t dbytes = round256(size_t(M) * Np * 2), space = g.space(p.dtype, d->sms);
   const size_t sbytes = want_db ? round256(size_t(row_blocks) * 2 * Np * 4) : 0;
-  WorkspaceLease lease = stream_workspace(d->dev, stream, 2 * dbytes + partial + sbytes + pk.bytes);
+  WorkspaceLease lease = stream_workspace(d->dev, stream, 2 * dbytes + space + sbytes + pk.bytes);
   if (lease.ptr == nullptr) return cuda_fail(cudaErrorMemoryAllocation);
   char* const ws = static_cast<char*>(lease.ptr);
   char* const dgp = ws;
   char* const dup = ws + dbytes;
-  float* const sums = reinterpret_cast<float*>(ws + 2 * dbytes + partial);
-  pk.place(ws + 2 * dbytes + partial + sbytes);
+  float* const sums = reinterpret_cast<float*>(ws + 2 * dbytes + space);
+  pk.place(ws + 2 * dbytes + space + sbytes);
   g.dx.a[0].p = dgp;
   g.dx.a[1].p = dup;
   for (int i = 0; i < g.dw.outputs; ++i) g.dw.a[i].p = g.dw.y[i] == p.dwg ? dgp : dup;
@@ -779,14 +798,14 @@ int linear_backward(const poot_linear_backward_args* ap, cudaStream_t stream) {
   const Operand w = {p.w, N, K, K};
   g.make(1, &dy, &w, {p.x, M, K, ldx}, p.dx, &p.dw, M, N, K, d->sms, &pk);
   if (g.count > 0) pk.need(&dy);
-  const size_t partial = g.partial_bytes();
+  const size_t space = g.space(p.dtype, d->sms);
   WorkspaceLease lease;
-  if (partial + pk.bytes > 0) {
-    lease = stream_workspace(d->dev, stream, partial + pk.bytes);
+  if (space + pk.bytes > 0) {
+    lease = stream_workspace(d->dev, stream, space + pk.bytes);
     if (lease.ptr == nullptr) return cuda_fail(cudaErrorMemoryAllocation);
   }
   char* const ws = static_cast<char*>(lease.ptr);
-  pk.place(ws + partial);
+  pk.place(ws + space);
   g.dx.a[0] = g.dw.a[0] = dy;
   const cudaError_t e = pk.run(d->sms, stream);
   if (e != cudaSuccess) return finish(lease, cuda_fail(e));
