@@ -656,6 +656,9 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && leader) {
+      // (reads no global memory: the waits below are limited in time, and that
+      // of the previous grid must not count)
+      grid_dep_wait();
       int stage = 0;
       uint32_t phase = 0;
       int buf = 0;

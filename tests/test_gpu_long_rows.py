@@ -26,3 +26,28 @@ def test_rows_up_to_31_bits(M, K, variant):
     assert L.VARIANT_NAMES[L.variant_for(x, w, b, y)] == variant
     assert L.poot_linear_device_status(0) == L.POOT_OK
     assert y[:, 0].tolist() == [float(1 + sum((i + 1) * ((i + m) % 5 - 1) for i in range(len(at)))) for m in range(M)]
+
+
+def test_a_product_behind_a_kernel_of_seconds():
+    """The GEMM's bounded waits (two seconds) start when the previous kernel in
+    the stream has ended, although its blocks may be resident before: here
+    behind a single block's pass over 2^31 - 1 elements."""
+    dev, K = "cuda:0", (1 << 31) - 1
+    x = torch.zeros(1, K, dtype=torch.float16, device=dev)
+    w = torch.zeros(1, K, dtype=torch.float16, device=dev)
+    b = torch.ones(1, dtype=torch.float16, device=dev)
+    g = torch.Generator().manual_seed(1)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g).half()
+    dy, xs, ws = ints(300, 264), ints(300, 200), ints(264, 200)
+    dev_in = [t.to(dev) for t in (dy, xs, ws)]
+    L.linear_backward(*dev_in)   # (the workspace and the kernels are there)
+    torch.cuda.synchronize()
+    y = torch.empty(1, 1, dtype=torch.float16, device=dev)
+    L.linear(x, w, b, out=y)
+    dx, dw, db = L.linear_backward(*dev_in)
+    torch.cuda.synchronize()
+    assert L.poot_linear_device_status(0) == L.POOT_OK
+    d = dy.double()
+    assert (y == 1).all()
+    for o, r in ((dx, d @ ws.double()), (dw, d.T @ xs.double()), (db, d.sum(0))):
+        assert torch.equal(o.cpu(), r.half())
