@@ -58,7 +58,9 @@ enum poot_ffn_act {
  * Errors: POOT_ERR_INVALID_ARG (sizes outside [0, POOT_FFN_MAX_SIZE], NULL,
  * ldx < K, a matrix that spans more than 2^50 elements, an unknown dtype or activation, only one of g and u, an output overlapping an
  * input or another output); POOT_ERR_MISALIGNED (a pointer not 2-byte
- * aligned); otherwise as poot_linear_f16.
+ * aligned); POOT_ERR_CUDA where there is no memory for copies (nothing is queued
+ * then; sums that were to be split over K, for which there is none, go unsplit);
+ * otherwise as poot_linear_f16.
  */
 typedef struct poot_gated_linear_args {
     const void* x;

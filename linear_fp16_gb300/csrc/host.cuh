@@ -246,11 +246,17 @@ inline WorkspaceLease stream_workspace(int dev, cudaStream_t stream, size_t byte
   }
   std::unique_lock<std::mutex> held(ws->mu);
   if (ws->bytes < bytes) {
-    size_t want = bytes > 2 * ws->bytes ? bytes : 2 * ws->bytes;
-    want = (want + (size_t(1) << 20) - 1) & ~((size_t(1) << 20) - 1);
+    const auto whole = [](size_t v) { return (v + (size_t(1) << 20) - 1) & ~((size_t(1) << 20) - 1); };
+    size_t want = whole(bytes > 2 * ws->bytes ? bytes : 2 * ws->bytes);
     void* p = nullptr;
-    if (cudaMalloc(&p, want) != cudaSuccess) {
-      (void)cudaGetLastError();  // no split-K then; not an error of the call
+    cudaError_t e = cudaMalloc(&p, want);
+    if (e != cudaSuccess && whole(bytes) < want) {  // no room to double: what the call needs
+      (void)cudaGetLastError();
+      want = whole(bytes);
+      e = cudaMalloc(&p, want);
+    }
+    if (e != cudaSuccess) {
+      (void)cudaGetLastError();  // the caller goes without, or reports it
       return lease;
     }
     if (ws->ptr != nullptr) {

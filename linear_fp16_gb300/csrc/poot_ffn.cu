@@ -348,6 +348,21 @@ struct FfnSpace {
   }
 };
 
+// Leases the workspace of products under *plan, and `more` bytes behind them;
+// *space is what the products take.  Where the device has no room for it, the
+// products go unsplit.  false: no room even so.
+bool lease_products(const FfnProduct* const* ps, int count, FfnPlan* plan, int dtype, size_t more, const FfnDevice& d,
+                    cudaStream_t stream, size_t* space, WorkspaceLease* lease) {
+  for (;;) {
+    *space = FfnSpace(ps, count, *plan, dtype, d.sms).bytes();
+    if (*space + more == 0) return true;
+    *lease = stream_workspace(d.dev, stream, *space + more);
+    if (lease->ptr != nullptr) return true;
+    if (plan->split[0] == 1 && plan->split[1] == 1) return false;
+    plan->split[0] = plan->split[1] = 1;
+  }
+}
+
 // Runs up to two products (dx and dW) in one launch, with the
 // bias gradients `bg` (may be nullptr) beside them, then the second halves of
 // split products.  `ws`: workspace as FfnSpace lays it out.
@@ -591,17 +606,15 @@ int gated_linear(const poot_gated_linear_args* ap, cudaStream_t stream) {
   ep.bias[0] = p.bg;
   ep.bias[1] = p.bu;
   const FfnProduct* const ps[1] = {&q};
-  const FfnPlan plan = plan_ffn(ps, 1, d->sms);
+  FfnPlan plan = plan_ffn(ps, 1, d->sms);
   Packer pk;
   pk.need(&q.a[0]);
   pk.need(&q.b[0]);
   pk.need(&q.b[1]);
-  const size_t space = FfnSpace(ps, 1, plan, p.dtype, d->sms).bytes();
+  size_t space;
   WorkspaceLease lease;
-  if (space + pk.bytes > 0) {
-    lease = stream_workspace(d->dev, stream, space + pk.bytes);
-    if (lease.ptr == nullptr) return cuda_fail(cudaErrorMemoryAllocation);
-  }
+  if (!lease_products(ps, 1, &plan, p.dtype, pk.bytes, *d, stream, &space, &lease))
+    return cuda_fail(cudaErrorMemoryAllocation);
   char* ws = static_cast<char*>(lease.ptr);
   pk.place(ws + space);
   const cudaError_t e = pk.run(d->sms, stream);
@@ -656,7 +669,6 @@ struct Grads {
     }
     plan = plan_ffn(ps, count, sms);
   }
-  size_t space(int dtype, int sms) const { return FfnSpace(ps, count, plan, dtype, sms).bytes(); }
   int run(const FfnEpilogue& ep, const FfnBiasGrad* bg, char* ws, const FfnDevice& dev, cudaStream_t stream) const {
     return run_products(ps, count, plan, ep, bg, ws, dev, stream);
   }
@@ -710,10 +722,12 @@ int gated_linear_backward(const poot_gated_linear_backward_args* ap, cudaStream_
   const Operand dmat[2] = {{nullptr, M, N, Np}, {nullptr, M, N, Np}}, w[2] = {{p.wg, N, K, K}, {p.wu, N, K, K}};
   void* const dwp[2] = {p.dwg, p.dwu};
   g.make(2, dmat, w, {p.x, M, K, ldx}, p.dx, dwp, M, N, K, d->sms, &pk);
-  const size_t dbytes = round256(size_t(M) * Np * 2), space = g.space(p.dtype, d->sms);
+  const size_t dbytes = round256(size_t(M) * Np * 2);
   const size_t sbytes = want_db ? round256(size_t(row_blocks) * 2 * Np * 4) : 0;
-  WorkspaceLease lease = stream_workspace(d->dev, stream, 2 * dbytes + space + sbytes + pk.bytes);
-  if (lease.ptr == nullptr) return cuda_fail(cudaErrorMemoryAllocation);
+  size_t space;
+  WorkspaceLease lease;
+  if (!lease_products(g.ps, g.count, &g.plan, p.dtype, 2 * dbytes + sbytes + pk.bytes, *d, stream, &space, &lease))
+    return cuda_fail(cudaErrorMemoryAllocation);
   char* const ws = static_cast<char*>(lease.ptr);
   char* const dgp = ws;
   char* const dup = ws + dbytes;
@@ -798,12 +812,10 @@ int linear_backward(const poot_linear_backward_args* ap, cudaStream_t stream) {
   const Operand w = {p.w, N, K, K};
   g.make(1, &dy, &w, {p.x, M, K, ldx}, p.dx, &p.dw, M, N, K, d->sms, &pk);
   if (g.count > 0) pk.need(&dy);
-  const size_t space = g.space(p.dtype, d->sms);
+  size_t space;
   WorkspaceLease lease;
-  if (space + pk.bytes > 0) {
-    lease = stream_workspace(d->dev, stream, space + pk.bytes);
-    if (lease.ptr == nullptr) return cuda_fail(cudaErrorMemoryAllocation);
-  }
+  if (!lease_products(g.ps, g.count, &g.plan, p.dtype, pk.bytes, *d, stream, &space, &lease))
+    return cuda_fail(cudaErrorMemoryAllocation);
   char* const ws = static_cast<char*>(lease.ptr);
   pk.place(ws + space);
   g.dx.a[0] = g.dw.a[0] = dy;

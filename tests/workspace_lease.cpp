@@ -94,6 +94,12 @@ int main() {
     check(big.ptr != nullptr && big.ptr != p, "a larger buffer");
   }
   {
+    // 8 MB held: doubled to 16 where there is room, else what is asked for
+    g_fail_allocs = 1;
+    WorkspaceLease l = stream_workspace(0, a, size_t(9) << 20);
+    check(l.ptr != nullptr && g_fail_allocs == 0, "a buffer that cannot be doubled grows to what the call needs");
+  }
+  {
     g_fail_allocs = 1;
     WorkspaceLease l = stream_workspace(0, a, size_t(64) << 20);
     check(l.ptr == nullptr, "no workspace where none can be had");
