@@ -19,8 +19,10 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cuda_runtime_api.h>
+
 #include <cstdint>
-#include <optional>
+#include <cstring>
 #include <vector>
 
 #include "poot_ffn.h"
@@ -100,6 +102,18 @@ int64_t rows_of(PyObject* o, const char* name) {
   return t.size(0);
 }
 
+// Without the interpreter's lock while it lives.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
 // The stream of a call and the tensors it allocates: from that stream's
 // memory, and kept from reuse while the caller's current stream may still
 // read them.
@@ -122,15 +136,23 @@ class Run {
     c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), current_);
     return t;
   }
-  // runs f(stream) with the device current and without the interpreter's lock
+  // Runs f(stream) with the device current and without the interpreter's lock.
+  // The library takes its workspace from the device, where torch's cache may
+  // hold all of it: a call that found none queued nothing, and is made again
+  // when torch has given back what it does not use (not under capture, where the
+  // workspace is the graph's and the cache may not be touched).
   template <typename F>
   int call(F&& f) {
     const c10::cuda::CUDAGuard guard(device_);
-    int rc;
-    Py_BEGIN_ALLOW_THREADS
-    rc = f(reinterpret_cast<poot_stream_t>(stream_.stream()));
-    Py_END_ALLOW_THREADS
-    return rc;
+    const auto s = reinterpret_cast<poot_stream_t>(stream_.stream());
+    const Unlocked unlocked;
+    const int rc = f(s);
+    if (rc != POOT_ERR_CUDA || std::strcmp(poot_linear_last_cuda_error(), "cudaErrorMemoryAllocation") != 0) return rc;
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream_.stream(), &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone)
+      return rc;
+    c10::cuda::CUDACachingAllocator::emptyCache();
+    return f(s);
   }
 
  private:

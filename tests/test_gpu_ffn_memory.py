@@ -1,5 +1,6 @@
 """The feed-forward calls where device memory is short: sums that were to be
-split over K go unsplit."""
+split over K go unsplit; a workspace that torch's cache holds the memory of is
+taken from it."""
 import pytest
 import torch
 
@@ -57,3 +58,23 @@ def test_split_sums_without_a_workspace():
     assert torch.equal(out[1], g) and torch.equal(out[2], u)
     assert torch.equal(out[0], h)
     assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+
+
+def test_a_workspace_that_torch_holds_the_memory_of():
+    """dg and du (4.3 GB) where 2 GB are free and torch's cache holds the rest unused."""
+    M, N = 65536, 16384
+    t = torch.ones(M, N, dtype=F16, device=DEV)
+    x, w = torch.ones(M, 8, dtype=F16, device=DEV), torch.ones(N, 8, dtype=F16, device=DEV)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = torch.empty(torch.cuda.mem_get_info()[0] - (2 << 30), dtype=torch.uint8, device=DEV)
+    del held
+    assert torch.cuda.mem_get_info()[0] < 3 << 30
+    with torch.cuda.stream(s):
+        out = L.gated_linear_backward(t, x, w, w, t, t, need_dx=False, need_dw=False, need_db=True)
+    s.synchronize()
+    assert L.poot_linear_device_status(0) == L.POOT_OK
+    # silu(1) = 0.7311, silu'(1) = 0.9277: 65536 equal terms, one rounding
+    for got, v in zip(out[3:], (0.92767051187, 0.73105857863)):
+        assert bool(((got.double() / (M * v) - 1).abs() <= 2.0 ** -11 + 2.0 ** -18).all())
