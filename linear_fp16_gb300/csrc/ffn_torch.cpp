@@ -116,7 +116,8 @@ class Unlocked {
 
 // The stream of a call and the tensors it allocates: from that stream's
 // memory, and kept from reuse while the caller's current stream may still
-// read them.
+// read them.  The caller's tensors are kept from reuse while that stream may
+// still use them, whatever becomes of them meanwhile.
 class Run {
  public:
   // stream: None (the current one) or (stream_id, device_index, device_type)
@@ -126,6 +127,7 @@ class Run {
     long long id = 0;
     int index = 0, type = 0;
     if (!PyArg_ParseTuple(stream, "Lii", &id, &index, &type)) throw Refused{};
+    if (index != device) refuse(PyExc_ValueError, "%s must be one of the tensors' device", "stream");
     stream_ = c10::cuda::CUDAStream::unpack3(id, static_cast<c10::DeviceIndex>(index), static_cast<c10::DeviceType>(type));
   }
   at::Tensor empty(std::initializer_list<int64_t> shape, at::ScalarType dtype) {
@@ -135,6 +137,13 @@ class Run {
     at::Tensor t = at::empty(at::IntArrayRef(shape), options);
     c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), current_);
     return t;
+  }
+  void uses(PyObject* o) const {  // a tensor of the caller's, or None
+    if (o != Py_None && !(stream_ == current_))
+      c10::cuda::CUDACachingAllocator::recordStream(THPVariable_Unpack(o).storage().data_ptr(), stream_);
+  }
+  void uses(PyObject* const* a, int n) const {
+    for (int i = 0; i < n; ++i) uses(a[i]);
   }
   // Runs f(stream) with the device current and without the interpreter's lock.
   // The library takes its workspace from the device, where torch's cache may
@@ -221,6 +230,7 @@ PyObject* gated_linear(PyObject* const* a, Py_ssize_t n) {
     p.g = ptr(g);
     p.u = ptr(u);
   }
+  run.uses(a, 6);
   const int rc = run.call([&](poot_stream_t s) { return poot_gated_linear(&p, s); });
   if (rc != POOT_OK) return PyLong_FromLong(rc);
   if (!save && a[5] != Py_None) {
@@ -263,6 +273,7 @@ PyObject* gated_linear_backward(PyObject* const* a, Py_ssize_t n) {
   p.dwu = ptr(dwu);
   p.dbg = ptr(dbg);
   p.dbu = ptr(dbu);
+  run.uses(a, 6);
   const int rc = run.call([&](poot_stream_t s) { return poot_gated_linear_backward(&p, s); });
   return rc != POOT_OK ? PyLong_FromLong(rc) : wrap_all({&dx, &dwg, &dwu, &dbg, &dbu});
 }
@@ -286,6 +297,7 @@ PyObject* linear_backward(PyObject* const* a, Py_ssize_t n) {
   p.dx = ptr(dx);
   p.dw = ptr(dw);
   p.db = ptr(db);
+  run.uses(a, 3);
   const int rc = run.call([&](poot_stream_t s) { return poot_linear_backward(&p, s); });
   return rc != POOT_OK ? PyLong_FromLong(rc) : wrap_all({&dx, &dw, &db});
 }
@@ -329,6 +341,10 @@ PyObject* clip_grad_norm(PyObject* const* a, Py_ssize_t n) {
   Run run(device, a[3]);
   at::Tensor norm = run.empty({}, at::kFloat);
   float* const out = static_cast<float*>(norm.data_ptr());
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    run.uses(PyList_GET_ITEM(a[0], i));
+    if (a[1] != Py_None) run.uses(PyList_GET_ITEM(a[1], i));
+  }
   const int rc = run.call(
       [&](poot_stream_t s) { return poot_clip_grad_norm(table.data(), count, static_cast<float>(max_norm), out, s); });
   return rc != POOT_OK ? PyLong_FromLong(rc) : wrap(norm);

@@ -147,7 +147,9 @@ def gated_linear(x, wg, wu, bg=None, bu=None, *, activation: str = "silu", save:
     dtype.  ``activation``: "silu", "gelu_tanh" or "gelu_erf".  Returns h
     [M,N] (``out`` if given), or with ``save`` (h, g, u): the two
     pre-activations, rounded to the dtype, that gated_linear_backward reads.
-    Runs on ``stream`` (default: the current stream of x's device).  Raises
+    Runs on ``stream`` (default: the current stream of x's device), which the
+    caller orders after the work that makes the inputs; memory of the tensors
+    given is not reused before that stream is done with it.  Raises
     PootLinearError on a status other than POOT_OK.
     """
     r = (_ext or load_tensor_calls()).gated_linear(x, wg, wu, bg, bu, out, _act(activation), save, _stream(stream))
