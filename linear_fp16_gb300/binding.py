@@ -238,6 +238,22 @@ def _check(t, name, ndim):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _stream_for(stream, dev, *tensors):
+    """The stream of a call on `dev` (None: the current one).  Memory of the
+    tensors is not handed out again before a stream other than the current one
+    is done with them."""
+    import torch
+    current = torch.cuda.current_stream(dev)
+    if stream is None or stream == current:
+        return current
+    if stream.device != dev:
+        raise ValueError("stream must be one of the tensors' device")
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return stream
+
+
 def linear(x, w, b, out=None, *, variant: int = VARIANT_AUTO, gemv_warps_per_row: int = 0,
            gemm_tile_n: int = 0, gemm_group_m: int = 0, gemm_k_chunk: int = 0,
            gemm_cluster: int = 0, gemm_split_k: int = 0, stream=None):
@@ -265,7 +281,7 @@ def linear(x, w, b, out=None, *, variant: int = VARIANT_AUTO, gemv_warps_per_row
         if tuple(out.shape) != (M, N) or out.device != dev:
             raise ValueError("out must be [M, N] on x's device")
     with torch.cuda.device(dev):
-        s = torch.cuda.current_stream(dev) if stream is None else stream
+        s = _stream_for(stream, dev, x, w, b, out)
         rc = poot_linear_f16_ex(x.data_ptr(), w.data_ptr(), b.data_ptr(), out.data_ptr(), M, N, K,
                                 options(variant, gemv_warps_per_row, gemm_tile_n, gemm_group_m,
                                         gemm_k_chunk, gemm_cluster, gemm_split_k),
@@ -350,7 +366,7 @@ def contract(x, w, b=None, out=None, *, out_f32: bool = False, steps=(), gemm_ti
     opts = options(variant, 0, gemm_tile_n, gemm_group_m, gemm_k_chunk, gemm_cluster, gemm_split_k)
     bp = b.data_ptr() if b is not None else 0
     with torch.cuda.device(x.device):
-        s = torch.cuda.current_stream(x.device) if stream is None else stream
+        s = _stream_for(stream, x.device, x, w, b, out, *(st[1] for st in steps if not isinstance(st, str)))
         if grouped:
             rc = poot_contract_grouped(x.data_ptr(), w.data_ptr(), bp, out.data_ptr(), G, M, N, K, spec, opts,
                                        s.cuda_stream)

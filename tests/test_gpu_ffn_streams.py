@@ -1,6 +1,6 @@
-"""The tensor calls on a stream that is not the current one: the caller may drop
-its tensors at once, and their memory is not handed out again before that
-stream has read them."""
+"""The tensor calls, the linear's and the widened contraction's too, on a stream
+that is not the current one: the caller may drop its tensors at once, and their
+memory is not handed out again before that stream has read them."""
 import pytest
 import torch
 
@@ -23,6 +23,9 @@ CALLS = {
                             lambda t, s: [L.gated_linear(*t, stream=s)]),
     "gated_linear_backward": (((M, N), (M, K), (N, K), (N, K), (M, N), (M, N)),
                               lambda t, s: L.gated_linear_backward(*t, need_db=True, stream=s)),
+    "linear": (((M, K), (N, K), (N,)), lambda t, s: [L.linear(*t, stream=s)]),
+    "contract": (((M, K), (N, K), (N,), (M, N)),
+                 lambda t, s: [L.contract(*t[:3], steps=["silu", ("mul", t[3])], stream=s)]),
     "linear_backward": (((M, N), (M, K), (N, K)), lambda t, s: L.linear_backward(*t, stream=s)),
 }
 
@@ -86,3 +89,6 @@ def test_a_stream_of_another_device_is_refused():
         L.gated_linear(*t, stream=Elsewhere())
     with pytest.raises(ValueError):
         L.clip_grad_norm(t, 1.0, stream=Elsewhere())
+    Elsewhere.device = torch.device("cuda", 1)
+    with pytest.raises(ValueError):
+        L.linear(t[0], t[1], t[1][:, 0].contiguous(), stream=Elsewhere())
