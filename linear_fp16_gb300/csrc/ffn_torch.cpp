@@ -169,6 +169,13 @@ class Run {
   c10::cuda::CUDAStream current_, stream_;
 };
 
+// The call has written to a tensor of the caller's: a graph that saved its former
+// values finds out (inference tensors carry no version).
+void written(PyObject* o) {
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject* wrap(const at::Tensor& t) {
   if (!t.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(t);
@@ -233,6 +240,7 @@ PyObject* gated_linear(PyObject* const* a, Py_ssize_t n) {
   run.uses(a, 6);
   const int rc = run.call([&](poot_stream_t s) { return poot_gated_linear(&p, s); });
   if (rc != POOT_OK) return PyLong_FromLong(rc);
+  if (a[5] != Py_None) written(a[5]);
   if (!save && a[5] != Py_None) {
     Py_INCREF(a[5]);
     return a[5];
@@ -347,7 +355,10 @@ PyObject* clip_grad_norm(PyObject* const* a, Py_ssize_t n) {
   }
   const int rc = run.call(
       [&](poot_stream_t s) { return poot_clip_grad_norm(table.data(), count, static_cast<float>(max_norm), out, s); });
-  return rc != POOT_OK ? PyLong_FromLong(rc) : wrap(norm);
+  if (rc != POOT_OK) return PyLong_FromLong(rc);
+  PyObject* const results = a[1] != Py_None ? a[1] : a[0];
+  for (Py_ssize_t i = 0; i < count; ++i) written(PyList_GET_ITEM(results, i));
+  return wrap(norm);
 }
 
 // C++ exceptions end here: torch's become its Python errors.

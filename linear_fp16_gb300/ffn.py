@@ -2,7 +2,9 @@
 
 ``gated_linear`` (h = act(x Wg^T + bg) * (x Wu^T + bu)) and its gradients
 ``gated_linear_backward``, the linear's gradients ``linear_backward``, and
-``clip_grad_norm`` over a list of gradients.  The functions named like the C
+``clip_grad_norm`` over a list of gradients.  The calls record no graph for
+torch's automatic differentiation: tensors that require gradients are taken as
+values, and the gradients are the calls for them.  The functions named like the C
 entry points (include/poot_ffn.h) take the argument structures and return
 the status code; every step of the computation runs in the CUDA library.
 """
@@ -147,6 +149,7 @@ def gated_linear(x, wg, wu, bg=None, bu=None, *, activation: str = "silu", save:
     dtype.  ``activation``: "silu", "gelu_tanh" or "gelu_erf".  Returns h
     [M,N] (``out`` if given), or with ``save`` (h, g, u): the two
     pre-activations, rounded to the dtype, that gated_linear_backward reads.
+    No result is attached to torch's autograd graph.
     Runs on ``stream`` (default: the current stream of x's device), which the
     caller orders after the work that makes the inputs; memory of the tensors
     given is not reused before that stream is done with it.  Raises
@@ -187,7 +190,10 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, stream=None):
     bfloat16 or float32, any mixture), clipped in place; with ``out``, a
     sequence of tensors of the same shapes and dtypes, the results go there
     instead.  The norm, over all tensors together, is a float32 scalar tensor
-    on the device (the call does not synchronise).
+    on the device (the call does not synchronise).  Tensors written to count as
+    modified in place (their version goes up); ones that require gradients are
+    written all the same.  An empty sequence raises ValueError: there is no device
+    to put a norm on.
     """
     r = (_ext or load_tensor_calls()).clip_grad_norm(list(grads), None if out is None else list(out), max_norm,
                                                  _stream(stream))
