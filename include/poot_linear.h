@@ -335,7 +335,8 @@ POOT_API int poot_contract_grouped(const void* x, const void* w, const void* b, 
  *   point on that device (no other entry point touches it).  Calls whose
  *   work can overlap in time — on different streams with no event or
  *   synchronisation ordering them — race on it and give wrong results;
- *   calls on one stream, or otherwise ordered, are safe.
+ *   calls on one stream, of any number of host threads, or otherwise ordered,
+ *   are safe.
  * Setup: the first call on each device looks the array's address up
  *   (cudaGetSymbolAddress, with that device current) and keeps it; make
  *   that first call outside stream capture.

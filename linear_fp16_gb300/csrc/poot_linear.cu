@@ -840,11 +840,13 @@ int contract(const void* x, const void* w, const void* b, void* y, int64_t G, in
 // holds the device's memory budget, or in a serving loop that cannot take an
 // allocation's implicit synchronisation — still get split-K.  Every element
 // a call reads is written earlier in the same call, so it is never cleared.
-// Calls that overlap in time race on it (one array per device).
+// Calls that overlap in time race on it (one array per device); a call's two
+// launches are queued without another thread's between them.
 static_assert(POOT_NOALLOC_SCRATCH_BYTES % 256 == 0, "scratch size");
 static __device__ __align__(256) float g_noalloc_scratch[POOT_NOALLOC_SCRATCH_BYTES / sizeof(float)];
 
 std::mutex g_noalloc_mu;
+std::mutex g_noalloc_call[kMaxDevices];
 void* g_noalloc_addr[kMaxDevices] = {};
 
 // Address of the array on device `dev` (the current device), looked up once.
@@ -880,6 +882,7 @@ int run_splitk_noalloc(const void* x, const void* w, const void* b, void* y, int
   float* scratch = nullptr;
   rc = noalloc_scratch(dev, &scratch);
   if (rc != POOT_OK) return rc;
+  std::lock_guard<std::mutex> lock(g_noalloc_call[dev]);
   return launch_gemm(variant, *st, x, w, b, y, M, N, K, 0, 0, 0, 0, split_k, stream, nullptr, 1, scratch,
                      POOT_NOALLOC_SCRATCH_BYTES);
 }

@@ -45,6 +45,15 @@ def _calls():
         out.append((f"linear, odd rows {i}", lambda a=lin: (L.linear(*a),)))
         split = (h(64, 8192), h(512, 8192), h(512))
         out.append((f"linear, split {i}", lambda a=split: (L.linear(*a),)))
+        noalloc = (h(64, 4096), h(512, 4096), h(512))
+
+        def fixed(a=noalloc):
+            y = torch.empty(64, 512, dtype=torch.float16, device=DEV)
+            rc = L.poot_linear_f16_splitk_noalloc(a[0].data_ptr(), a[1].data_ptr(), a[2].data_ptr(), y.data_ptr(),
+                                                  64, 512, 4096, 4, torch.cuda.current_stream().cuda_stream)
+            assert rc == L.POOT_OK
+            return (y,)
+        out.append((f"linear, split in the fixed array {i}", fixed))
         grads = [n(5000 + 999 * i).to(DEV), h(300 + i)]
 
         def clip(gs=grads):
@@ -67,7 +76,7 @@ def test_two_host_threads_on_one_stream():
             torch.cuda.set_device(0)
             start.wait()
             for rep in range(60):
-                results = [(k, calls[k][1]()) for k in range(i, len(calls), 2) for _ in range(3)]
+                results = [(k, calls[k][1]()) for k in range(len(calls)) if calls[k][0].endswith(str(i)) for _ in range(3)]
                 for k, got in results:
                     if not all(torch.equal(a, b) for a, b in zip(got, alone[k]) if a is not None):
                         wrong.append((rep, calls[k][0]))
