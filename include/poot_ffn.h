@@ -19,8 +19,9 @@
  * before they are multiplied with the weights and x, as operands of 16-bit
  * products.  Sums are FP32 in a fixed order: equal calls give equal bits.  The
  * tensor core truncates towards zero where it adds products to a sum, so sums of
- * many terms of one sign come out low, whatever their length by less than an
- * eighth of the result's rounding (M > 16).
+ * many terms of one sign come out low: whatever their length by about an eighth
+ * of binary16's rounding and a twentieth of bfloat16's (5e-5 and 2e-4); in the
+ * GEMV kernels (M <= 16) by 8e-10 per element of K, 5e-5 at 65536.
  */
 #ifndef POOT_FFN_H
 #define POOT_FFN_H
@@ -56,11 +57,12 @@ enum poot_ffn_act {
  * copied to 16-byte-pitched rows in the library's workspace.
  * M == 0 or N == 0 does nothing; K == 0 gives g = bg, u = bu.
  * Errors: POOT_ERR_INVALID_ARG (sizes outside [0, POOT_FFN_MAX_SIZE], NULL,
- * ldx < K, a matrix that spans more than 2^50 elements, an unknown dtype or activation, only one of g and u, an output overlapping an
- * input or another output); POOT_ERR_MISALIGNED (a pointer not 2-byte
- * aligned); POOT_ERR_CUDA where there is no memory for copies (nothing is queued
- * then; sums that were to be split over K, for which there is none, go unsplit);
- * otherwise as poot_linear_f16.
+ * ldx < K, a matrix that spans more than 2^50 elements, an unknown dtype or
+ * activation, only one of g and u, an output overlapping an input or another
+ * output); POOT_ERR_MISALIGNED (a pointer not 2-byte aligned); POOT_ERR_CUDA
+ * where there is no memory for copies (nothing is queued then; sums that were to
+ * be split over K, for which there is none, go unsplit); otherwise as
+ * poot_linear_f16.
  */
 typedef struct poot_gated_linear_args {
     const void* x;
@@ -144,9 +146,11 @@ typedef struct poot_grad_tensor {
  *   dst   = RN(src * scale), in the tensor's dtype
  * norm: device pointer to one float, written on `stream` (the call does not
  * synchronise).  Squares are summed in FP32 over at most 33 elements and in
- * FP64 beyond (scaled first where FP32 squares would overflow or vanish).  A norm that is NaN makes every result NaN; an infinite norm gives
- * scale 0.  Tensors may be empty, of mixed dtypes and at any alignment of
- * their elements; count == 0 writes norm = 0.
+ * FP64 beyond (scaled first where FP32 squares would overflow or vanish).  A
+ * norm that is NaN makes every result NaN; an infinite norm gives scale 0 under
+ * a finite max_norm, and NaN under an infinite one, as the formula does.
+ * Tensors may be empty, of mixed dtypes and at any alignment of their elements;
+ * count == 0 writes norm = 0.
  * A dst must be its own src or overlap no src and no other dst.
  * Errors: POOT_ERR_INVALID_ARG (count < 0, NULL, n < 0 or n > 2^40, an
  * unknown dtype, max_norm negative or NaN, overlap), POOT_ERR_MISALIGNED (a

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) gated_gemv_kernel(cons
   const int c_end = c_begin + per + ((int)blockIdx.x < extra ? 1 : 0);
   constexpr int KS = 32 * kGgSteps;
   // K is split over a.kw warps (as many as have a slot's worth of it, a power
-  // of two); the warps are 16 / kw teams, each with every (16 / kw)-th pass
+  // of two); the warps are WARPS / kw teams, each with every (WARPS / kw)-th pass
   const int kw = a.kw, teams = WARPS / kw, team = warp / kw;
   const int slice = ((K + kw * KS - 1) / (kw * KS)) * KS;
   const int k_begin = min(K, (warp & (kw - 1)) * slice), k_end = min(K, k_begin + slice);

@@ -217,13 +217,13 @@ struct FfnProduct {
   }
 };
 
-// Time of a plan, in microseconds, from a model fitted to GB300 timings of 240
-// single and paired products of 17 .. 8192 rows under every tile and split
-// (the plan it picks is within 2% of the best of them on average, 31% at
-// worst): a tile takes its K blocks at the shape's rate plus a fill, or its
-// epilogue where that is longer; the tiles fill the CTAs (pairs) as
-// FfnSchedule deals them; all of it takes at least the operands' time from
-// HBM; a split adds the second kernel and the partial sums' traffic.
+// Time of a plan, in microseconds, from a model: a tile takes its K blocks at
+// the shape's rate plus a fill, or its epilogue where that is longer; the tiles
+// fill the CTAs (pairs) as FfnSchedule deals them; all of it takes at least the
+// operands' time from HBM; a split adds the second kernel and the partial sums'
+// traffic.  The constants are a fit to GB300 timings of single and paired
+// products of 17 .. 8192 rows under every tile and split; they rank plans, and
+// are not the times of the present kernels.
 struct FfnShape {
   int cl, bn;
   double per_kb;  // 64 elements of K

@@ -71,3 +71,15 @@ def test_every_element(name, above, in_place):
     assert all(torch.equal(f.view(torch.int16 if f.element_size() == 2 else torch.int32),
                            guard[dt].view(torch.int16 if f.element_size() == 2 else torch.int32))
                for dt, f in flat.items())
+
+
+@pytest.mark.parametrize("dt", [F16, BF16, F32])
+def test_an_infinite_max_norm(dt):
+    """Never clips a finite norm; an infinite one over it is NaN, as in the formula."""
+    t = torch.linspace(-3, 3, 20001).to(dt).to(DEV)
+    kept = t.clone()
+    norm = float(L.clip_grad_norm([t], float("inf")))
+    ref = float(kept.double().norm())
+    assert torch.equal(t, kept) and abs(norm - ref) <= 2.0 ** -18 * ref
+    t[7] = float("inf")
+    assert float(L.clip_grad_norm([t], float("inf"))) == float("inf") and torch.isnan(t).all()
