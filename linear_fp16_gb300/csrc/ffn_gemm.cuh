@@ -139,16 +139,17 @@ __device__ __forceinline__ uint4 ffn_pack8(const float (&f)[8]) {
 // error is FP32's subnormal step, far below bfloat16's.
 // Where s (1 - s) is 0 in FP32 z' may overflow: the second term is then
 // dropped, as in the limit.
-// 2^-22 relative.  Subnormal results are kept for bfloat16, whose range they lie
-// in; binary16 products of 2^-126 round to zero either way, so its form drops
-// them (a few instructions fewer: 2047 x 1000 x 770 with g and u 19.2 us
-// with them, 19.0 so).
+// 2^x for x <= 0.  Subnormal results are kept for bfloat16, whose range they lie
+// in: 2^(x + 24) times 2^-24, within 2^-20 (the sum's rounding; the instruction
+// that keeps them itself takes three more around it: 7540 x 1845 with bias
+// gradients 47.5 us against 45.4).  binary16 products of 2^-126 round to zero
+// either way, so its form drops them.
 template <int DT>
 __device__ __forceinline__ float act_exp2(float x) {
   float y;
-  if constexpr (DT == kEpiF16) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  else asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+  if constexpr (DT != kEpiF16) x += 24.0f;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return DT == kEpiF16 ? y : y * 5.9604644775390625e-8f;
 }
 __device__ __forceinline__ float act_rcp(float x) {  // of 1 and more (its result is never subnormal here)
   float y;
