@@ -18,11 +18,11 @@
 // which promotes every 1024 elements: these operators' outputs are rounded once
 // from the FP32 value to 11 or 8 bits and carry no 2-ulp rule (chunks: see
 // ffn_chunk_k).  The accumulators of two tiles fit TMEM, so the epilogue of a
-// tile runs under the main loop of the next.  Bound by the
-// tensor pipe under the power cap where K is long (GB300, bfloat16, 8192 x
-// 14336 x 4096: gated with g and u 1.13 ms, 1.70 PFLOP/s; dx and both dW 2.24
-// ms, 1.72 PFLOP/s), by operand loads from L2 (about 80 GB/s per SM) and the
-// start-up where one wave of tiles holds the problem.
+// tile runs under the main loop of the next.  Bound by the tensor pipe under the
+// power cap where K is long (GB300, bfloat16, 8192 x 14336 x 4096: gated with g
+// and u 1.12 - 1.16 ms, 1.66 - 1.71 PFLOP/s; dx and both dW 2.25 - 2.34 ms, 1.64 -
+// 1.71 PFLOP/s), by operand loads from L2 (about 80 GB/s per SM) and the start-up
+// where one wave of tiles holds the problem.
 //
 // The gated tile: half of the tile's BN accumulator columns hold gate
 // columns and half the same columns of up, so that one thread has g and u
