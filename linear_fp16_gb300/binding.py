@@ -246,11 +246,12 @@ def _stream_for(stream, dev, *tensors):
     current = torch.cuda.current_stream(dev)
     if stream is None or stream == current:
         return current
-    if stream.device != dev:
+    if getattr(stream, "device", dev) != dev:
         raise ValueError("stream must be one of the tensors' device")
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
+    if isinstance(stream, torch.Stream):  # (an object with a handle alone is taken too: its owner sees to the rest)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
     return stream
 
 

@@ -92,3 +92,16 @@ def test_a_stream_of_another_device_is_refused():
     Elsewhere.device = torch.device("cuda", 1)
     with pytest.raises(ValueError):
         L.linear(t[0], t[1], t[1][:, 0].contiguous(), stream=Elsewhere())
+
+
+def test_a_stream_given_by_its_handle_alone():
+    class Handle:
+        def __init__(self, stream):
+            self.cuda_stream = stream.cuda_stream
+    x, w, b = _make(((40, 64), (48, 64), (48,)), 4)
+    want = L.linear(x, w, b)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = L.linear(x, w, b, stream=Handle(s))
+    s.synchronize()
+    assert torch.equal(got, want)
