@@ -55,7 +55,7 @@ __device__ __forceinline__ void ffn_pack_rows(const FfnPackArgs& a, int block, i
   }
 }
 
-__global__ void __launch_bounds__(256) ffn_pack_kernel(const FfnPackArgs a) {
+static __global__ void __launch_bounds__(256) ffn_pack_kernel(const FfnPackArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   ffn_pack_rows(a, blockIdx.x, gridDim.x);
@@ -195,7 +195,7 @@ struct FfnReduceArgs {
 // Second half of a split product: the S partial sums of an element are added
 // in order; then the gated epilogue or one rounding.  Four columns a thread
 // (the workspace's rows are padded to that).
-__global__ void __launch_bounds__(256) ffn_reduce_kernel(const FfnReduceArgs a) {
+static __global__ void __launch_bounds__(256) ffn_reduce_kernel(const FfnReduceArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   const int dt = a.dtype, quads = a.ldw / 4;
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(256) ffn_reduce_kernel(const FfnReduceArgs a) 
 }
 
 // K == 0: g = bg, u = bu in every row.
-__global__ void __launch_bounds__(256) gated_bias_kernel(const FfnReduceArgs a) {
+static __global__ void __launch_bounds__(256) gated_bias_kernel(const FfnReduceArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   const int dt = a.dtype;
