@@ -5,10 +5,12 @@ contraction (bfloat16 heads, no bias, FP32 output, fused epilogue steps);
 ``gated_linear``, ``gated_linear_backward``, ``linear_backward`` and
 ``clip_grad_norm`` are the feed-forward block, its gradients and the clip
 before an update;
+``linear_cross_entropy`` and ``linear_cross_entropy_backward`` are the loss of a
+vocabulary head and its gradients;
 ``column_parallel_linear`` and ``row_parallel_linear`` split the op over
 torch.distributed ranks;
 the C entry points of include/poot_linear.h are mirrored one to one in
-``binding``, those of include/poot_ffn.h in ``ffn``.
+``binding``, those of include/poot_ffn.h in ``ffn``, of include/poot_train.h in ``train``.
 """
 from .binding import (  # noqa: F401
     GEMV_MAX_M, Options, options, POOT_ERR_CUDA, POOT_ERR_DEVICE_TIMEOUT, POOT_ERR_INVALID_ARG,
@@ -27,6 +29,10 @@ from .ffn import (  # noqa: F401
     ACT_CODES, ACT_GELU_ERF, ACT_GELU_TANH, ACT_SILU, GRAD_BF16, GRAD_F16, GRAD_F32, GatedLinearArgs,
     GatedLinearBackwardArgs, GradTensor, LinearBackwardArgs, clip_grad_norm, gated_linear, gated_linear_backward,
     linear_backward, poot_clip_grad_norm, poot_gated_linear, poot_gated_linear_backward, poot_linear_backward,
+)
+from .train import (  # noqa: F401
+    LinearCrossEntropyArgs, LinearCrossEntropyBackwardArgs, linear_cross_entropy, linear_cross_entropy_backward,
+    poot_linear_cross_entropy, poot_linear_cross_entropy_backward,
 )
 from .tensor_parallel import (  # noqa: F401
     shard_range, column_parallel_linear, row_parallel_linear,

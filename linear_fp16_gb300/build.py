@@ -22,14 +22,14 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpoot_linear.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("poot_linear.cu", "poot_ffn.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("poot_linear.cu", "poot_ffn.cu", "poot_head.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in (
     "ptx.cuh", "gemm_tcgen05.cuh", "gemv.cuh", "epilogue.cuh", "splitk.cuh", "pack.cuh", "shards.cuh", "host.cuh",
-    "mma.cuh", "ffn_plan.cuh", "ffn_gemm.cuh", "ffn_gemv.cuh", "ffn_elem.cuh", "clip.cuh")] + [
-    os.path.join(INCLUDE, f) for f in ("poot_linear.h", "poot_ffn.h")]
+    "mma.cuh", "ffn_plan.cuh", "ffn_gemm.cuh", "ffn_gemv.cuh", "ffn_elem.cuh", "clip.cuh", "head.cuh", "head_elem.cuh")] + [
+    os.path.join(INCLUDE, f) for f in ("poot_linear.h", "poot_ffn.h", "poot_train.h")]
 
 EXT_SOURCE = os.path.join(CSRC, "ffn_torch.cpp")
-EXT_DEPENDS = [EXT_SOURCE, os.path.join(CSRC, "tensor_call.h")] + [os.path.join(INCLUDE, f) for f in ("poot_linear.h", "poot_ffn.h")]
+EXT_DEPENDS = [EXT_SOURCE, *(os.path.join(CSRC, f) for f in ("tensor_call.h", "train_calls.h"))] + [os.path.join(INCLUDE, f) for f in ("poot_linear.h", "poot_ffn.h", "poot_train.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -11,6 +11,13 @@
 //   dW         dW_q = D_q^T x, q = 1 or 2 outputs
 //              A = D_q [M,N] and B = x [M,K], both MN-major
 //
+// and those of a vocabulary head (see head.cuh), whose logits z = x W^T + b stay
+// in the kernel (A = x, B = W, both K-major):
+//   lse        per row and tile the maximum and the sum of exp of its logits
+//   dz         q = dloss (exp(z - lse) - [column = target]) in the head dtype
+//   scaled     the gradients of a product above, with a scale taken out at the
+//              end, and dx added up over launches
+//
 // A persistent CTA (or a CTA pair on one 256-row tile, 2-SM MMA) per SM walks
 // output tiles.  Warp roles as in the linear's GEMM: epilogue warps, one
 // thread that issues the MMAs, one or two that issue the TMA loads.  A sum stays
@@ -39,10 +46,14 @@
 #include <type_traits>
 
 #include "epilogue.cuh"
+#include "head.cuh"
 #include "pack.cuh"
 #include "ptx.cuh"
 
 namespace poot {
+
+// What a kernel does with its sums (the products of each are listed above).
+enum FfnMode : int { kFfnGrads = 0, kFfnGated = 1, kFfnLse = 2, kFfnDz = 3, kFfnScaled = 4 };
 
 enum FfnAct : int { kActSilu = 0, kActGeluTanh = 1, kActGeluErf = 2 };
 
@@ -320,6 +331,17 @@ struct FfnGemmArgs {
   float4* scratch;   // sums of earlier chunks, kFfnScratchBytes a CTA; nullptr: no sum has two
 };
 constexpr int kFfnScratchBytes = kFfnBM * kFfnMaxBN * 4;
+struct FfnHeadGemmArgs : FfnGemmArgs {
+  HeadArgs head;
+};
+__device__ __forceinline__ const uint16_t* head_bias(const FfnGemmArgs&) { return nullptr; }
+__device__ __forceinline__ const uint16_t* head_bias(const FfnHeadGemmArgs& a) { return a.head.bias; }
+__device__ __forceinline__ bool head_sums(const FfnGemmArgs&) { return false; }
+__device__ __forceinline__ bool head_sums(const FfnHeadGemmArgs& a) { return a.head.sum_dx != 0; }
+__device__ __forceinline__ bool head_accumulates(const FfnGemmArgs&) { return false; }
+__device__ __forceinline__ bool head_accumulates(const FfnHeadGemmArgs& a) { return a.head.accumulate != 0; }
+template <int MODE>
+using FfnModeArgs = std::conditional_t<(MODE >= kFfnLse), FfnHeadGemmArgs, FfnGemmArgs>;
 
 // The tiles of one CTA (or pair): its round-robin share of the job with the
 // longer tiles (deal.first); then, where that leaves it one tile short of
@@ -406,6 +428,12 @@ __device__ __forceinline__ void ffn_load(bool mn, uint32_t dst, const CUtensorMa
   }
 }
 
+// K blocks of the sums that one accumulator holds
+template <int MODE>
+__device__ constexpr int ffn_mode_chunk_kb(int cl, int dtype) {
+  return MODE == kFfnLse ? kHeadChunkK / (kFfnBK * ffn_sub(cl)) : ffn_chunk_kb(cl, dtype);
+}
+
 // the epilogue warps of a gradient kernel
 __device__ __forceinline__ void ffn_epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(ffn_epi_warps(false) * 32) : "memory"); }
 
@@ -413,8 +441,8 @@ __device__ __forceinline__ void ffn_epi_sync() { asm volatile("bar.sync 1, %0;" 
 // groups of 8 columns (of all outputs, side by side), a lane every so-many-th
 // row of one group.  Lanes of a group meet by shuffles, warps in shared
 // memory, in a fixed order.  FP32 sums, one rounding.
-template <int DT>
-__device__ __forceinline__ void ffn_bias_grad(const FfnBiasGrad& b, float* red, int cta, int ctas) {
+template <int DT, bool SCALED>
+__device__ __forceinline__ void ffn_bias_grad(const FfnBiasGrad& b, float scale, float* red, int cta, int ctas) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per_out = (b.N + 7) / 8;             // groups of one output
   const int groups = per_out * b.outputs;
@@ -477,6 +505,7 @@ __device__ __forceinline__ void ffn_bias_grad(const FfnBiasGrad& b, float* red, 
         float t = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) t += red[(w * 32 + gg) * 9 + j];
+        if constexpr (SCALED) t *= scale;
         out[col] = (uint16_t)ep_pack_t<DT>(t, 0.0f);
       }
     }
@@ -504,13 +533,98 @@ __device__ __forceinline__ void ffn_add_scratch(const float4* p, uint32_t (&r)[3
   }
 }
 
+// The epilogue of the lse kernel: a lane has a row of its tile, a warp every
+// fourth box of 32 columns, at most two.  The sums of a tile's chunks of K are added up in
+// registers, rounded to nearest (64 a lane; sixteen warps leave 112 registers
+// each): the tensor core's truncation, 6.3e-9 of a sum per term, would come
+// through to the loss unrounded.  With an accumulator's columns drained in
+// about 500 cycles a chunk of 1024 (16 x 512 cycles of MMAs a CTA) hides it.
+template <int CL, int DT>
+__device__ __forceinline__ void ffn_lse_rows(const FfnHeadGemmArgs& args, const FfnSchedule& sched, float* sbias,
+                                             uint32_t tmem_base, uint32_t bar_cfull, uint32_t bar_cempty,
+                                             volatile int* abort_flag, int rank) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, part = warp >> 2;
+  const FfnJob& job = args.job[0];
+  const HeadArgs& head = args.head;
+  const int boxes = args.cols / 32, tiles = sched.count(0);
+  const int chunks = (job.kb_total + ffn_mode_chunk_kb<kFfnLse>(CL, DT) - 1) / ffn_mode_chunk_kb<kFfnLse>(CL, DT);
+  int buf = 0;
+  uint32_t buf_phase = 0;
+  for (int ti = 0; ti < tiles; ++ti) {
+    const FfnTile tile(job, (uint32_t)sched.tile(0, ti));
+    const int m0 = tile.mb * CL * kFfnBM + rank * kFfnBM + q * 32, nc = tile.nb * args.cols + part * 32;
+    const int row = m0 + lane;
+    // boxes of this warp with columns of the vocabulary: 0, 1 or 2, 128 columns apart
+    const int mine = m0 < job.M ? (part < boxes && nc < job.N) + (part + 4 < boxes && nc + 128 < job.N) : 0;
+    const int target = row < job.M ? head_target(head, row) : -1;
+    if (mine > 0 && head.bias != nullptr) {
+      __syncwarp();
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int col = nc + b * 128 + lane;
+        sbias[b * 32 + lane] = b < mine && col < job.N ? ep_unpack_t<DT>(__ldg(head.bias + col)).x : 0.0f;
+      }
+      __syncwarp();
+    }
+    float z[2][32];
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      const bool got = mbar_wait_long(bar_cfull + 8u * buf, buf_phase, abort_flag);
+      if (!__all_sync(0xffffffffu, got)) return;
+      tc_fence_after_sync();
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kFfnMaxBN + part * 32);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if (b >= mine) break;
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(taddr + (uint32_t)(b * 128), r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z[b][j] = c == 0 ? __uint_as_float(r[j]) : z[b][j] + __uint_as_float(r[j]);
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CL == 2) mbar_arrive_cluster(map_to_cta(bar_cempty + 8u * buf, 0u));
+        else mbar_arrive(bar_cempty + 8u * buf);
+      }
+      if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (b >= mine) break;
+      if (head.bias != nullptr) head_add(z[b], sbias + b * 32);
+      if (nc + b * 128 + 32 > job.N) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (nc + b * 128 + j >= job.N) z[b][j] = -INFINITY;
+      }
+      head_pick(z[b], target - (nc + b * 128), head.picked, row);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) top = fmaxf(top, z[b][j]);
+    }
+    const float top2 = top * kHeadLog2e, base = head_base(top2);
+    float sum = 0.0f;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (b >= mine) break;
+      sum += head_exp_sum(z[b], base);
+    }
+    if (row < job.M) head.partial[((size_t)tile.nb * kHeadParts + part) * job.M + row] = make_float2(top2, sum);
+  }
+}
+
 // CHUNKS: some sum has more than one chunk (host: FfnSpace).  A form of its own,
 // because the code for it costs the others 2 - 3% (1024 x 1024 x 768 gradients
 // 16.4 -> 17.0 us).
-template <int CL, bool GATED, int DT, bool CHUNKS>
-__global__ void __launch_bounds__(ffn_threads(GATED), 1)
-    ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemmArgs args) {
+template <int CL, int MODE, int DT, bool CHUNKS>
+__global__ void __launch_bounds__(ffn_threads(MODE == kFfnGated), 1)
+    ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnModeArgs<MODE> args) {
   using L = FfnLayout;
+  constexpr bool GATED = MODE == kFfnGated;
+  constexpr bool LOGITS = MODE == kFfnLse || MODE == kFfnDz;
+  constexpr bool ROWS = GATED || LOGITS;  // both operands K-major, one job
   constexpr bool PAIR = CL == 2;
   constexpr int EPI_WARPS = ffn_epi_warps(GATED), MMA_WARP = EPI_WARPS, PROD_WARP = EPI_WARPS + 1;  // A's; then B's
   constexpr int STG = L::STG_BOXES / EPI_WARPS;  // staging boxes of a warp
@@ -613,11 +727,11 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
             for (int h = 0; h < SUB; ++h) {
               const int k0 = kc + h * kFfnBK;
               if constexpr (IS_A)
-                ffn_load<CL>(!GATED && ji == 1, stage_a(stage) + (uint32_t)(h * A_SUB),
+                ffn_load<CL>(!ROWS && ji == 1, stage_a(stage) + (uint32_t)(h * A_SUB),
                              &maps.a[ji][GATED ? 0 : (ji == 1 ? tile.g : part)], fbl, arow, kFfnBM, k0);
               if constexpr (IS_B) {
                 const uint32_t db = stage_b(stage) + (uint32_t)(h * B_SUB);
-                ffn_load<CL>(!GATED, db, &maps.b[ji][GATED ? (PAIR ? (int)rank : 0) : (ji == 1 ? 0 : part)], fbl, brow,
+                ffn_load<CL>(!ROWS, db, &maps.b[ji][GATED ? (PAIR ? (int)rank : 0) : (ji == 1 ? 0 : part)], fbl, brow,
                              GATED ? BN / 2 : BN / CL, k0);
                 if constexpr (GATED && !PAIR)
                   ffn_load<CL>(false, db + (uint32_t)(BN / 2) * 128u, &maps.b[0][1], fbl, brow, BN / 2, k0);
@@ -631,10 +745,10 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
       auto load_jobs = [&](auto op) {
         const std::integral_constant<int, 0> j0;
         const std::integral_constant<int, 1> j1;
-        if (GATED || args.deal.first == 0) {
+        if (ROWS || args.deal.first == 0) {
           load_job(j0, op);
-          if constexpr (!GATED) load_job(j1, op);
-        } else {
+          if constexpr (!ROWS) load_job(j1, op);
+        } else if constexpr (!ROWS) {
           load_job(j1, op);
           load_job(j0, op);
         }
@@ -671,7 +785,7 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
       // 4096 x 14336, both gradients: 1073 us against 1006)
       auto issue_job = [&](auto ji_tag) {
         constexpr int ji = decltype(ji_tag)::value;
-        constexpr bool A_MN = !GATED && ji == 1, B_MN = !GATED;
+        constexpr bool A_MN = !ROWS && ji == 1, B_MN = !ROWS;
         // 16 elements along K: 32 bytes inside the swizzle row (K-major), two
         // 8-row groups (MN-major)
         constexpr uint32_t AK = A_MN ? 2048u >> 4 : 2u, BKS = B_MN ? 2048u >> 4 : 2u;
@@ -685,7 +799,7 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
           const int s = (int)(q - job.by_split.div(q) * (uint32_t)job.split);
           const int kb0 = s * job.kb_split, kb1 = min(job.kb_total, kb0 + job.kb_split);
           for (int kc = kb0;;) {  // chunks
-            const int kend = CHUNKS ? min(kb1, kc + ffn_chunk_kb(CL, DT)) : kb1;
+            const int kend = CHUNKS ? min(kb1, kc + ffn_mode_chunk_kb<MODE>(CL, DT)) : kb1;
             if (!mbar_wait(bar_cempty(buf), buf_phase ^ 1u, abort_flag)) { ok = false; break; }
             tc_fence_after_sync();
             const uint32_t d_tmem = tmem_base + (uint32_t)(buf * kFfnMaxBN);
@@ -718,10 +832,10 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
           if (!ok) break;
         }
       };
-      if (GATED || args.deal.first == 0) {
+      if (ROWS || args.deal.first == 0) {
         issue_job(std::integral_constant<int, 0>{});
-        if constexpr (!GATED) issue_job(std::integral_constant<int, 1>{});
-      } else {
+        if constexpr (!ROWS) issue_job(std::integral_constant<int, 1>{});
+      } else if constexpr (!ROWS) {
         issue_job(std::integral_constant<int, 1>{});
         issue_job(std::integral_constant<int, 0>{});
       }
@@ -742,10 +856,17 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
     int buf = 0;
     uint32_t buf_phase = 0;
     grid_dep_wait();
-    if (!GATED && args.bias_grad.outputs > 0)
+    float out_scale = 1.0f;
+    if constexpr (MODE == kFfnScaled) out_scale = args.head.scale[1];
+    if (!ROWS && args.bias_grad.outputs > 0)
       // (16 x 32 x 9 FP32 over the staging boxes of all epilogue warps)
-      ffn_bias_grad<DT>(args.bias_grad, reinterpret_cast<float*>(smem + L::OFF_STG), (int)blockIdx.x, (int)gridDim.x);
-    const int tiles0 = sched.count(sched.first), tiles = tiles0 + (GATED ? 0 : sched.count(1 - sched.first));
+      ffn_bias_grad<DT, MODE == kFfnScaled>(args.bias_grad, out_scale, reinterpret_cast<float*>(smem + L::OFF_STG),
+                                            (int)blockIdx.x, (int)gridDim.x);
+    if constexpr (MODE == kFfnLse)
+      ffn_lse_rows<CL, DT>(args, sched, reinterpret_cast<float*>(stg0), tmem_base, bar_cfull(0), bar_cempty(0), abort_flag,
+                           (int)rank);
+    const int tiles0 = MODE == kFfnLse ? 0 : sched.count(sched.first),
+              tiles = tiles0 + (ROWS ? 0 : sched.count(1 - sched.first));
     for (int ti = 0; ti < tiles; ++ti) {
       const int ji = ti < tiles0 ? sched.first : 1 - sched.first, t = sched.tile(ji, ti < tiles0 ? ti : ti - tiles0);
       const FfnJob& job = args.job[ji];
@@ -833,7 +954,10 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d(&maps.partial[ji], smem_addr(stg), nc + 16 * h, m0, slab);
+            if (MODE == kFfnScaled && ji == 0 && head_accumulates(args))
+              tma_add_3d(&maps.partial[ji], smem_addr(stg), nc + 16 * h, m0, slab);
+            else
+              tma_store_3d(&maps.partial[ji], smem_addr(stg), nc + 16 * h, m0, slab);
             bulk_commit_group();
           }
         }
@@ -864,6 +988,8 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
           else mbar_arrive(bar_cempty(buf));
         }
       };
+      HeadRow hrow;  // of this lane's row
+      if constexpr (MODE == kFfnDz) hrow = head_row(args.head, m0 + lane, M);
       bool ok = true;
       if constexpr (CHUNKS) {
         // all chunks but the last: added up in the scratch
@@ -952,13 +1078,33 @@ __global__ void __launch_bounds__(ffn_threads(GATED), 1)
           else if (args.act == kActGeluTanh) gate(std::integral_constant<int, kActGeluTanh>{});
           else gate(std::integral_constant<int, kActGeluErf>{});
         } else {
+          uint16_t* const sbias = reinterpret_cast<uint16_t*>(smem + L::OFF_BIAS) + (buf * 8 + bx) * 32;
+          const bool biased = MODE == kFfnDz && head_bias(args) != nullptr;
+          if (biased) {  // (as in the gated tile, by the four warps of a box)
+            sbias[lane] = nc + lane < N ? __ldg(head_bias(args) + nc + lane) : (uint16_t)0;
+            __syncwarp();
+          }
           tmem_ld_wait();
           if (chunked) ffn_add_scratch(scratch(bx), r);
+          if (biased) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float v[8];
+              ffn_unpack8<DT>(reinterpret_cast<const uint4*>(sbias)[j], v);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) r[8 * j + k] = __float_as_uint(__uint_as_float(r[8 * j + k]) + v[k]);
+            }
+          }
           if (bx + EPI_WARPS / 4 >= boxes) {
             release();
             held = false;
           }
-          if (job.split > 1) store_partial(r, g * job.split + s, nc);
+          if constexpr (MODE == kFfnDz) head_gradient(r, hrow, nc);
+          if (job.split > 1 || (MODE == kFfnScaled && ji == 0 && head_sums(args))) store_partial(r, g * job.split + s, nc);
+          else if constexpr (MODE == kFfnScaled)
+            store_box(g, nc, [&](int i) {
+              return ep_pack_t<DT>(__uint_as_float(r[2 * i]) * out_scale, __uint_as_float(r[2 * i + 1]) * out_scale);
+            });
           else
             store_box(g, nc, [&](int i) { return ep_pack_t<DT>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])); });
         }

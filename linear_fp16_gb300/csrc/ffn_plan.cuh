@@ -135,13 +135,16 @@ struct FfnPlan {
 // One family of products (see FfnJob) before it is planned.
 struct FfnProduct {
   bool gated = false, mn_a = false;
+  bool logits = false;  // both operands K-major, one product (the vocabulary head's)
   Operand a[2], b[2];
   int parts = 1, outputs = 1;
   int64_t rows = 0, cols = 0, kext = 0;  // of one output; K extent of one part
   void* y[3] = {nullptr, nullptr, nullptr};
+  int64_t ldy = 0;      // row pitch of y; 0: contiguous
+  bool sum = false;     // the output stays FP32 sums, added up over launches
   int64_t kb() const { return ceil_div(kext, kFfnBK) * parts; }
   size_t partial_bytes(int split) const {
-    return split > 1 ? round256(size_t(split) * (gated ? 2 : outputs) * rows * ceil_div(cols, 4) * 16) : 0;
+    return split > 1 || sum ? round256(size_t(split) * (gated ? 2 : outputs) * rows * ceil_div(cols, 4) * 16) : 0;
   }
 };
 
@@ -203,7 +206,7 @@ inline double plan_time(const FfnProduct* const* ps, int count, const FfnShape& 
   return std::max(t + last, bytes / 5.95e6) + added;
 }
 
-inline FfnPlan plan_ffn(const FfnProduct* const* ps, int count, int sms) {
+inline FfnPlan plan_ffn(const FfnProduct* const* ps, int count, int sms, bool may_split = true) {
   double bytes = 0;
   for (int i = 0; i < count; ++i) {
     const FfnProduct& q = *ps[i];
@@ -219,7 +222,7 @@ inline FfnPlan plan_ffn(const FfnProduct* const* ps, int count, int sms) {
     for (int i = 0; i < count; ++i) {
       const FfnProduct& q = *ps[i];
       const int64_t tiles = ceil_div(q.rows, kFfnBM * s.cl) * ceil_div(q.cols, q.gated ? s.bn / 2 : s.bn) * q.outputs;
-      for (int S = 2; S <= 16 && tiles * S <= 2 * (sms / s.cl) && q.kb() >= 4 * S; S *= 2) {
+      for (int S = 2; may_split && !q.sum && S <= 16 && tiles * S <= 2 * (sms / s.cl) && q.kb() >= 4 * S; S *= 2) {
         int trial[2] = {split[0], split[1]};
         trial[i] = S;
         const double u = plan_time(ps, count, s, trial, sms, bytes);
@@ -336,8 +339,9 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
     j.by_span = FfnDiv(static_cast<uint32_t>(j.group_m) * static_cast<uint32_t>(j.num_n));
     j.by_group = FfnDiv(static_cast<uint32_t>(j.group_m));
     j.by_rest = FfnDiv(static_cast<uint32_t>((j.num_m - 1) % j.group_m + 1));
-    const int ny = q.gated ? (ep.save ? 3 : 1) : q.outputs;
-    j.tma_store = j.split == 1 && q.cols % 8 == 0;
+    const int ny = q.gated ? (ep.save ? 3 : 1) : (q.y[0] != nullptr ? q.outputs : 0);
+    const int64_t ldy = q.ldy != 0 ? q.ldy : q.cols;
+    j.tma_store = j.split == 1 && !q.sum && ldy % 8 == 0;
     for (int o = 0; o < ny; ++o) {
       j.y[o] = static_cast<uint16_t*>(q.y[o]);
       if (!aligned(q.y[o], 16)) j.tma_store = 0;
@@ -349,11 +353,11 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
     const int na = q.gated ? 1 : (q.mn_a ? q.outputs : q.parts), nb = q.gated ? 2 : (q.mn_a ? 1 : q.parts);
     bool ok = true;
     for (int o = 0; o < na; ++o) ok = ok && encode(&m.a[ji][o], q.a[o], q.mn_a, kFfnBM);
-    for (int o = 0; o < nb; ++o) ok = ok && encode(&m.b[ji][o], q.b[o], !q.gated, p.bn / 2);
+    for (int o = 0; o < nb; ++o) ok = ok && encode(&m.b[ji][o], q.b[o], !q.gated && !q.logits, q.logits ? p.bn / p.cl : p.bn / 2);
     if (j.tma_store)
       for (int o = 0; o < ny; ++o)
-        ok = ok && encode_2d(&m.y[ji][o], q.y[o], q.cols, q.rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, bf16);
-    if (j.split > 1)
+        ok = ok && encode_2d(&m.y[ji][o], q.y[o], q.cols, q.rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, bf16, ldy);
+    if (j.split > 1 || q.sum)
       ok = ok && encode_3d_f32(&m.partial[ji], partial[i], ceil_div(q.cols, 4) * 4, q.rows,
                                uint64_t(j.split) * (q.gated ? 2 : q.outputs), 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
     if (!ok) return cuda_fail(cudaErrorInvalidValue);
@@ -386,7 +390,7 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
   for (int i = 0; i < count; ++i) {
     const FfnProduct& q = *ps[i];
     const FfnJob& j = a.job[q.mn_a ? 1 : 0];
-    if (j.split == 1) continue;
+    if (j.split == 1 || q.sum) continue;
     const cudaError_t r = launch_reduce(q, j, partial[i]);
     if (r != cudaSuccess) return cuda_fail(r);
   }

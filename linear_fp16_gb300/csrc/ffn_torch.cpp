@@ -1,15 +1,17 @@
-// The tensor-level calls of the feed-forward operators: argument checks on
-// torch tensors, allocation of the results, and the call of the C entry point
-// (include/poot_ffn.h) on a stream.  No computation.
+// The tensor-level calls of the feed-forward and the training operators:
+// argument checks on torch tensors, allocation of the results, and the call of
+// the C entry point (include/poot_ffn.h, include/poot_train.h) on a stream.  No
+// computation.
 //
 // A decode step or a small model's gradients take ten microseconds on the
 // GPU; the same checks and allocations in Python took 15 - 25 (GB300 host,
-// 1024 x 1024 x 768 gradients: 28 us a call against 17.6).  ffn.py holds the
+// 1024 x 1024 x 768 gradients: 28 us a call against 17.6).  ffn.py and train.py hold the
 // documented functions, which pass their arguments through.
 //
 // A function returns its result, or the status code (an int) that is not
 // POOT_OK, or raises TypeError / ValueError for arguments it cannot take.
 #include "tensor_call.h"
+#include "train_calls.h"
 
 #include <vector>
 
@@ -176,6 +178,8 @@ PyMethodDef g_methods[] = {method<gated_linear>("gated_linear"),
                            method<gated_linear_backward>("gated_linear_backward"),
                            method<linear_backward>("linear_backward"),
                            method<clip_grad_norm>("clip_grad_norm"),
+                           method<linear_cross_entropy>("linear_cross_entropy"),
+                           method<linear_cross_entropy_backward>("linear_cross_entropy_backward"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ffn_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -55,6 +55,8 @@ inline int device_query(int dev, int* sms) {
 // The feed-forward kernels' device error word on the current device, read
 // and cleared (poot_ffn.cu).
 cudaError_t take_ffn_device_error(unsigned int* word);
+// The vocabulary head's, likewise (poot_head.cu).
+cudaError_t take_head_device_error(unsigned int* word);
 
 // Launch with programmatic stream serialisation (see grid_dep_wait in
 // ptx.cuh): the kernel may be scheduled while the previous kernel in the

@@ -1073,11 +1073,14 @@ int poot_linear_device_status(poot_stream_t stream) {
     e = cudaMemcpyToSymbol(poot::g_device_error, &zero, sizeof(zero));
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  // the feed-forward kernels' word (their own translation unit)
+  // the words of the feed-forward and of the head's kernels (translation units of their own)
   unsigned int ffn_word = 0;
   e = take_ffn_device_error(&ffn_word);
   if (e != cudaSuccess) return cuda_fail(e);
-  return (word | ffn_word) != 0 ? POOT_ERR_DEVICE_TIMEOUT : POOT_OK;
+  unsigned int head_word = 0;
+  e = take_head_device_error(&head_word);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return (word | ffn_word | head_word) != 0 ? POOT_ERR_DEVICE_TIMEOUT : POOT_OK;
 }
 
 int poot_linear_version(void) { return kVersion; }
