@@ -88,6 +88,78 @@ typedef struct poot_linear_cross_entropy_backward_args {
 POOT_API int poot_linear_cross_entropy_backward(const poot_linear_cross_entropy_backward_args* args,
                                                 poot_stream_t stream);
 
+/*
+ * One AdamW step (Loshchilov and Hutter, decoupled weight decay) over a list of tensors:
+ *   g = grad * grad_scale
+ *   m = beta1 m + (1 - beta1) g           v = beta2 v + (1 - beta2) g^2
+ *   param = param (1 - lr weight_decay)
+ *           - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ *   copy  = param                          where copy is given
+ * in FP32, each operation rounded on its own in this order; the factors that depend on lr,
+ * weight_decay, step and the betas alone are computed in FP64 and rounded once.  param is rounded
+ * once to its dtype.  Equal calls give equal bits, whatever else is in the list.
+ * param, grad: binary16, bfloat16 or FP32 (POOT_GRAD_*), any alignment of their elements; copy:
+ * binary16 or bfloat16, for an FP32 param (master weights).
+ * bits 32: m and v are FP32 [n].  bits 8: m is int8 [n], v uint8 [n], and each has an FP32
+ * scale for every POOT_ADAMW_BLOCK elements in order ([ceil(n / 256)]):
+ *   m = m_scale c |c|       (-127 <= c <= 127, m_scale = max |m| / 127^2)
+ *   v = (v_scale c^2)^2     (0 <= c <= 255, v_scale = max sqrt(v) / 255^2)
+ * The step itself uses the new m and v before they are rounded to codes; codes are
+ * nearest in c, a nonzero v has a code of at least 1, and a block whose |m| are all below 2^-110
+ * counts as zero.  An average moves only when a step changes it by half the distance of two codes:
+ * 0.8% of m and of v at the top of a block, more below.  A block with an m or v that is not finite
+ * reads as NaN.  All zeros are a valid first state in either form.
+ * step counts from 1.  lr, step and grad_scale are read from device memory
+ * when the step runs where lr_device, step_device or grad_scale_device is given
+ * (a captured graph follows them); with lr_device, 1 - lr weight_decay is one FP32 operation.
+ * Tensors may be empty.  What a call writes may overlap nothing else of it.
+ * Errors: POOT_ERR_INVALID_ARG (count < 0, NULL, n < 0 or n > 2^40, an unknown dtype or
+ * bits, a copy of a 16-bit param, beta outside [0, 1), eps, lr or weight_decay negative or not
+ * finite, a grad_scale that is not finite, step < 1, overlap), POOT_ERR_MISALIGNED (a pointer
+ * below its element's alignment), POOT_ERR_CUDA.
+ */
+#define POOT_ADAMW_BLOCK 256
+
+typedef struct poot_adamw_tensor {
+    void* param;
+    const void* grad;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    void* copy;
+    int64_t n;
+    double weight_decay;
+    int param_dtype, grad_dtype, copy_dtype;
+} poot_adamw_tensor;
+
+typedef struct poot_adamw_args {
+    const poot_adamw_tensor* tensors;
+    int64_t count;
+    const float* lr_device;
+    const int64_t* step_device;
+    const float* grad_scale_device;
+    int64_t step;
+    double lr, beta1, beta2, eps, grad_scale;
+    int bits;
+} poot_adamw_args;
+POOT_API int poot_adamw_step(const poot_adamw_args* args, poot_stream_t stream);
+
+/*
+ * The FP32 values that 8-bit states stand for (for a checkpoint, or to look at
+ * them): m_out and v_out, [n] each.  Errors as above.
+ */
+typedef struct poot_adamw_codes {
+    const void* m;
+    const void* v;
+    const float* m_scale;
+    const float* v_scale;
+    float* m_out;
+    float* v_out;
+    int64_t n;
+} poot_adamw_codes;
+POOT_API int poot_adamw_values(const poot_adamw_codes* states, int64_t count, poot_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

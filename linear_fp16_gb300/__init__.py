@@ -6,7 +6,7 @@ contraction (bfloat16 heads, no bias, FP32 output, fused epilogue steps);
 ``clip_grad_norm`` are the feed-forward block, its gradients and the clip
 before an update;
 ``linear_cross_entropy`` and ``linear_cross_entropy_backward`` are the loss of a
-vocabulary head and its gradients;
+vocabulary head and its gradients, ``adamw_step`` the update with the clipped gradients;
 ``column_parallel_linear`` and ``row_parallel_linear`` split the op over
 torch.distributed ranks;
 the C entry points of include/poot_linear.h are mirrored one to one in
@@ -31,7 +31,8 @@ from .ffn import (  # noqa: F401
     linear_backward, poot_clip_grad_norm, poot_gated_linear, poot_gated_linear_backward, poot_linear_backward,
 )
 from .train import (  # noqa: F401
-    LinearCrossEntropyArgs, LinearCrossEntropyBackwardArgs, linear_cross_entropy, linear_cross_entropy_backward,
+    ADAMW_BLOCK, AdamWState, AdamwArgs, AdamwCodes, AdamwTensor, LinearCrossEntropyArgs, LinearCrossEntropyBackwardArgs,
+    adamw_state, adamw_step, linear_cross_entropy, linear_cross_entropy_backward, poot_adamw_step, poot_adamw_values,
     poot_linear_cross_entropy, poot_linear_cross_entropy_backward,
 )
 from .tensor_parallel import (  # noqa: F401

@@ -22,10 +22,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpoot_linear.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("poot_linear.cu", "poot_ffn.cu", "poot_head.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("poot_linear.cu", "poot_ffn.cu", "poot_head.cu", "poot_adamw.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in (
     "ptx.cuh", "gemm_tcgen05.cuh", "gemv.cuh", "epilogue.cuh", "splitk.cuh", "pack.cuh", "shards.cuh", "host.cuh",
-    "mma.cuh", "ffn_plan.cuh", "ffn_gemm.cuh", "ffn_gemv.cuh", "ffn_elem.cuh", "clip.cuh", "head.cuh", "head_elem.cuh")] + [
+    "mma.cuh", "ffn_plan.cuh", "ffn_gemm.cuh", "ffn_gemv.cuh", "ffn_elem.cuh", "clip.cuh", "head.cuh", "head_elem.cuh", "adamw.cuh")] + [
     os.path.join(INCLUDE, f) for f in ("poot_linear.h", "poot_ffn.h", "poot_train.h")]
 
 EXT_SOURCE = os.path.join(CSRC, "ffn_torch.cpp")

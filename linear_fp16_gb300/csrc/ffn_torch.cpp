@@ -180,6 +180,8 @@ PyMethodDef g_methods[] = {method<gated_linear>("gated_linear"),
                            method<clip_grad_norm>("clip_grad_norm"),
                            method<linear_cross_entropy>("linear_cross_entropy"),
                            method<linear_cross_entropy_backward>("linear_cross_entropy_backward"),
+                           method<adamw_step>("adamw_step"),
+                           method<adamw_values>("adamw_values"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ffn_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -122,11 +122,11 @@ class Run {
     if (index != device) refuse(PyExc_ValueError, "%s must be one of the tensors' device", "stream");
     stream_ = c10::cuda::CUDAStream::unpack3(id, static_cast<c10::DeviceIndex>(index), static_cast<c10::DeviceType>(type));
   }
-  at::Tensor empty(std::initializer_list<int64_t> shape, at::ScalarType dtype) {
+  at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype) {
     const auto options = at::TensorOptions().dtype(dtype).device(at::kCUDA, device_);
-    if (stream_ == current_) return at::empty(at::IntArrayRef(shape), options);
+    if (stream_ == current_) return at::empty(shape, options);
     c10::cuda::CUDAStreamGuard guard(stream_);
-    at::Tensor t = at::empty(at::IntArrayRef(shape), options);
+    at::Tensor t = at::empty(shape, options);
     c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), current_);
     return t;
   }

@@ -2,7 +2,8 @@
 
 ``linear_cross_entropy`` is the softmax cross entropy of a vocabulary head z =
 x W^T + b, without the logits in memory, and ``linear_cross_entropy_backward``
-its gradients.  Like the feed-forward calls
+its gradients.  ``adamw_step`` updates a list of parameters with the clipped
+gradients; ``adamw_state`` makes the state that it keeps, in 32 or in 8 bits.  Like the feed-forward calls
 (``ffn``) they record no graph for torch's automatic differentiation: tensors
 that require gradients are taken as values.  The functions named like the C
 entry points (include/poot_train.h) take the argument structures and return
@@ -33,10 +34,31 @@ class LinearCrossEntropyBackwardArgs(ctypes.Structure):
                 + [(n, _I64) for n in ("M", "V", "K", "ldx", "dloss_stride", "ignore_index")] + [("dtype", _INT)])
 
 
+class AdamwTensor(ctypes.Structure):
+    """struct poot_adamw_tensor."""
+    _fields_ = ([(n, _VP) for n in ("param", "grad", "m", "v", "m_scale", "v_scale", "copy")]
+                + [("n", _I64), ("weight_decay", ctypes.c_double)]
+                + [(n, _INT) for n in ("param_dtype", "grad_dtype", "copy_dtype")])
+
+
+class AdamwArgs(ctypes.Structure):
+    """struct poot_adamw_args."""
+    _fields_ = ([("tensors", ctypes.POINTER(AdamwTensor)), ("count", _I64)]
+                + [(n, _VP) for n in ("lr_device", "step_device", "grad_scale_device")] + [("step", _I64)]
+                + [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "grad_scale")] + [("bits", _INT)])
+
+
+class AdamwCodes(ctypes.Structure):
+    """struct poot_adamw_codes."""
+    _fields_ = [(n, _VP) for n in ("m", "v", "m_scale", "v_scale", "m_out", "v_out")] + [("n", _I64)]
+
+
 # (restype, argtypes) of every function of include/poot_train.h
 EXPORTS = {
     "poot_linear_cross_entropy": (_INT, [ctypes.POINTER(LinearCrossEntropyArgs), _VP]),
     "poot_linear_cross_entropy_backward": (_INT, [ctypes.POINTER(LinearCrossEntropyBackwardArgs), _VP]),
+    "poot_adamw_step": (_INT, [ctypes.POINTER(AdamwArgs), _VP]),
+    "poot_adamw_values": (_INT, [ctypes.POINTER(AdamwCodes), _I64, _VP]),
 }
 
 _lock = threading.Lock()
@@ -70,6 +92,16 @@ def poot_linear_cross_entropy(args, stream: int) -> int:
 def poot_linear_cross_entropy_backward(args, stream: int) -> int:
     """args: a LinearCrossEntropyBackwardArgs instance."""
     return load_library().poot_linear_cross_entropy_backward(_ref(args), stream)
+
+
+def poot_adamw_step(args, stream: int) -> int:
+    """args: an AdamwArgs instance."""
+    return load_library().poot_adamw_step(_ref(args), stream)
+
+
+def poot_adamw_values(states, count: int, stream: int) -> int:
+    """states: an array of AdamwCodes (or None with count 0)."""
+    return load_library().poot_adamw_values(states, count, stream)
 
 
 # ---- tensor-level calls (checks and allocation: csrc/train_calls.h) ----------
@@ -110,3 +142,75 @@ def linear_cross_entropy_backward(dloss, x, w, target, lse, bias=None, *, ignore
     if r.__class__ is int:
         raise _b.PootLinearError(r, "poot_linear_cross_entropy_backward")
     return r
+
+
+ADAMW_BLOCK = 256  # elements that share a scale of an 8-bit state
+
+
+class AdamWState:
+    """The averages m and v that adamw_step keeps for a list of parameters.
+
+    32 bits: lists ``m`` and ``v`` of float32 tensors, shaped like the
+    parameters.  8 bits: int8 ``m`` and uint8 ``v``, shaped likewise, with float32
+    ``m_scale`` and ``v_scale`` of one element for each 256 of a parameter, in order
+    (include/poot_train.h has the codes).  The lists may be saved and
+    given again; ``adamw_state`` makes them for a first step.
+    """
+
+    def __init__(self, m, v, m_scale=None, v_scale=None):
+        self.m, self.v = list(m), list(v)
+        self.m_scale, self.v_scale = list(m_scale or ()) or None, list(v_scale or ()) or None
+
+    @property
+    def bits(self) -> int:
+        return 32 if self.m_scale is None else 8
+
+    def values(self, *, stream=None):
+        """(m, v): lists of float32 tensors; with 8 bits new ones, what the codes stand for."""
+        if self.m_scale is None:
+            return self.m, self.v
+        r = _calls().adamw_values(self.m, self.v, self.m_scale, self.v_scale, _ffn._stream(stream))
+        if r.__class__ is int:
+            raise _b.PootLinearError(r, "poot_adamw_values")
+        return r
+
+
+def adamw_state(params, *, bits: int = 32) -> AdamWState:
+    """A state of zeros for adamw_step, beside each of the parameters."""
+    import torch
+    if bits not in (32, 8):
+        raise ValueError(f"bits must be 32 or 8, not {bits!r}")
+    params = list(params)
+
+    def zeros(dtype, shape=None):
+        return [torch.zeros(p.shape if shape is None else shape(p), dtype=dtype, device=p.device) for p in params]
+    if bits == 32:
+        return AdamWState(zeros(torch.float32), zeros(torch.float32))
+
+    def blocks(p):
+        return -(-p.numel() // ADAMW_BLOCK)
+    return AdamWState(zeros(torch.int8), zeros(torch.uint8), zeros(torch.float32, blocks), zeros(torch.float32, blocks))
+
+
+def adamw_step(params, grads, state: AdamWState, *, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+               weight_decay=0.01, grad_scale=1.0, copies=None, stream=None) -> None:
+    """One AdamW step over all parameters at once, in place.
+
+    With g = grad * grad_scale: m = b1 m + (1 - b1) g, v = b2 v + (1 - b2) g^2,
+    p = p (1 - lr weight_decay) - lr / (1 - b1^step) m / (sqrt(v) / sqrt(1 -
+    b2^step) + eps).  params and grads: sequences of contiguous CUDA tensors of
+    one device (float16, bfloat16 or float32, any mixture).  ``copies``: a
+    sequence of float16 or bfloat16 tensors (or None in places) that receive the
+    new values of float32 parameters.  ``weight_decay``: one number, or one for each
+    tensor.  ``step`` counts from 1.  ``step`` (int64), ``lr`` and
+    ``grad_scale`` (float32) may be CUDA tensors of one element, read when the step
+    runs: a captured graph follows them.  Tensors written to count as modified
+    in place; ones that require gradients are written all the same.  An empty
+    sequence raises ValueError.  Streams and errors as in gated_linear.
+    """
+    decay = weight_decay if isinstance(weight_decay, (int, float)) else list(weight_decay)
+    r = _calls().adamw_step(list(params), list(grads), state.m, state.v, state.m_scale, state.v_scale,
+                            None if copies is None else list(copies), decay, step, lr, grad_scale, betas[0], betas[1],
+                            eps, _ffn._stream(stream))
+    if r is not None:
+        raise _b.PootLinearError(r, "poot_adamw_step")

@@ -3,7 +3,6 @@
 Argument errors are found before any CUDA call, so no GPU is needed; the
 addresses are never dereferenced.
 """
-import ctypes
 import os
 import re
 
@@ -31,8 +30,7 @@ def test_structures_match_the_header():
     for body, name in re.findall(r"typedef struct \w+ \{(.*?)\} (\w+);", src, flags=re.S):
         fields = [f.strip(" *") for line in body.split(";") if line.strip()
                   for f in re.sub(r"^\s*(const\s+)?\w+", "", line.strip()).split(",")]
-        cls = getattr(L, "".join(part.capitalize() for part in name[len("poot_"):].split("_"))
-                      .replace("Adamw", "AdamW"))
+        cls = getattr(L, "".join(part.capitalize() for part in name[len("poot_"):].split("_")))
         assert [f for f, _ in cls._fields_] == fields, name
 
 
@@ -107,3 +105,90 @@ def test_tensor_calls_refuse_what_they_cannot_take():
         L.linear_cross_entropy([1.0], w, t)
     with pytest.raises(ValueError):
         L.linear_cross_entropy_backward(lse, x, w, t, lse)
+
+
+B = A[0]
+NAN, INF = float("nan"), float("inf")
+
+
+def tensors(*changes):
+    """Parameters of 8 elements far apart, with the changes made to each."""
+    out = []
+    for i, kw in enumerate(changes):
+        base = B + i * 0x1000_0000
+        d = dict(param=base, grad=base + 0x100_0000, m=base + 0x200_0000, v=base + 0x300_0000, m_scale=base + 0x400_0000,
+                 v_scale=base + 0x500_0000, copy=0, n=8, weight_decay=0.01, param_dtype=2, grad_dtype=1, copy_dtype=1)
+        d.update(kw)
+        out.append(L.AdamwTensor(**d))
+    return (L.AdamwTensor * max(1, len(out)))(*out)
+
+
+def adamw(*changes, **kw):
+    d = dict(tensors=tensors(*changes), count=len(changes), step=1, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8,
+             grad_scale=1.0, bits=32)
+    d.update(kw)
+    return L.poot_adamw_step(L.AdamwArgs(**d), 0)
+
+
+@pytest.mark.parametrize("changes,kw,code", [
+    ([{}], dict(count=-1), INV), ([{}], dict(tensors=None), INV), ([{}], dict(bits=16), INV),
+    ([{}], dict(beta1=1.0), INV), ([{}], dict(beta1=-0.1), INV), ([{}], dict(beta2=1.0), INV), ([{}], dict(beta2=NAN), INV),
+    ([{}], dict(eps=-1e-8), INV), ([{}], dict(eps=NAN), INV), ([{}], dict(lr=-1.0), INV), ([{}], dict(lr=INF), INV),
+    ([{}], dict(step=0), INV), ([{}], dict(grad_scale=INF), INV), ([{}], dict(lr_device=A[3] + 2), MIS),
+    ([{}], dict(step_device=A[3] + 4), MIS), ([{}], dict(grad_scale_device=A[3] + 1), MIS),
+    ([dict(n=-1)], {}, INV), ([dict(n=(1 << 40) + 1)], {}, INV), ([dict(param_dtype=3)], {}, INV),
+    ([dict(grad_dtype=-1)], {}, INV), ([dict(weight_decay=-1.0)], {}, INV), ([dict(weight_decay=NAN)], {}, INV),
+    ([dict(param=0)], {}, INV), ([dict(grad=0)], {}, INV), ([dict(m=0)], {}, INV), ([dict(v=0)], {}, INV),
+    ([dict(m_scale=0)], dict(bits=8), INV), ([dict(v_scale=0)], dict(bits=8), INV),
+    ([dict(copy=B + 0x600_0000, copy_dtype=2)], {}, INV), ([dict(copy=B + 0x600_0000, param_dtype=1)], {}, INV),
+    ([dict(param=B + 2)], {}, MIS), ([dict(grad=B + 0x100_0001)], {}, MIS), ([dict(m=B + 0x200_0002)], {}, MIS),
+    ([dict(copy=B + 0x600_0001)], {}, MIS), ([dict(m_scale=B + 0x400_0002)], dict(bits=8), MIS),
+    ([dict(grad=B + 16)], {}, INV),                                     # inside the parameter
+    ([dict(v=B + 0x200_0000)], {}, INV),                                # m and v the same
+    ([dict(m=B + 28)], {}, INV), ([dict(v_scale=B + 0x200_0004)], dict(bits=8), INV),
+    ([{}, dict(param=B)], {}, INV),                                     # one parameter twice
+    ([{}, dict(param=B + 0x100_0000)], {}, INV),                        # a parameter that is another's gradient
+    ([{}, dict(copy=B + 0x100_0000)], {}, INV),                         # a copy over another's gradient
+    ([{}], dict(step_device=B + 0x200_0000), INV), ([{}], dict(lr_device=B + 4), INV),
+])
+def test_adamw_refusals(changes, kw, code):
+    assert adamw(*changes, **kw) == code
+
+
+def test_adamw_takes():
+    assert L.poot_adamw_step(None, 0) == INV
+    assert adamw() == L.POOT_OK and adamw(dict(n=0, param=0, grad=0, m=0, v=0)) == L.POOT_OK
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    # every check passes; the device query then fails without a GPU
+    assert adamw({}, {}) == L.POOT_ERR_CUDA
+    assert adamw(dict(grad=B + 0x100_0000), dict(grad=B + 0x100_0000)) == L.POOT_ERR_CUDA   # one gradient for two
+    assert adamw(dict(m=B + 0x200_0001, v=B + 0x300_0003), bits=8) == L.POOT_ERR_CUDA       # codes anywhere
+    assert adamw({}, step=0, step_device=A[3], lr=NAN, lr_device=A[4], grad_scale=NAN,
+                 grad_scale_device=A[5]) == L.POOT_ERR_CUDA
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=-1), INV), (dict(m=0), INV), (dict(v_scale=0), INV), (dict(m_out=0), INV), (dict(m_scale=A[2] + 1), MIS),
+    (dict(v_out=A[5] + 2), MIS), (dict(m_out=A[0]), INV), (dict(v_out=A[4] + 16), INV), (dict(n=0, m=0), L.POOT_OK),
+])
+def test_adamw_values_refusals(kw, code):
+    d = dict(m=A[0], v=A[1], m_scale=A[2], v_scale=A[3], m_out=A[4], v_out=A[5], n=8)
+    d.update(kw)
+    assert L.poot_adamw_values((L.AdamwCodes * 1)(L.AdamwCodes(**d)), 1, 0) == code
+
+
+def test_adamw_calls_refuse_what_they_cannot_take():
+    p = [torch.zeros(4, 8)]
+    for bits in (32, 8):
+        state = L.adamw_state(p, bits=bits)
+        assert state.bits == bits and [t.shape for t in state.m] == [(4, 8)]
+        with pytest.raises(ValueError):
+            L.adamw_step(p, p, state, step=1)          # CPU tensors
+    assert state.m[0].dtype == torch.int8 and state.v[0].dtype == torch.uint8 and state.m_scale[0].shape == (1,)
+    with pytest.raises(ValueError):
+        L.adamw_step([], [], state, step=1)
+    with pytest.raises(ValueError):
+        L.adamw_step(p, [], state, step=1)
+    with pytest.raises(ValueError):
+        L.adamw_state(p, bits=16)
