@@ -58,6 +58,7 @@ struct AdamArgs {
   double lr, log_b1, log_b2;
   long long step;
   float b1, omb1, b2, omb2, eps, grad_scale;
+  float minus_zero;             // -0, unknown to the compiler: see adam_product
   float step_size, root_scale;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
 };
 
@@ -152,13 +153,53 @@ struct AdamCodes {
   }
 };
 
-__device__ __forceinline__ float adam_m(uint32_t w, int j, float scale) {
-  const float c = (float)(int8_t)(w >> (8 * (j & 3)));
-  return __fmul_rn(scale, __fmul_rn(c, fabsf(c)));  // c |c| is exact
+// Two FP32 operations in one instruction, each rounded to nearest.
+__device__ __forceinline__ float2 adam_add(float2 a, float2 b) {
+  add_f32x2(a.x, a.y, b.x, b.y);
+  return a;
 }
-__device__ __forceinline__ float adam_root(uint32_t w, int j, float scale) {
-  const float c = (float)(uint8_t)(w >> (8 * (j & 3)));
-  return __fmul_rn(scale, __fmul_rn(c, c));
+__device__ __forceinline__ float2 adam_mul(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 s, t;\n\t"
+      "mov.b64 s, {%2, %3};\n\t"
+      "mov.b64 t, {%4, %5};\n\t"
+      "mul.rn.f32x2 s, s, t;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 adam_fma(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 s, t, u;\n\t"
+      "mov.b64 s, {%2, %3};\n\t"
+      "mov.b64 t, {%4, %5};\n\t"
+      "mov.b64 u, {%6, %7};\n\t"
+      "fma.rn.f32x2 s, s, t, u;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 adam_both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 adam_neg(float2 v) { return make_float2(-v.x, -v.y); }
+
+// Bytes j and j + 1 of a word as floats: in the low bits of 2^23's, which is then
+// taken off (conversions run at an eighth of the rate).
+__device__ __forceinline__ float2 adam_bytes(uint32_t w, int j, float off) {
+  const float2 t = make_float2(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | (j & 3))),
+                               __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | ((j & 3) + 1))));
+  return adam_add(t, adam_both(off));
+}
+// w ^ 0x80808080: c + 128 in 0 .. 255
+__device__ __forceinline__ float2 adam_m(uint32_t w, int j, float scale) {
+  const float2 c = adam_bytes(w ^ 0x80808080u, j, -8388736.0f);
+  // (c |c| is exact)
+  return adam_mul(adam_both(scale), make_float2(__fmul_rn(c.x, fabsf(c.x)), __fmul_rn(c.y, fabsf(c.y))));
+}
+__device__ __forceinline__ float2 adam_root(uint32_t w, int j, float scale) {
+  const float2 c = adam_bytes(w, j, -8388608.0f);
+  return adam_mul(adam_both(scale), adam_mul(c, c));
 }
 
 // The scale of a block whose largest value has the bits `most` (as integers, those of
@@ -178,30 +219,104 @@ __device__ __forceinline__ AdamScale adam_scale(uint32_t most) {
   return {__fmul_rn(f, kPart), __fmul_rn(__frcp_rn(f), kSquare)};
 }
 
-// The integer c nearest to sqrt(y), y in 0 .. 255^2 (1 + 2^-22): c + 1 from y > (c + 1/2)^2 on.
+// Two integers c nearest to sqrt(y), y in 0 .. 255^2 (1 + 2^-22): c + 1 from y > (c + 1/2)^2 on.
 // The square root is approximate; taken 2^-10 low, its rounding is the result or
 // one less, and the comparison, exact in FP32, decides.
-__device__ __forceinline__ uint32_t adam_code(float y) {
-  float s;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(y));
-  const float t = (s - 0.0009765625f) + 8388608.0f;  // 2^23: the sum's low bits are the rounded value
-  const float c = t - 8388608.0f;
-  return (__float_as_uint(t) & 0xffu) + (y > fmaf(c, c, c) + 0.25f ? 1u : 0u);
+__device__ __forceinline__ uint2 adam_code(float2 y) {
+  float2 s;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(y.x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(y.y));
+  // 2^23: the sum's low bits are the rounded value
+  const float2 t = adam_add(adam_add(s, adam_both(-0.0009765625f)), adam_both(8388608.0f));
+  const float2 c = adam_add(t, adam_both(-8388608.0f));
+  const float2 edge = adam_add(adam_fma(c, c, c), adam_both(0.25f));
+  return make_uint2((__float_as_uint(t.x) & 0xffu) + (y.x > edge.x ? 1u : 0u),
+                    (__float_as_uint(t.y) & 0xffu) + (y.y > edge.y ? 1u : 0u));
 }
 
 struct AdamHyper {
-  float b1, omb1, b2, omb2, eps, grad_scale, step_size, root_scale, lr;
+  float b1, omb1, b2, omb2, eps, grad_scale, step_size, root_scale, lr, minus_zero;
 };
 
-// One element: m and v updated, sqrt(v) and the new p.
-__device__ __forceinline__ void adam_element(const AdamHyper& h, float decay, float g, float& p, float& m, float& v,
-                                             float& root) {
-  g = __fmul_rn(g, h.grad_scale);
-  m = __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.omb1));
-  v = __fadd_rn(__fmul_rn(v, h.b2), __fmul_rn(__fmul_rn(g, g), h.omb2));
-  root = __fsqrt_rn(v);
-  const float step = __fdiv_rn(m, __fadd_rn(__fmul_rn(root, h.root_scale), h.eps));
-  p = __fsub_rn(__fmul_rn(p, decay), __fmul_rn(step, h.step_size));
+// a b rounded, for a sum: the assembler fuses a packed product with the addition behind it, .rn or
+// not, but not a product that is one already (adding -0 changes nothing).
+__device__ __forceinline__ float2 adam_product(const AdamHyper& h, float2 a, float b) {
+  return adam_fma(a, adam_both(b), adam_both(h.minus_zero));
+}
+
+// sqrt(v) correctly rounded, for v of 2^-100 .. 2^100: from an approximate 1 /
+// sqrt(v) one coupled Newton step for sqrt and half its reciprocal, then the
+// remainder v - g^2, exact in an FMA, added back (P. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990).
+__device__ __forceinline__ float2 adam_sqrt(float2 v) {
+  float2 y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(v.x));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(v.y));
+  float2 g = adam_mul(v, y), h = adam_mul(y, adam_both(0.5f));
+  const float2 e = adam_fma(adam_neg(h), g, adam_both(0.5f));
+  g = adam_fma(g, e, g);
+  h = adam_fma(h, e, h);
+  return adam_fma(adam_fma(adam_neg(g), g, v), h, g);
+}
+
+// m / d rounded to nearest likewise, for d of 2^-60 .. 2^60 and m of 2^-75 or more (below, the
+// remainder may be subnormal and the last place off by one).
+__device__ __forceinline__ float2 adam_div(float2 m, float2 d) {
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+  const float2 n = adam_neg(d);
+  r = adam_fma(adam_fma(n, r, adam_both(1.0f)), r, r);
+  const float2 q = adam_mul(m, r);
+  return adam_fma(adam_fma(n, q, m), r, q);
+}
+
+// A lane's eight elements: m and v updated, sqrt(v) and the new p.  All 32 lanes call it.
+__device__ __forceinline__ void adam_update(const AdamHyper& h, float decay, const float (&gs)[8], float (&p)[8],
+                                            float (&m)[8], float (&v)[8], float (&root)[8]) {
+  float lo = INFINITY, hi = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float2 g = adam_mul(make_float2(gs[j], gs[j + 1]), adam_both(h.grad_scale));
+    const float2 a = adam_add(adam_product(h, make_float2(m[j], m[j + 1]), h.b1), adam_product(h, g, h.omb1));
+    const float2 b = adam_add(adam_product(h, make_float2(v[j], v[j + 1]), h.b2),
+                              adam_product(h, adam_mul(g, g), h.omb2));
+    m[j] = a.x;
+    m[j + 1] = a.y;
+    v[j] = b.x;
+    v[j + 1] = b.y;
+    lo = fminf(lo, fminf(b.x, b.y));
+    hi = fmaxf(hi, fmaxf(b.x, b.y));
+  }
+  // (NaN comes through either way.  Zeros, of elements that have had no gradient yet, take the second.)
+  const bool plain = lo >= 7.888609052210118e-31f && hi <= 1.2676506002282294e30f && h.eps <= 1e15f;
+  if (__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float2 r = adam_sqrt(make_float2(v[j], v[j + 1]));
+      const float2 d = adam_add(adam_product(h, r, h.root_scale), adam_both(h.eps));
+      const float2 q = adam_div(make_float2(m[j], m[j + 1]), d);
+      const float2 n = adam_add(adam_product(h, make_float2(p[j], p[j + 1]), decay), adam_product(h, q, -h.step_size));
+      root[j] = r.x;
+      root[j + 1] = r.y;
+      p[j] = n.x;
+      p[j + 1] = n.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      root[j] = __fsqrt_rn(v[j]);
+      const float q = __fdiv_rn(m[j], __fadd_rn(__fmul_rn(root[j], h.root_scale), h.eps));
+      p[j] = __fsub_rn(__fmul_rn(p[j], decay), __fmul_rn(q, h.step_size));
+    }
+  }
+}
+
+// NaN where either is
+__device__ __forceinline__ float adam_max(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 struct AdamTensor {
@@ -231,8 +346,7 @@ __device__ __forceinline__ void adam_chunk(const AdamTensor& t, const AdamHyper&
     lp.get(p);
     lm.get(m);
     lv.get(v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) adam_element(h, t.decay, g[j], p[j], m[j], v[j], root[j]);
+    adam_update(h, t.decay, g, p, m, v, root);
     adam_store<kGradF32, VEC>(t.m, e0, n, lane, m);
     adam_store<kGradF32, VEC>(t.v, e0, n, lane, v);
   } else {
@@ -243,26 +357,34 @@ __device__ __forceinline__ void adam_chunk(const AdamTensor& t, const AdamHyper&
     const float ms = t.ms[block], vs = t.vs[block];
     lg.get(g);
     lp.get(p);
-    uint32_t most_m = 0, most_r = 0;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float2 a = adam_m(cm.w[j >> 2], j, ms), r = adam_root(cv.w[j >> 2], j, vs), b = adam_mul(r, r);
+      m[j] = a.x;
+      m[j + 1] = a.y;
+      v[j] = b.x;
+      v[j + 1] = b.y;
+    }
+    adam_update(h, t.decay, g, p, m, v, root);
+    float most_m = 0.0f, most_r = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      m[j] = adam_m(cm.w[j >> 2], j, ms);
-      const float r = adam_root(cv.w[j >> 2], j, vs);
-      v[j] = __fmul_rn(r, r);
-      adam_element(h, t.decay, g[j], p[j], m[j], v[j], root[j]);
-      most_m = max(most_m, __float_as_uint(fabsf(m[j])));
-      most_r = max(most_r, __float_as_uint(fabsf(root[j])));
+      most_m = adam_max(most_m, fabsf(m[j]));
+      most_r = adam_max(most_r, root[j]);
     }
     // (elements that do not exist are zeros times the scale: NaN in a block that was not finite, as it stays)
-    const AdamScale sm = adam_scale<127>(__reduce_max_sync(0xffffffffu, most_m));
-    const AdamScale sv = adam_scale<255>(__reduce_max_sync(0xffffffffu, most_r));
+    const AdamScale sm = adam_scale<127>(__reduce_max_sync(0xffffffffu, __float_as_uint(most_m)));
+    const AdamScale sv = adam_scale<255>(__reduce_max_sync(0xffffffffu, __float_as_uint(most_r)));
     cm.w[0] = cm.w[1] = cv.w[0] = cv.w[1] = 0u;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t c = adam_code(__fmul_rn(fabsf(m[j]), sm.inverse));
-      cm.w[j >> 2] |= ((m[j] < 0.0f ? 0u - c : c) & 0xffu) << (8 * (j & 3));
-      const uint32_t k = adam_code(__fmul_rn(root[j], sv.inverse));
-      cv.w[j >> 2] |= ((root[j] > 0.0f ? max(k, 1u) : k) & 0xffu) << (8 * (j & 3));
+    for (int j = 0; j < 8; j += 2) {
+      const uint2 c = adam_code(adam_mul(make_float2(fabsf(m[j]), fabsf(m[j + 1])), adam_both(sm.inverse)));
+      const uint2 k = adam_code(adam_mul(make_float2(root[j], root[j + 1]), adam_both(sv.inverse)));
+      const uint32_t c0 = m[j] < 0.0f ? 0u - c.x : c.x, c1 = m[j + 1] < 0.0f ? 0u - c.y : c.y;
+      const uint32_t k0 = root[j] > 0.0f ? max(k.x, 1u) : k.x, k1 = root[j + 1] > 0.0f ? max(k.y, 1u) : k.y;
+      // bytes 0 of four words
+      cm.w[j >> 2] |= __byte_perm(c0, c1, (j & 2) ? 0x4000 : 0x0040) & ((j & 2) ? 0xffff0000u : 0xffffu);
+      cv.w[j >> 2] |= __byte_perm(k0, k1, (j & 2) ? 0x4000 : 0x0040) & ((j & 2) ? 0xffff0000u : 0xffffu);
     }
     cm.store(t.m, e0, n, lane);
     cv.store(t.v, e0, n, lane);
@@ -319,7 +441,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
   __shared__ AdamHyper shared;
   grid_dep_wait();
   grid_dep_launch();
-  AdamHyper h{a.b1, a.omb1, a.b2, a.omb2, a.eps, a.grad_scale, a.step_size, a.root_scale, 0.0f};
+  AdamHyper h{a.b1, a.omb1, a.b2, a.omb2, a.eps, a.grad_scale, a.step_size, a.root_scale, 0.0f, a.minus_zero};
   if (a.lr_dev != nullptr || a.step_dev != nullptr || a.grad_scale_dev != nullptr) {
     if (threadIdx.x == 0) {
       const double lr = a.lr_dev != nullptr ? (double)*a.lr_dev : a.lr;
@@ -380,10 +502,12 @@ __device__ __forceinline__ void adam_expand(const void* m, const void* v, float 
   cv.load(v, e0, n, lane);
   float fm[8], fv[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    fm[j] = adam_m(cm.w[j >> 2], j, ms);
-    const float r = adam_root(cv.w[j >> 2], j, vs);
-    fv[j] = __fmul_rn(r, r);
+  for (int j = 0; j < 8; j += 2) {
+    const float2 a = adam_m(cm.w[j >> 2], j, ms), r = adam_root(cv.w[j >> 2], j, vs), b = adam_mul(r, r);
+    fm[j] = a.x;
+    fm[j + 1] = a.y;
+    fv[j] = b.x;
+    fv[j + 1] = b.y;
   }
   adam_store<kGradF32, VEC>(mo, e0, n, lane, fm);
   adam_store<kGradF32, VEC>(vo, e0, n, lane, fv);

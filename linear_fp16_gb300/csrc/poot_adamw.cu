@@ -181,6 +181,7 @@ int adamw_step(const poot_adamw_args* ap, cudaStream_t stream) {
   a.omb2 = static_cast<float>(1.0 - p.beta2);
   a.eps = static_cast<float>(p.eps);
   a.grad_scale = static_cast<float>(p.grad_scale);
+  a.minus_zero = -0.0f;
   if (p.lr_device == nullptr && p.step_device == nullptr)
     adam_factors(p.lr, a.log_b1, a.log_b2, static_cast<double>(p.step), &a.step_size, &a.root_scale);
   const int most = d->blocks[small ? 1 : 0];

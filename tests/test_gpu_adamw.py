@@ -176,6 +176,20 @@ def test_codes_are_nearest_and_values_are_what_they_stand_for():
         assert bool((cv[root.flatten() > 0] >= 1).all())
 
 
+def test_roots_and_quotients_are_rounded_to_nearest():
+    """Every significand of v (1 <= v < 4: powers of 4 only shift the exponent) and
+    many of m: with g = 0, betas of 1/2 and factors of 1 the step leaves p = -m / sqrt(v)."""
+    v = torch.arange(0x3f800000, 0x40800000, device=DEV, dtype=torch.int64).to(torch.int32).view(torch.float32)
+    gen = torch.Generator(device=DEV).manual_seed(12)
+    for exponent in (0, -90, 90):
+        for m in (torch.ones_like(v), torch.randn(v.shape, generator=gen, device=DEV),
+                  torch.randn(v.shape, generator=gen, device=DEV) * 1e-3):
+            p, s = torch.zeros_like(v), v * 2.0 ** exponent
+            L.adamw_step([p], [torch.zeros_like(v)], L.AdamWState([2 * m], [2 * s]), step=2 ** 40, lr=1.0,
+                         betas=(0.5, 0.5), eps=0.0, weight_decay=0.0)
+            assert torch.equal(p, -(m / s.sqrt()))
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_copies_of_master_weights(bits):
     host, dev = make([300, 4096, 77, 1000], torch.float32, torch.bfloat16, bits, 4)
