@@ -30,6 +30,10 @@ namespace poot {
 constexpr int kAdamThreads = 256;
 constexpr int kAdamWarps = kAdamThreads / 32;
 constexpr int kAdamBlock = 256;     // elements of a scale, and of a warp's turn
+// Shared memory of a block with states in 8 bits: two chunks a warp, of up to 4
+// + 4 bytes of p and g and two codes an element
+constexpr int kAdamStage = kAdamBlock * (4 + 4 + 2);
+constexpr int kAdamSmem = 2 * kAdamWarps * kAdamStage;
 constexpr int kAdamTable = 384;     // tensors of one launch
 constexpr int kAdamTableFew = 48;   // short lists: less to pass to the launch
 
@@ -48,7 +52,7 @@ struct AdamTable {
   unsigned char types[T];  // GradDtype of p, g << 2, copy << 4; kAdamVec
   int count;
 };
-constexpr int kAdamVec = 64;  // every pointer is on a boundary of four elements
+constexpr int kAdamVec = 64;  // every pointer is on a 16-byte boundary
 
 struct AdamArgs {
   // read on the device where not nullptr
@@ -62,13 +66,23 @@ struct AdamArgs {
   float step_size, root_scale;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
 };
 
-// Eight elements of a lane: two fours 128 apart (VEC), or every 32nd; `n` of the
-// chunk's 256 exist, the others are zero.
-template <int DT, bool VEC>
+// Which eight elements of a chunk a lane has: every 32nd, of which `n` of the
+// 256 exist (the others are zero); two fours, 128 apart; or consecutive ones, in shared
+// memory and where they are stored.
+enum AdamLane : int { kAdamEach = 0, kAdamFours = 1, kAdamEight = 2 };
+
+template <int DT, int VEC>
 struct AdamLoad {
   uint32_t w[DT == kGradF32 ? 8 : 4];
   __device__ __forceinline__ void load(const void* base, long long e0, int n, int lane) {
-    if constexpr (VEC && DT == kGradF32) {
+    if constexpr (VEC == kAdamEight) {
+      const uint4* p = static_cast<const uint4*>(base) + lane * (DT == kGradF32 ? 2 : 1);
+#pragma unroll
+      for (int i = 0; i < (DT == kGradF32 ? 2 : 1); ++i) {
+        const uint4 a = p[i];
+        w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
+      }
+    } else if constexpr (VEC && DT == kGradF32) {
       const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + e0) + lane;
       const uint4 a = p[0], b = p[32];
       w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
@@ -105,9 +119,16 @@ struct AdamLoad {
   }
 };
 
-template <int DT, bool VEC>
+template <int DT, int VEC>
 __device__ __forceinline__ void adam_store(void* base, long long e0, int n, int lane, const float (&f)[8]) {
-  if constexpr (VEC && DT == kGradF32) {
+  if constexpr (VEC == kAdamEight && DT == kGradF32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + e0) + lane * 2;
+    p[0] = make_float4(f[0], f[1], f[2], f[3]);
+    p[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else if constexpr (VEC == kAdamEight) {
+    reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + e0)[lane] =
+        make_uint4(ep_pack_t<DT>(f[0], f[1]), ep_pack_t<DT>(f[2], f[3]), ep_pack_t<DT>(f[4], f[5]), ep_pack_t<DT>(f[6], f[7]));
+  } else if constexpr (VEC && DT == kGradF32) {
     float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + e0) + lane;
     p[0] = make_float4(f[0], f[1], f[2], f[3]);
     p[32] = make_float4(f[4], f[5], f[6], f[7]);
@@ -125,12 +146,16 @@ __device__ __forceinline__ void adam_store(void* base, long long e0, int n, int 
 }
 
 // ---- codes -------------------------------------------------------------------
-template <bool VEC>
+template <int VEC>
 struct AdamCodes {
   uint32_t w[2];  // byte j & 3 of word j >> 2
   __device__ __forceinline__ void load(const void* base, long long e0, int n, int lane) {
     const unsigned char* p = static_cast<const unsigned char*>(base) + e0;
-    if constexpr (VEC) {
+    if constexpr (VEC == kAdamEight) {
+      const uint2 a = reinterpret_cast<const uint2*>(p)[lane];
+      w[0] = a.x;
+      w[1] = a.y;
+    } else if constexpr (VEC) {
       w[0] = reinterpret_cast<const uint32_t*>(p)[lane];
       w[1] = reinterpret_cast<const uint32_t*>(p)[32 + lane];
     } else {
@@ -142,7 +167,9 @@ struct AdamCodes {
   }
   __device__ __forceinline__ void store(void* base, long long e0, int n, int lane) const {
     unsigned char* p = static_cast<unsigned char*>(base) + e0;
-    if constexpr (VEC) {
+    if constexpr (VEC == kAdamEight) {
+      reinterpret_cast<uint2*>(p)[lane] = make_uint2(w[0], w[1]);
+    } else if constexpr (VEC) {
       reinterpret_cast<uint32_t*>(p)[lane] = w[0];
       reinterpret_cast<uint32_t*>(p)[32 + lane] = w[1];
     } else {
@@ -182,7 +209,8 @@ __device__ __forceinline__ float2 adam_fma(float2 a, float2 b, float2 c) {
   return r;
 }
 __device__ __forceinline__ float2 adam_both(float v) { return make_float2(v, v); }
-__device__ __forceinline__ float2 adam_neg(float2 v) { return make_float2(-v.x, -v.y); }
+// (packed operands take no sign)
+__device__ __forceinline__ float2 adam_neg(float2 v) { return adam_mul(v, adam_both(-1.0f)); }
 
 // Bytes j and j + 1 of a word as floats: in the low bits of 2^23's, which is then
 // taken off (conversions run at an eighth of the rate).
@@ -222,16 +250,24 @@ __device__ __forceinline__ AdamScale adam_scale(uint32_t most) {
 // Two integers c nearest to sqrt(y), y in 0 .. 255^2 (1 + 2^-22): c + 1 from y > (c + 1/2)^2 on.
 // The square root is approximate; taken 2^-10 low, its rounding is the result or
 // one less, and the comparison, exact in FP32, decides.
-__device__ __forceinline__ uint2 adam_code(float2 y) {
-  float2 s;
+__device__ __forceinline__ float2 adam_code(float2 y) {
+  float2 s, up;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(y.x));
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(y.y));
-  // 2^23: the sum's low bits are the rounded value
-  const float2 t = adam_add(adam_add(s, adam_both(-0.0009765625f)), adam_both(8388608.0f));
-  const float2 c = adam_add(t, adam_both(-8388608.0f));
+  // (beside 2^23 only integers are left)
+  const float2 c = adam_add(adam_add(adam_add(s, adam_both(-0.0009765625f)), adam_both(8388608.0f)), adam_both(-8388608.0f));
   const float2 edge = adam_add(adam_fma(c, c, c), adam_both(0.25f));
-  return make_uint2((__float_as_uint(t.x) & 0xffu) + (y.x > edge.x ? 1u : 0u),
-                    (__float_as_uint(t.y) & 0xffu) + (y.y > edge.y ? 1u : 0u));
+  asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(up.x) : "f"(y.x), "f"(edge.x));
+  asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(up.y) : "f"(y.y), "f"(edge.y));
+  return adam_add(c, up);
+}
+// The low bytes of four integers, in two's complement.
+__device__ __forceinline__ uint32_t adam_pack(float2 a, float2 b) {
+  a = adam_add(a, adam_both(12582912.0f));  // 1.5 2^23
+  b = adam_add(b, adam_both(12582912.0f));
+  const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
 }
 
 struct AdamHyper {
@@ -252,11 +288,11 @@ __device__ __forceinline__ float2 adam_sqrt(float2 v) {
   float2 y;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(v.x));
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(v.y));
-  float2 g = adam_mul(v, y), h = adam_mul(y, adam_both(0.5f));
-  const float2 e = adam_fma(adam_neg(h), g, adam_both(0.5f));
+  float2 g = adam_mul(v, y), h = adam_mul(y, adam_both(-0.5f));  // h: minus half the reciprocal
+  const float2 e = adam_fma(h, g, adam_both(0.5f));
   g = adam_fma(g, e, g);
   h = adam_fma(h, e, h);
-  return adam_fma(adam_fma(adam_neg(g), g, v), h, g);
+  return adam_fma(adam_fma(g, g, adam_neg(v)), h, g);
 }
 
 // m / d rounded to nearest likewise, for d of 2^-60 .. 2^60 and m of 2^-75 or more (below, the
@@ -271,9 +307,17 @@ __device__ __forceinline__ float2 adam_div(float2 m, float2 d) {
   return adam_fma(adam_fma(n, q, m), r, q);
 }
 
-// A lane's eight elements: m and v updated, sqrt(v) and the new p.  All 32 lanes call it.
-__device__ __forceinline__ void adam_update(const AdamHyper& h, float decay, const float (&gs)[8], float (&p)[8],
-                                            float (&m)[8], float (&v)[8], float (&root)[8]) {
+// NaN where one is
+__device__ __forceinline__ float adam_max(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// A lane's eight elements: m and v updated, sqrt(v) and the new p; `most`: the largest v.
+// Whether all the warp's v are of 2^-100 .. 2^100.  All 32 lanes call it.
+__device__ __forceinline__ bool adam_update(const AdamHyper& h, float decay, const float (&gs)[8], float (&p)[8],
+                                            float (&m)[8], float (&v)[8], float (&root)[8], float& most) {
   float lo = INFINITY, hi = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
@@ -286,11 +330,13 @@ __device__ __forceinline__ void adam_update(const AdamHyper& h, float decay, con
     v[j] = b.x;
     v[j + 1] = b.y;
     lo = fminf(lo, fminf(b.x, b.y));
-    hi = fmaxf(hi, fmaxf(b.x, b.y));
+    hi = adam_max(hi, adam_max(b.x, b.y));
   }
-  // (NaN comes through either way.  Zeros, of elements that have had no gradient yet, take the second.)
-  const bool plain = lo >= 7.888609052210118e-31f && hi <= 1.2676506002282294e30f && h.eps <= 1e15f;
-  if (__all_sync(0xffffffffu, plain)) {
+  most = hi;
+  // (zeros, of elements that have had no gradient yet, and NaN take the second way)
+  const bool plain =
+      __all_sync(0xffffffffu, lo >= 7.888609052210118e-31f && hi <= 1.2676506002282294e30f && h.eps <= 1e15f);
+  if (plain) {
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
       const float2 r = adam_sqrt(make_float2(v[j], v[j + 1]));
@@ -310,13 +356,7 @@ __device__ __forceinline__ void adam_update(const AdamHyper& h, float decay, con
       p[j] = __fsub_rn(__fmul_rn(p[j], decay), __fmul_rn(q, h.step_size));
     }
   }
-}
-
-// NaN where either is
-__device__ __forceinline__ float adam_max(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
+  return plain;
 }
 
 struct AdamTensor {
@@ -330,67 +370,106 @@ struct AdamTensor {
   int copy_dtype;
 };
 
-// 256 elements from e0 on (`n` of them exist).
-template <int PD, int GD, int BITS, bool VEC>
-__device__ __forceinline__ void adam_chunk(const AdamTensor& t, const AdamHyper& h, long long e0, int n, int lane) {
-  AdamLoad<PD, VEC> lp;
-  AdamLoad<GD, VEC> lg;
-  lg.load(t.g, e0, n, lane);
-  lp.load(t.p, e0, n, lane);
-  float p[8], g[8], m[8], v[8], root[8];
+// 256 elements of a tensor as they come from memory, `n` of which exist.
+template <int PD, int GD, int BITS, int VEC>
+struct AdamChunk {
+  AdamLoad<PD, VEC> p;
+  AdamLoad<GD, VEC> g;
+  AdamLoad<kGradF32, VEC> m, v;
+  __device__ __forceinline__ void load(const AdamTensor& t, long long e0, int n, int lane) {
+    g.load(t.g, e0, n, lane);
+    p.load(t.p, e0, n, lane);
+    m.load(t.m, e0, n, lane);
+    v.load(t.v, e0, n, lane);
+  }
+};
+template <int PD, int GD, int VEC>
+struct AdamChunk<PD, GD, 8, VEC> {
+  AdamLoad<PD, VEC> p;
+  AdamLoad<GD, VEC> g;
+  AdamCodes<VEC> m, v;
+  float ms, vs;
+  __device__ __forceinline__ void load(const AdamTensor& t, long long e0, int n, int lane) {
+    g.load(t.g, e0, n, lane);
+    p.load(t.p, e0, n, lane);
+    m.load(t.m, e0, n, lane);
+    v.load(t.v, e0, n, lane);
+    ms = t.ms[e0 / kAdamBlock];
+    vs = t.vs[e0 / kAdamBlock];
+  }
+};
+
+// A chunk on its way to a warp's shared memory, 16 bytes a lane and copy.
+template <int DT>
+__device__ __forceinline__ void adam_fetch(uint32_t stage, const void* base, long long e0, int lane) {
+  const char* p = static_cast<const char*>(base) + e0 * (DT == kGradF32 ? 4 : 2) + lane * 16;
+  cp_async_16(stage + lane * 16, p, 16);
+  if constexpr (DT == kGradF32) cp_async_16(stage + 512 + lane * 16, p + 512, 16);
+}
+constexpr int kAdamStageG = kAdamBlock * 4, kAdamStageM = kAdamBlock * 8, kAdamStageV = kAdamBlock * 9;
+template <int PD, int GD>
+__device__ __forceinline__ void adam_fetch_chunk(uint32_t stage, const AdamTensor& t, long long e0, int lane) {
+  adam_fetch<GD>(stage + kAdamStageG, t.g, e0, lane);
+  adam_fetch<PD>(stage, t.p, e0, lane);
+  // codes: m by the lower lanes, v by the upper
+  const char* c = static_cast<const char*>(lane < 16 ? t.m : t.v) + e0 + (lane & 15) * 16;
+  cp_async_16(stage + kAdamStageM + lane * 16, c, 16);
+}
+
+// Its step, from e0 on.
+template <int PD, int GD, int BITS, int VEC>
+__device__ __forceinline__ void adam_chunk(const AdamTensor& t, const AdamHyper& h, const AdamChunk<PD, GD, BITS, VEC>& x,
+                                           long long e0, int n, int lane) {
+  float p[8], g[8], m[8], v[8], root[8], most_v;
+  x.g.get(g);
+  x.p.get(p);
   if constexpr (BITS == 32) {
-    AdamLoad<kGradF32, VEC> lm, lv;
-    lm.load(t.m, e0, n, lane);
-    lv.load(t.v, e0, n, lane);
-    lg.get(g);
-    lp.get(p);
-    lm.get(m);
-    lv.get(v);
-    adam_update(h, t.decay, g, p, m, v, root);
+    x.m.get(m);
+    x.v.get(v);
+    adam_update(h, t.decay, g, p, m, v, root, most_v);
     adam_store<kGradF32, VEC>(t.m, e0, n, lane, m);
     adam_store<kGradF32, VEC>(t.v, e0, n, lane, v);
   } else {
-    AdamCodes<VEC> cm, cv;
-    cm.load(t.m, e0, n, lane);
-    cv.load(t.v, e0, n, lane);
-    const long long block = e0 / kAdamBlock;
-    const float ms = t.ms[block], vs = t.vs[block];
-    lg.get(g);
-    lp.get(p);
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-      const float2 a = adam_m(cm.w[j >> 2], j, ms), r = adam_root(cv.w[j >> 2], j, vs), b = adam_mul(r, r);
+      const float2 a = adam_m(x.m.w[j >> 2], j, x.ms), r = adam_root(x.v.w[j >> 2], j, x.vs), b = adam_mul(r, r);
       m[j] = a.x;
       m[j + 1] = a.y;
       v[j] = b.x;
       v[j + 1] = b.y;
     }
-    adam_update(h, t.decay, g, p, m, v, root);
-    float most_m = 0.0f, most_r = 0.0f;
+    const bool positive = adam_update(h, t.decay, g, p, m, v, root, most_v);
+    float most_m = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      most_m = adam_max(most_m, fabsf(m[j]));
-      most_r = adam_max(most_r, root[j]);
-    }
-    // (elements that do not exist are zeros times the scale: NaN in a block that was not finite, as it stays)
+    for (int j = 0; j < 8; ++j) most_m = adam_max(most_m, fabsf(m[j]));
+    // (elements that do not exist are zeros times the scale: NaN in a block that was not finite, as it stays.
+    // The largest sqrt(v) is the largest v's.)
     const AdamScale sm = adam_scale<127>(__reduce_max_sync(0xffffffffu, __float_as_uint(most_m)));
-    const AdamScale sv = adam_scale<255>(__reduce_max_sync(0xffffffffu, __float_as_uint(most_r)));
-    cm.w[0] = cm.w[1] = cv.w[0] = cv.w[1] = 0u;
+    const AdamScale sv = adam_scale<255>(__float_as_uint(
+        __fsqrt_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most_v))))));
+    AdamCodes<VEC> cm, cv;
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const uint2 c = adam_code(adam_mul(make_float2(fabsf(m[j]), fabsf(m[j + 1])), adam_both(sm.inverse)));
-      const uint2 k = adam_code(adam_mul(make_float2(root[j], root[j + 1]), adam_both(sv.inverse)));
-      const uint32_t c0 = m[j] < 0.0f ? 0u - c.x : c.x, c1 = m[j + 1] < 0.0f ? 0u - c.y : c.y;
-      const uint32_t k0 = root[j] > 0.0f ? max(k.x, 1u) : k.x, k1 = root[j + 1] > 0.0f ? max(k.y, 1u) : k.y;
-      // bytes 0 of four words
-      cm.w[j >> 2] |= __byte_perm(c0, c1, (j & 2) ? 0x4000 : 0x0040) & ((j & 2) ? 0xffff0000u : 0xffffu);
-      cv.w[j >> 2] |= __byte_perm(k0, k1, (j & 2) ? 0x4000 : 0x0040) & ((j & 2) ? 0xffff0000u : 0xffffu);
+    for (int w = 0; w < 2; ++w) {
+      float2 c[2], k[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = 4 * w + 2 * i;
+        c[i] = adam_code(make_float2(__fmul_rn(fabsf(m[j]), sm.inverse), __fmul_rn(fabsf(m[j + 1]), sm.inverse)));
+        c[i] = make_float2(copysignf(c[i].x, m[j]), copysignf(c[i].y, m[j + 1]));
+        k[i] = adam_code(adam_mul(make_float2(root[j], root[j + 1]), adam_both(sv.inverse)));
+        if (positive)
+          k[i] = make_float2(fmaxf(k[i].x, 1.0f), fmaxf(k[i].y, 1.0f));
+        else
+          k[i] = make_float2(root[j] > 0.0f ? fmaxf(k[i].x, 1.0f) : k[i].x, root[j + 1] > 0.0f ? fmaxf(k[i].y, 1.0f) : k[i].y);
+      }
+      cm.w[w] = adam_pack(c[0], c[1]);
+      cv.w[w] = adam_pack(k[0], k[1]);
     }
     cm.store(t.m, e0, n, lane);
     cv.store(t.v, e0, n, lane);
     if (lane == 0) {
-      t.ms[block] = sm.scale;
-      t.vs[block] = sv.scale;
+      t.ms[e0 / kAdamBlock] = sm.scale;
+      t.vs[e0 / kAdamBlock] = sv.scale;
     }
   }
   adam_store<PD, VEC>(t.p, e0, n, lane, p);
@@ -400,19 +479,88 @@ __device__ __forceinline__ void adam_chunk(const AdamTensor& t, const AdamHyper&
   }
 }
 
-template <int BITS, bool VEC>
-__device__ __forceinline__ void adam_dispatch(int types, const AdamTensor& t, const AdamHyper& h, long long e0, int n,
-                                              int lane) {
+// A warp's chunks of one tensor: every kAdamWarps-th from c on, below end.  States
+// in 8 bits take some sixty instructions an element, too many for loads and
+// arithmetic of the warps that fit to take turns: the next two chunks are on their way to shared
+// memory while one is worked on.
+template <int PD, int GD, int BITS>
+__device__ __forceinline__ void adam_run(const AdamTensor& t, const AdamHyper& h, bool vec, long long c, long long end,
+                                         int lane, uint8_t* stages) {
+  if (vec) {
+    const long long whole = min(end, t.n / kAdamBlock);
+    if constexpr (BITS == 8) {
+      if (c < whole) {
+        AdamChunk<PD, GD, BITS, kAdamEight> x;
+        const uint32_t sa = smem_addr(stages);
+        float ms[2], vs[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const long long d = c + i * kAdamWarps;
+          if (d < whole) {
+            adam_fetch_chunk<PD, GD>(sa + i * kAdamStage, t, d * kAdamBlock, lane);
+            ms[i] = t.ms[d];
+            vs[i] = t.vs[d];
+          }
+          cp_async_commit();
+        }
+        int slot = 0;
+        for (; c < whole; c += kAdamWarps) {
+          cp_async_wait_group<1>();
+          __syncwarp();
+          const uint8_t* from = stages + slot * kAdamStage;
+          x.g.load(from + kAdamStageG, 0, kAdamBlock, lane);
+          x.p.load(from, 0, kAdamBlock, lane);
+          x.m.load(from + kAdamStageM, 0, kAdamBlock, lane);
+          x.v.load(from + kAdamStageV, 0, kAdamBlock, lane);
+          x.ms = ms[0];
+          x.vs = vs[0];
+          ms[0] = ms[1];
+          vs[0] = vs[1];
+          __syncwarp();  // all lanes have read the slot
+          const long long d = c + 2 * kAdamWarps;
+          if (d < whole) {
+            adam_fetch_chunk<PD, GD>(sa + slot * kAdamStage, t, d * kAdamBlock, lane);
+            ms[1] = t.ms[d];
+            vs[1] = t.vs[d];
+          }
+          cp_async_commit();
+          slot ^= 1;
+          adam_chunk<PD, GD, BITS, kAdamEight>(t, h, x, c * kAdamBlock, kAdamBlock, lane);
+        }
+        cp_async_wait_group<0>();
+        __syncwarp();
+      }
+    } else {
+      AdamChunk<PD, GD, BITS, kAdamFours> x;
+      for (; c < whole; c += kAdamWarps) {
+        x.load(t, c * kAdamBlock, kAdamBlock, lane);
+        adam_chunk<PD, GD, BITS, kAdamFours>(t, h, x, c * kAdamBlock, kAdamBlock, lane);
+      }
+    }
+  }
+  for (; c < end; c += kAdamWarps) {
+    const long long e0 = c * kAdamBlock;
+    const int n = (int)min(t.n - e0, (long long)kAdamBlock);
+    AdamChunk<PD, GD, BITS, kAdamEach> x;
+    x.load(t, e0, n, lane);
+    adam_chunk<PD, GD, BITS, kAdamEach>(t, h, x, e0, n, lane);
+  }
+}
+
+template <int BITS>
+__device__ __forceinline__ void adam_dispatch(int types, const AdamTensor& t, const AdamHyper& h, long long c, long long end,
+                                              int lane, uint8_t* stages) {
+  const bool vec = (types & kAdamVec) != 0;
   switch (types & 15) {
-    case kGradF16 | kGradF16 << 2: return adam_chunk<kGradF16, kGradF16, BITS, VEC>(t, h, e0, n, lane);
-    case kGradF16 | kGradBf16 << 2: return adam_chunk<kGradF16, kGradBf16, BITS, VEC>(t, h, e0, n, lane);
-    case kGradF16 | kGradF32 << 2: return adam_chunk<kGradF16, kGradF32, BITS, VEC>(t, h, e0, n, lane);
-    case kGradBf16 | kGradF16 << 2: return adam_chunk<kGradBf16, kGradF16, BITS, VEC>(t, h, e0, n, lane);
-    case kGradBf16 | kGradBf16 << 2: return adam_chunk<kGradBf16, kGradBf16, BITS, VEC>(t, h, e0, n, lane);
-    case kGradBf16 | kGradF32 << 2: return adam_chunk<kGradBf16, kGradF32, BITS, VEC>(t, h, e0, n, lane);
-    case kGradF32 | kGradF16 << 2: return adam_chunk<kGradF32, kGradF16, BITS, VEC>(t, h, e0, n, lane);
-    case kGradF32 | kGradBf16 << 2: return adam_chunk<kGradF32, kGradBf16, BITS, VEC>(t, h, e0, n, lane);
-    default: return adam_chunk<kGradF32, kGradF32, BITS, VEC>(t, h, e0, n, lane);
+    case kGradF16 | kGradF16 << 2: return adam_run<kGradF16, kGradF16, BITS>(t, h, vec, c, end, lane, stages);
+    case kGradF16 | kGradBf16 << 2: return adam_run<kGradF16, kGradBf16, BITS>(t, h, vec, c, end, lane, stages);
+    case kGradF16 | kGradF32 << 2: return adam_run<kGradF16, kGradF32, BITS>(t, h, vec, c, end, lane, stages);
+    case kGradBf16 | kGradF16 << 2: return adam_run<kGradBf16, kGradF16, BITS>(t, h, vec, c, end, lane, stages);
+    case kGradBf16 | kGradBf16 << 2: return adam_run<kGradBf16, kGradBf16, BITS>(t, h, vec, c, end, lane, stages);
+    case kGradBf16 | kGradF32 << 2: return adam_run<kGradBf16, kGradF32, BITS>(t, h, vec, c, end, lane, stages);
+    case kGradF32 | kGradF16 << 2: return adam_run<kGradF32, kGradF16, BITS>(t, h, vec, c, end, lane, stages);
+    case kGradF32 | kGradBf16 << 2: return adam_run<kGradF32, kGradBf16, BITS>(t, h, vec, c, end, lane, stages);
+    default: return adam_run<kGradF32, kGradF32, BITS>(t, h, vec, c, end, lane, stages);
   }
 }
 
@@ -434,10 +582,14 @@ __device__ __forceinline__ int adam_find(const long long (&first)[T], int count,
   return lo;
 }
 
-// A block has consecutive chunks of all tensors', dealt out in equal shares, and its
-// warps take them in turn.
+// A block has consecutive chunks of all tensors', in equal shares, and its warps take them
+// in turn.  GB300, 705M bfloat16 elements: states in FP32 2.24 ms (6.9 TB/s, four blocks of 64 registers
+// an SM; 2.38 with one share for each resident block, as SMs differ in speed); in 8 bits 1.64 ms (4.3 TB/s, three
+// blocks of 80 registers; 1.70 with four, whose register pairs for packed constants spill), bound by the
+// issue of about 65 instructions an element.
 template <int T, int BITS>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamTable<T> t, const AdamArgs a) {
+__global__ void __launch_bounds__(kAdamThreads, BITS == 8 ? 3 : 4) adamw_kernel(const __grid_constant__ AdamTable<T> t, const AdamArgs a) {
+  extern __shared__ __align__(16) uint8_t adam_smem[];
   __shared__ AdamHyper shared;
   grid_dep_wait();
   grid_dep_launch();
@@ -455,10 +607,11 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
     h = shared;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* const stages = adam_smem + warp * 2 * kAdamStage;
   const long long chunks = t.first[t.count];
   const long long c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
   int k = adam_find(t.first, t.count, c0);
-  for (long long c = c0 + warp; c < c1; c += kAdamWarps) {
+  for (long long c = c0 + warp; c < c1;) {
     while (c >= t.first[k + 1]) ++k;
     AdamTensor x;
     x.p = t.p[k];
@@ -472,10 +625,9 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
     x.decay = a.lr_dev != nullptr ? fmaf(-h.lr, t.decay[k], 1.0f) : t.decay[k];
     const int types = t.types[k];
     x.copy_dtype = (types >> 4) & 3;
-    const long long e0 = (c - t.first[k]) * kAdamBlock;
-    const long long left = x.n - e0;
-    if ((types & kAdamVec) && left >= kAdamBlock) adam_dispatch<BITS, true>(types, x, h, e0, kAdamBlock, lane);
-    else adam_dispatch<BITS, false>(types, x, h, e0, (int)min(left, (long long)kAdamBlock), lane);
+    const long long first = t.first[k], end = min(c1, t.first[k + 1]);
+    adam_dispatch<BITS>(types, x, h, c - first, end - first, lane, stages);
+    c += (end - c + kAdamWarps - 1) / kAdamWarps * kAdamWarps;
   }
 }
 
@@ -494,7 +646,7 @@ struct AdamValueTable {
   int count;
 };
 
-template <bool VEC>
+template <int VEC>
 __device__ __forceinline__ void adam_expand(const void* m, const void* v, float ms, float vs, float* mo, float* vo,
                                             long long e0, int n, int lane) {
   AdamCodes<VEC> cm, cv;
@@ -526,9 +678,9 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_values_kernel(const __grid
     const long long block = c - t.first[k], e0 = block * kAdamBlock, left = t.n[k] - e0;
     const float ms = t.ms[k][block], vs = t.vs[k][block];
     if (t.vec[k] && left >= kAdamBlock)
-      adam_expand<true>(t.m[k], t.v[k], ms, vs, t.mo[k], t.vo[k], e0, kAdamBlock, lane);
+      adam_expand<kAdamFours>(t.m[k], t.v[k], ms, vs, t.mo[k], t.vo[k], e0, kAdamBlock, lane);
     else
-      adam_expand<false>(t.m[k], t.v[k], ms, vs, t.mo[k], t.vo[k], e0, (int)min(left, (long long)kAdamBlock), lane);
+      adam_expand<kAdamEach>(t.m[k], t.v[k], ms, vs, t.mo[k], t.vo[k], e0, (int)min(left, (long long)kAdamBlock), lane);
   }
 }
 

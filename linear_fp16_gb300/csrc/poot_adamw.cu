@@ -27,6 +27,7 @@ struct AdamDevice {
   int sms = 0;
   int blocks[2] = {0, 0};  // that run at one time: states in 32, in 8 bits
 };
+int adam_smem_bytes(bool small) { return small ? kAdamSmem : 0; }
 std::mutex g_mu;
 AdamDevice g_devices[kMaxDevices];
 
@@ -45,8 +46,11 @@ int adam_device(AdamDevice** out) {
         int few = 0, many = 0;
         auto fewer = b == 0 ? adamw_kernel<kAdamTableFew, 32> : adamw_kernel<kAdamTableFew, 8>;
         auto more = b == 0 ? adamw_kernel<kAdamTable, 32> : adamw_kernel<kAdamTable, 8>;
-        if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&few, fewer, kAdamThreads, 0)) != cudaSuccess ||
-            (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&many, more, kAdamThreads, 0)) != cudaSuccess)
+        const int smem = adam_smem_bytes(b == 1);
+        if ((e = cudaFuncSetAttribute(fewer, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(more, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess ||
+            (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&few, fewer, kAdamThreads, smem)) != cudaSuccess ||
+            (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&many, more, kAdamThreads, smem)) != cudaSuccess)
           return cuda_fail(e);
         d.blocks[b] = std::max(1, std::min(few, many)) * d.sms;
       }
@@ -85,9 +89,12 @@ inline int64_t blocks_of(int64_t n) { return (n + kAdamBlock - 1) / kAdamBlock; 
 inline int dtype_size(int dtype) { return dtype == POOT_GRAD_F32 ? 4 : 2; }
 inline bool dtype_ok(int dtype) { return dtype >= POOT_GRAD_F16 && dtype <= POOT_GRAD_F32; }
 
-// blocks that share `chunks` out, eight warps each
+// Blocks that share `chunks` out, eight warps each: as many as run at one time while a warp has
+// less than kTurns chunks, then one for every kTurns turns, so that SMs that are ahead take more of them.
+constexpr int64_t kTurns = 16;
 inline unsigned adam_grid(int64_t chunks, int most) {
-  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((chunks + kAdamWarps - 1) / kAdamWarps, most)));
+  const int64_t turns = (chunks + kAdamWarps - 1) / kAdamWarps;
+  return static_cast<unsigned>(std::max<int64_t>(1, std::max<int64_t>(std::min<int64_t>(turns, most), turns / kTurns)));
 }
 
 template <int T>
@@ -109,14 +116,13 @@ cudaError_t step_list(const poot_adamw_tensor* const* t, int count, const poot_a
     table.n[i] = x.n;
     table.first[i + 1] = table.first[i] + blocks_of(x.n);
     table.decay[i] = static_cast<float>(p.lr_device != nullptr ? x.weight_decay : 1.0 - p.lr * x.weight_decay);
-    const int size = small ? 1 : 4;
-    const bool vec = aligned(x.param, 4 * dtype_size(x.param_dtype)) && aligned(x.grad, 4 * dtype_size(x.grad_dtype)) &&
-                     aligned(x.m, 4 * size) && aligned(x.v, 4 * size) && (x.copy == nullptr || aligned(x.copy, 8));
+    const bool vec = aligned(x.param, 16) && aligned(x.grad, 16) && aligned(x.m, 16) && aligned(x.v, 16) &&
+                     aligned(x.copy, 16);
     table.types[i] = static_cast<unsigned char>(x.param_dtype | x.grad_dtype << 2 |
                                                 (x.copy != nullptr ? x.copy_dtype << 4 : 0) | (vec ? kAdamVec : 0));
   }
   return launch(small ? adamw_kernel<T, 8> : adamw_kernel<T, 32>, dim3(adam_grid(table.first[count], most)),
-                dim3(kAdamThreads), 0, stream, table, a);
+                dim3(kAdamThreads), adam_smem_bytes(small), stream, table, a);
 }
 
 int adamw_step(const poot_adamw_args* ap, cudaStream_t stream) {
