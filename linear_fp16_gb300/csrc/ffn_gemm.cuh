@@ -325,6 +325,7 @@ struct FfnGemmArgs {
   int cols;          // output columns of a tile
   int stages;
   int act, save;
+  int a_rows;        // logits, single CTAs: rows of A that a stage holds, 128 or, of one M block, fewer
   FfnJob job[2];     // gated: job 0; gradients: dx, dW (either may have no tiles)
   const uint16_t* bias[2];  // gated: bg, bu or nullptr
   FfnBiasGrad bias_grad;
@@ -550,20 +551,37 @@ __device__ __forceinline__ void ffn_lse_rows(const FfnHeadGemmArgs& args, const 
   const int chunks = (job.kb_total + ffn_mode_chunk_kb<kFfnLse>(CL, DT) - 1) / ffn_mode_chunk_kb<kFfnLse>(CL, DT);
   int buf = 0;
   uint32_t buf_phase = 0;
-  for (int ti = 0; ti < tiles; ++ti) {
+  // Where this warp works in tile ti, its rows' targets and, a lane each, its columns' biases: read
+  // a tile ahead, as their latency would be the longest part of a short tile's epilogue.
+  struct Place {
+    int m0, nc, nb, target;
+    float bias[2];
+  };
+  auto place = [&](int ti) {
     const FfnTile tile(job, (uint32_t)sched.tile(0, ti));
-    const int m0 = tile.mb * CL * kFfnBM + rank * kFfnBM + q * 32, nc = tile.nb * args.cols + part * 32;
-    const int row = m0 + lane;
-    // boxes of this warp with columns of the vocabulary: 0, 1 or 2, 128 columns apart
-    const int mine = m0 < job.M ? (part < boxes && nc < job.N) + (part + 4 < boxes && nc + 128 < job.N) : 0;
-    const int target = row < job.M ? head_target(head, row) : -1;
-    if (mine > 0 && head.bias != nullptr) {
-      __syncwarp();
+    Place p{tile.mb * CL * kFfnBM + rank * kFfnBM + q * 32, tile.nb * args.cols + part * 32, tile.nb, -1, {0.0f, 0.0f}};
+    if (p.m0 + lane < job.M) p.target = head_target(head, p.m0 + lane);
+    if (head.bias != nullptr) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const int col = nc + b * 128 + lane;
-        sbias[b * 32 + lane] = b < mine && col < job.N ? ep_unpack_t<DT>(__ldg(head.bias + col)).x : 0.0f;
+        const int col = p.nc + b * 128 + lane;
+        if (part + 4 * b < boxes && col < job.N) p.bias[b] = ep_unpack_t<DT>(__ldg(head.bias + col)).x;
       }
+    }
+    return p;
+  };
+  Place next{};
+  if (tiles > 0) next = place(0);
+  for (int ti = 0; ti < tiles; ++ti) {
+    const Place at = next;
+    if (ti + 1 < tiles) next = place(ti + 1);
+    const int m0 = at.m0, nc = at.nc, row = m0 + lane, target = at.target;
+    // boxes of this warp with columns of the vocabulary: 0, 1 or 2, 128 columns apart
+    const int mine = m0 < job.M ? (part < boxes && nc < job.N) + (part + 4 < boxes && nc + 128 < job.N) : 0;
+    if (head.bias != nullptr) {
+      __syncwarp();
+      sbias[lane] = at.bias[0];
+      sbias[32 + lane] = at.bias[1];
       __syncwarp();
     }
     float z[2][32];
@@ -573,24 +591,33 @@ __device__ __forceinline__ void ffn_lse_rows(const FfnHeadGemmArgs& args, const 
       if (!__all_sync(0xffffffffu, got)) return;
       tc_fence_after_sync();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kFfnMaxBN + part * 32);
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        if (b >= mine) break;
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(taddr + (uint32_t)(b * 128), r);
+      if (c == 0) {
+        if (mine > 0) tmem_ld_32x32b_x32(taddr, reinterpret_cast<uint32_t(&)[32]>(z[0]));
+        if (mine > 1) tmem_ld_32x32b_x32(taddr + 128u, reinterpret_cast<uint32_t(&)[32]>(z[1]));
         tmem_ld_wait();
+      } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) z[b][j] = c == 0 ? __uint_as_float(r[j]) : z[b][j] + __uint_as_float(r[j]);
+        for (int b = 0; b < 2; ++b) {
+          if (b >= mine) break;
+#pragma unroll
+          for (int j = 0; j < 32; j += 16) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(taddr + (uint32_t)(b * 128 + j), r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) z[b][j + k] += __uint_as_float(r[k]);
+          }
+        }
       }
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (CL == 2) mbar_arrive_cluster(map_to_cta(bar_cempty + 8u * buf, 0u));
+        if constexpr (CL == 2) mbar_arrive_remote(map_to_cta(bar_cempty + 8u * buf, 0u));
         else mbar_arrive(bar_cempty + 8u * buf);
       }
       if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
     }
-    float top = -INFINITY;
+    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       if (b >= mine) break;
@@ -602,16 +629,16 @@ __device__ __forceinline__ void ffn_lse_rows(const FfnHeadGemmArgs& args, const 
       }
       head_pick(z[b], target - (nc + b * 128), head.picked, row);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) top = fmaxf(top, z[b][j]);
+      for (int j = 0; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], z[b][j]);
     }
-    const float top2 = top * kHeadLog2e, base = head_base(top2);
+    const float top2 = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * kHeadLog2e, base = head_base(top2);
     float sum = 0.0f;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       if (b >= mine) break;
       sum += head_exp_sum(z[b], base);
     }
-    if (row < job.M) head.partial[((size_t)tile.nb * kHeadParts + part) * job.M + row] = make_float2(top2, sum);
+    if (row < job.M) head.partial[((size_t)at.nb * kHeadParts + part) * job.M + row] = make_float2(top2, sum);
   }
 }
 
@@ -629,8 +656,10 @@ __global__ void __launch_bounds__(ffn_threads(MODE == kFfnGated), 1)
   constexpr int EPI_WARPS = ffn_epi_warps(GATED), MMA_WARP = EPI_WARPS, PROD_WARP = EPI_WARPS + 1;  // A's; then B's
   constexpr int STG = L::STG_BOXES / EPI_WARPS;  // staging boxes of a warp
   constexpr int SUB = ffn_sub(CL);
-  constexpr int A_BYTES = ffn_a_bytes(CL);
-  constexpr int A_SUB = A_BYTES / SUB;
+  // (The MMA reads 128 rows of A in any case: of a shorter A those behind are bytes of B, and
+  // make accumulator rows that nothing reads.)
+  const int A_BYTES = LOGITS && !PAIR ? args.a_rows * kFfnBK * 2 : ffn_a_bytes(CL);
+  constexpr int A_SUB = ffn_a_bytes(CL) / SUB;
   const int BN = args.bn;
   const int STAGES = args.stages;
   const int B_BYTES = ffn_b_bytes(CL, BN);

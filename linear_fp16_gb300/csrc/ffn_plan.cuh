@@ -94,14 +94,15 @@ struct Packer {
   FfnPackArgs a;
   Operand* ops[4];
   size_t bytes = 0;
-  Packer() { std::memset(&a, 0, sizeof(a)); }
+  int64_t unit;  // elements whose multiple a copy's pitch is
+  explicit Packer(int64_t unit_ = 8) : unit(unit_) { std::memset(&a, 0, sizeof(a)); }
   void need(Operand* o) {
     if (o->p == nullptr || o->tma()) return;
     const int t = a.count++;
     ops[t] = o;
     a.src[t] = static_cast<const uint16_t*>(o->p);
     a.ld[t] = o->ld;
-    a.ldd[t] = ceil8(o->cols);
+    a.ldd[t] = ceil_div(o->cols, unit) * unit;
     a.rows[t] = static_cast<int>(o->rows);
     a.cols[t] = static_cast<int>(o->cols);
     bytes += round256(size_t(o->rows) * a.ldd[t] * 2);
@@ -299,6 +300,7 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
   std::memset(&a, 0, sizeof(a));
   std::memset(&m, 0, sizeof(m));
   a.bn = p.bn;
+  a.a_rows = kFfnBM;
   a.stages = ffn_stages(p.cl, p.bn);
   const bool gated = count > 0 && ps[0]->gated;
   a.cols = gated ? p.bn / 2 : p.bn;
@@ -346,13 +348,17 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
       j.y[o] = static_cast<uint16_t*>(q.y[o]);
       if (!aligned(q.y[o], 16)) j.tma_store = 0;
     }
+    if (q.logits && p.cl == 1 && q.rows < kFfnBM) {
+      a.a_rows = static_cast<int>(ceil8(q.rows));
+      a.stages = std::min(FfnLayout::RING_BYTES / (a.a_rows * kFfnBK * 2 + ffn_b_bytes(1, p.bn)), kFfnMaxStages);
+    }
     auto encode = [&](CUtensorMap* map, const Operand& o, bool mn, int rows) {
       return encode_2d(map, o.p, o.cols, o.rows, kFfnBK, mn ? kFfnBK : static_cast<uint32_t>(rows),
                        CU_TENSOR_MAP_SWIZZLE_128B, bf16, o.ld);
     };
     const int na = q.gated ? 1 : (q.mn_a ? q.outputs : q.parts), nb = q.gated ? 2 : (q.mn_a ? 1 : q.parts);
     bool ok = true;
-    for (int o = 0; o < na; ++o) ok = ok && encode(&m.a[ji][o], q.a[o], q.mn_a, kFfnBM);
+    for (int o = 0; o < na; ++o) ok = ok && encode(&m.a[ji][o], q.a[o], q.mn_a, a.a_rows);
     for (int o = 0; o < nb; ++o) ok = ok && encode(&m.b[ji][o], q.b[o], !q.gated && !q.logits, q.logits ? p.bn / p.cl : p.bn / 2);
     if (j.tma_store)
       for (int o = 0; o < ny; ++o)

@@ -107,6 +107,31 @@ struct ZeroOperands {
   }
 };
 
+// Elements whose multiple the pitch of a copy is: 128 bytes, a row's part of a
+// K block then lies in as few sectors as it can (2047 x 32003 x 770, rows of 1552
+// bytes: products of 97 us, of 1664 bytes ...).
+constexpr int64_t kHeadPitch = 64;
+
+// Tiles of the logits.  One M block of few rows is a stream of W, bound by HBM: single CTAs and
+// the widest tile that deals the columns out evenly (a last round that few CTAs
+// share leaves HBM to fewer loads).
+FfnPlan plan_logits(const FfnProduct& q, int sms) {
+  const FfnProduct* const ps[1] = {&q};
+  FfnPlan best = plan_ffn(ps, 1, sms, false);
+  if (q.rows > kFfnBM) return best;
+  best.cl = 1;
+  double best_fill = 0;
+  for (int bn = kFfnMaxBN; bn >= 64; bn -= 32) {
+    const int64_t tiles = ceil_div(q.cols, bn), rounds = ceil_div(tiles, sms);
+    const double fill = double(q.cols) / double(rounds * sms * bn);
+    if (fill > best_fill + 0.02) {
+      best_fill = fill;
+      best.bn = bn;
+    }
+  }
+  return best;
+}
+
 // ---- the loss --------------------------------------------------------------------
 template <int ROWS>
 cudaError_t launch_loss(const HeadLossArgs& a, cudaStream_t stream) {
@@ -141,8 +166,8 @@ int linear_cross_entropy(const poot_linear_cross_entropy_args* ap, cudaStream_t 
   q.cols = V;
   q.kext = Kz;
   const FfnProduct* const ps[1] = {&q};
-  const FfnPlan plan = plan_ffn(ps, 1, d->sms, false);
-  Packer pk;
+  const FfnPlan plan = plan_logits(q, d->sms);
+  Packer pk(kHeadPitch);
   if (K > 0) {
     pk.need(&q.a[0]);
     pk.need(&q.b[0]);
@@ -184,9 +209,9 @@ int linear_cross_entropy(const poot_linear_cross_entropy_args* ap, cudaStream_t 
   l.M = M;
   l.vocab = h.vocab;
   l.parts = static_cast<int>(parts);
-  // rows of a block: 32 (a warp's loads side by side), fewer while the blocks do not fill the SMs
+  // rows of a block: 32 (a warp's loads side by side), 8 (whole sectors) while the blocks do not fill the SMs
   e = M >= 32 * int64_t(d->sms) ? launch_loss<32>(l, stream)
-                                : (M >= 8 * int64_t(d->sms) ? launch_loss<8>(l, stream) : launch_loss<1>(l, stream));
+                                : (M >= 16 ? launch_loss<8>(l, stream) : launch_loss<1>(l, stream));
   return finish(lease, e == cudaSuccess ? POOT_OK : cuda_fail(e));
 }
 
@@ -232,13 +257,14 @@ int linear_cross_entropy_backward(const poot_linear_cross_entropy_backward_args*
     const int z = zero(p.dw, wb, stream);
     return z == POOT_OK ? zero(p.db, 2 * V, stream) : z;
   }
-  const int64_t Vc = piece_columns(M, V), ldq = ceil8(Vc), Kz = K == 0 ? 8 : K;
+  const int64_t Vc = piece_columns(M, V), ldq = ceil_div(Vc, kHeadPitch) * kHeadPitch, Kz = K == 0 ? 8 : K;
   // operands: x (copied where dW reads it, see head_prep_kernel), W
+  const int64_t ldxc = ceil_div(K, kHeadPitch) * kHeadPitch;
   Operand x = {p.x, M, K, ldx}, w = {p.w, V, K, K};
-  Packer pk;
+  Packer pk(kHeadPitch);
   size_t xbytes = 0;
   if (K > 0) {
-    if (want_dw) xbytes = round256(size_t(M) * ceil8(K) * 2);
+    if (want_dw) xbytes = round256(size_t(M) * ldxc * 2);
     else pk.need(&x);
     pk.need(&w);
   }
@@ -251,7 +277,7 @@ int linear_cross_entropy_backward(const poot_linear_cross_entropy_backward_args*
   z.ldy = ldq;
   z.cols = Vc;
   const FfnProduct* const zs[1] = {&z};
-  const FfnPlan zplan = plan_ffn(zs, 1, d->sms, false);
+  const FfnPlan zplan = plan_logits(z, d->sms);
   const FfnProduct* ps[2];
   int count = 0;
   if (want_dx) {
@@ -300,7 +326,7 @@ int linear_cross_entropy_backward(const poot_linear_cross_entropy_backward_args*
     pa.x = static_cast<const uint16_t*>(p.x);
     pa.ld = ldx;
     pa.xc = xc;
-    pa.ldc = ceil8(K);
+    pa.ldc = ldxc;
     pa.cols = static_cast<int>(K);
     pa.copy_blocks = static_cast<int>(std::min<int64_t>(ceil_div(M * ceil_div(K, kPackSpan), 8), int64_t(d->sms) * 8));
     x = {xc, M, K, pa.ldc};
