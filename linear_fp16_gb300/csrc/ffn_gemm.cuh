@@ -658,8 +658,8 @@ __global__ void __launch_bounds__(ffn_threads(MODE == kFfnGated), 1)
   constexpr int SUB = ffn_sub(CL);
   // (The MMA reads 128 rows of A in any case: of a shorter A those behind are bytes of B, and
   // make accumulator rows that nothing reads.)
-  const int A_BYTES = LOGITS && !PAIR ? args.a_rows * kFfnBK * 2 : ffn_a_bytes(CL);
-  constexpr int A_SUB = ffn_a_bytes(CL) / SUB;
+  const int A_SUB = LOGITS && !PAIR ? args.a_rows * kFfnBK * 2 : kFfnBM * kFfnBK * 2;
+  const int A_BYTES = A_SUB * SUB;
   const int BN = args.bn;
   const int STAGES = args.stages;
   const int B_BYTES = ffn_b_bytes(CL, BN);

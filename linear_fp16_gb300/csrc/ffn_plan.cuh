@@ -350,7 +350,7 @@ int run_products(const FfnProduct* const* ps, int count, const FfnPlan& p, const
     }
     if (q.logits && p.cl == 1 && q.rows < kFfnBM) {
       a.a_rows = static_cast<int>(ceil8(q.rows));
-      a.stages = std::min(FfnLayout::RING_BYTES / (a.a_rows * kFfnBK * 2 + ffn_b_bytes(1, p.bn)), kFfnMaxStages);
+      a.stages = std::min(FfnLayout::RING_BYTES / (a.a_rows * kFfnBK * 2 * ffn_sub(1) + ffn_b_bytes(1, p.bn)), kFfnMaxStages);
     }
     auto encode = [&](CUtensorMap* map, const Operand& o, bool mn, int rows) {
       return encode_2d(map, o.p, o.cols, o.rows, kFfnBK, mn ? kFfnBK : static_cast<uint32_t>(rows),

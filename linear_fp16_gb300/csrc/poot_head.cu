@@ -108,24 +108,29 @@ struct ZeroOperands {
 };
 
 // Elements whose multiple the pitch of a copy is: 128 bytes, a row's part of a
-// K block then lies in as few sectors as it can (2047 x 32003 x 770, rows of 1552
-// bytes: products of 97 us, of 1664 bytes ...).
+// K block then lies in as few sectors as it can (2047 x 32003 x 770, the products alone: 97 us
+// with rows of 1552 bytes, 75 with rows of 1664 and a shorter epilogue).
 constexpr int64_t kHeadPitch = 64;
 
-// Tiles of the logits.  One M block of few rows is a stream of W, bound by HBM: single CTAs and
-// the widest tile that deals the columns out evenly (a last round that few CTAs
-// share leaves HBM to fewer loads).
+// Tiles of the logits.  One M block on a W of some size is a stream of W: single CTAs, whose
+// short A leaves the ring to W, and the widest tile unless a narrower one deals the columns out
+// more evenly.  Times in microseconds: HBM's, or a CTA's rounds of tiles, whose K blocks arrive
+// 2.5 us after they are asked for, a ring full at a time (GB300, one row, 131072 x 4096: 224 wide 163 us, 128
+// wide 170, 96 wide 188, 64 wide 280; 256 wide 212 with 128 rows of A in a stage).
 FfnPlan plan_logits(const FfnProduct& q, int sms) {
   const FfnProduct* const ps[1] = {&q};
   FfnPlan best = plan_ffn(ps, 1, sms, false);
-  if (q.rows > kFfnBM) return best;
+  const double bytes = 2.0 * double(q.cols) * double(q.kext);
+  if (q.rows > kFfnBM || bytes < 8e6) return best;
   best.cl = 1;
-  double best_fill = 0;
-  for (int bn = kFfnMaxBN; bn >= 64; bn -= 32) {
-    const int64_t tiles = ceil_div(q.cols, bn), rounds = ceil_div(tiles, sms);
-    const double fill = double(q.cols) / double(rounds * sms * bn);
-    if (fill > best_fill + 0.02) {
-      best_fill = fill;
+  double best_time = 1e300;
+  for (int bn = kFfnMaxBN; bn >= 128; bn -= 32) {
+    const int stage = static_cast<int>(ceil8(std::min<int64_t>(q.rows, kFfnBM))) * kFfnBK * 2 + ffn_b_bytes(1, bn);
+    const double rounds = double(ceil_div(ceil_div(q.cols, bn), sms));
+    const double t = std::max(bytes / 6.6e6, rounds * double(ceil_div(q.kext, kFfnBK)) * 2.5 /
+                                                 std::min(FfnLayout::RING_BYTES / stage, kFfnMaxStages));
+    if (t < 0.97 * best_time) {
+      best_time = t;
       best.bn = bn;
     }
   }
