@@ -896,6 +896,24 @@ __global__ void __launch_bounds__(ffn_threads(MODE == kFfnGated), 1)
                            (int)rank);
     const int tiles0 = MODE == kFfnLse ? 0 : sched.count(sched.first),
               tiles = tiles0 + (ROWS ? 0 : sched.count(1 - sched.first));
+    // dz: what a lane's row and columns of a tile need, read a tile ahead
+    HeadRow next_row;
+    uint16_t next_bias[2];
+    auto read_ahead = [&](int ti) {
+      if constexpr (MODE == kFfnDz) {
+        if (ti >= tiles) return;
+        const FfnTile t(args.job[0], (uint32_t)sched.tile(0, ti));
+        next_row = head_row(args.head, t.mb * tile_rows + (int)rank * kFfnBM + q * 32 + lane, args.job[0].M);
+        if (args.head.bias != nullptr) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int col = t.nb * args.cols + (part + 4 * b) * 32 + lane;
+            next_bias[b] = part + 4 * b < boxes && col < args.job[0].N ? __ldg(args.head.bias + col) : (uint16_t)0;
+          }
+        }
+      }
+    };
+    read_ahead(0);
     for (int ti = 0; ti < tiles; ++ti) {
       const int ji = ti < tiles0 ? sched.first : 1 - sched.first, t = sched.tile(ji, ti < tiles0 ? ti : ti - tiles0);
       const FfnJob& job = args.job[ji];
@@ -938,7 +956,7 @@ __global__ void __launch_bounds__(ffn_threads(MODE == kFfnGated), 1)
                 *dst = *reinterpret_cast<const uint16_t*>(src + rr * 64 + (((lane >> 3) ^ ((rr >> 1) & 3)) << 4));
             }
           };
-          if constexpr (GATED) {
+          if constexpr (GATED || MODE == kFfnScaled) {
             // words of E elements, E rows of one instruction; N is a multiple of E
             auto store_words = [&](auto word) {
               using W = decltype(word);
@@ -954,7 +972,8 @@ __global__ void __launch_bounds__(ffn_threads(MODE == kFfnGated), 1)
             };
             // The widest stores that every row's start allows: three outputs of 840 x 7772 x 288
             // take 19.8 us so, 26.0 in single elements. The gradients' one output a job gains
-            // nothing, and the longer code costs that kernel registers (48.6 -> 51 us at 4648 x 4173 x 609).
+            // nothing, and the longer code costs that kernel registers (48.6 -> 51 us at 4648 x 4173 x 609);
+            // those of a vocabulary head, whose dW is most of what they move, gain.
             const uintptr_t align = reinterpret_cast<uintptr_t>(yo) | (uintptr_t)((uint32_t)N * 2u);
             if ((align & 7u) == 0) store_words(uint2{});
             else if ((align & 3u) == 0) store_words(uint32_t{});
@@ -1017,8 +1036,9 @@ __global__ void __launch_bounds__(ffn_threads(MODE == kFfnGated), 1)
           else mbar_arrive(bar_cempty(buf));
         }
       };
-      HeadRow hrow;  // of this lane's row
-      if constexpr (MODE == kFfnDz) hrow = head_row(args.head, m0 + lane, M);
+      const HeadRow hrow = next_row;
+      const uint16_t hbias[2] = {next_bias[0], next_bias[1]};
+      read_ahead(ti + 1);
       bool ok = true;
       if constexpr (CHUNKS) {
         // all chunks but the last: added up in the scratch
@@ -1110,7 +1130,7 @@ __global__ void __launch_bounds__(ffn_threads(MODE == kFfnGated), 1)
           uint16_t* const sbias = reinterpret_cast<uint16_t*>(smem + L::OFF_BIAS) + (buf * 8 + bx) * 32;
           const bool biased = MODE == kFfnDz && head_bias(args) != nullptr;
           if (biased) {  // (as in the gated tile, by the four warps of a box)
-            sbias[lane] = nc + lane < N ? __ldg(head_bias(args) + nc + lane) : (uint16_t)0;
+            sbias[lane] = bx < 4 ? hbias[0] : hbias[1];
             __syncwarp();
           }
           tmem_ld_wait();
