@@ -311,8 +311,9 @@ def kernel_source_hash() -> str:
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "linear_fp16_gb300", "csrc")
     for name in sorted(os.listdir(csrc)):
-        # (the feed-forward operators' files hold no kernel of this benchmark)
-        if name.endswith((".cu", ".cuh")) and not name.startswith(("ffn_", "poot_ffn", "clip")):
+        # (the feed-forward and the training operators' files hold no kernel of this benchmark)
+        if name.endswith((".cu", ".cuh")) and not name.startswith(("ffn_", "poot_ffn", "clip", "head", "poot_head",
+                                                                   "adamw", "poot_adamw")):
             with open(os.path.join(csrc, name), "rb") as fh:
                 h.update(name.encode() + b"\0" + fh.read())
     return h.hexdigest()[:16]

@@ -29,8 +29,9 @@ extern "C" {
  * nearest over chunks of 1024 elements of K; loss and lse are FP32.  Infinite
  * logits follow the formula: -inf takes no part in the sum, rows of nothing
  * else have lse -inf, +inf gives lse +inf.
- * The library's workspace holds 32 bytes for every row and 256 columns, and
- * copies of operands that TMA cannot read in place (see poot_gated_linear).
+ * The library's workspace holds 32 bytes for every row and tile of 64 to 256
+ * columns, and copies of operands that TMA cannot read in place (see
+ * poot_gated_linear).
  * M == 0 does nothing; K == 0 gives z = b.
  * Errors: POOT_ERR_INVALID_ARG (sizes outside [0, POOT_FFN_MAX_SIZE], V == 0
  * with M > 0, NULL, ldx < K, a matrix that spans more than 2^50 elements, an
@@ -60,7 +61,8 @@ POOT_API int poot_linear_cross_entropy(const poot_linear_cross_entropy_args* arg
  * not read in ignored rows).  The logits are computed again, over pieces of the vocabulary:
  * q of a piece is held in the workspace in the head dtype (at most 256 MB, or
  * 512 columns), scaled by a power of two that brings the largest |dloss| to
- * [2^14, 2^15), so that in binary16 probabilities down to 2^-29 keep their precision;
+ * [2^14, 2^15), so that in binary16 probabilities down to 2^-28 keep their precision in the rows
+ * of that |dloss|, and lose a step of 2^-39 of it at most in any;
  * dx is added up over the pieces in FP32.  Results are rounded once, after the
  * scale is taken out.  Ignored rows contribute nothing to any result, whatever
  * their x, lse and dloss hold; their dx is 0.  A row whose target is outside [0, V)

@@ -94,7 +94,9 @@ inline bool dtype_ok(int dtype) { return dtype >= POOT_GRAD_F16 && dtype <= POOT
 constexpr int64_t kTurns = 16;
 inline unsigned adam_grid(int64_t chunks, int most) {
   const int64_t turns = (chunks + kAdamWarps - 1) / kAdamWarps;
-  return static_cast<unsigned>(std::max<int64_t>(1, std::max<int64_t>(std::min<int64_t>(turns, most), turns / kTurns)));
+  // (2^20 blocks times the chunks of a launch, below 2^41, stay in 64 bits)
+  const int64_t blocks = std::max<int64_t>(std::min<int64_t>(turns, most), turns / kTurns);
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(blocks, int64_t(1) << 20)));
 }
 
 template <int T>

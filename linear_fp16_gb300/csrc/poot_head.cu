@@ -302,10 +302,14 @@ int linear_cross_entropy_backward(const poot_linear_cross_entropy_backward_args*
   }
   FfnPlan plan = plan_ffn(ps, count, d->sms);
   FfnSpace zspace(zs, 1, zplan, p.dtype, d->sms);
+  // column sums of q in a launch of their own where q is large and has many rows
+  const int64_t sum_rows = 256;
+  const int64_t sum_blocks = want_db && M >= 1024 && M * Vc >= (int64_t(1) << 24) ? ceil_div(M, sum_rows) : 0;
+  const size_t sbytes = round256(size_t(sum_blocks) * ceil8(Vc) * 4);
   const size_t qbytes = round256(size_t(M) * ldq * 2);
   size_t space;
   WorkspaceLease lease;
-  if (!lease_products(ps, count, &plan, p.dtype, 256 + qbytes + zspace.bytes() + xbytes + pk.bytes + zeros.bytes(), *d,
+  if (!lease_products(ps, count, &plan, p.dtype, 256 + qbytes + zspace.bytes() + sbytes + xbytes + pk.bytes + zeros.bytes(), *d,
                       stream, &space, &lease))
     return cuda_fail(cudaErrorMemoryAllocation);
   char* at = static_cast<char*>(lease.ptr);
@@ -318,6 +322,7 @@ int linear_cross_entropy_backward(const poot_linear_cross_entropy_backward_args*
   float* const scale = reinterpret_cast<float*>(take(256));
   char* const q = take(qbytes);
   char* const zws = take(zspace.bytes());
+  float* const sums = reinterpret_cast<float*>(take(sbytes));
   uint16_t* const xc = reinterpret_cast<uint16_t*>(take(xbytes));
   HeadPrepArgs pa;
   std::memset(&pa, 0, sizeof(pa));
@@ -396,12 +401,31 @@ int linear_cross_entropy_backward(const poot_linear_cross_entropy_backward_args*
     FfnBiasGrad bg;
     std::memset(&bg, 0, sizeof(bg));
     if (want_db) {
-      bg.d = reinterpret_cast<const uint16_t*>(q);
-      bg.ld = ldq;
-      bg.rows = M;
       bg.outputs = 1;
       bg.N = static_cast<int>(cols);
       bg.out[0] = static_cast<uint16_t*>(p.db) + c0;
+      if (sum_blocks > 0) {
+        HeadSumsArgs s;
+        std::memset(&s, 0, sizeof(s));
+        s.q = reinterpret_cast<const uint16_t*>(q);
+        s.sums = sums;
+        s.ld = ldq;
+        s.M = M;
+        s.cols = static_cast<int>(cols);
+        s.pitch = static_cast<int>(ceil8(cols));
+        s.rows = static_cast<int>(sum_rows);
+        const int64_t blocks = sum_blocks * ceil_div(s.pitch, 256);
+        if (blocks > INT32_MAX) return finish(lease, POOT_ERR_INVALID_ARG);
+        e = launch(p.dtype == POOT_DTYPE_BF16 ? head_sums_kernel<kEpiBf16> : head_sums_kernel<kEpiF16>,
+                   dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, s);
+        if (e != cudaSuccess) return finish(lease, cuda_fail(e));
+        bg.sums = sums;
+        bg.rows = sum_blocks;
+      } else {
+        bg.d = reinterpret_cast<const uint16_t*>(q);
+        bg.ld = ldq;
+        bg.rows = M;
+      }
     }
     r = run_products(
         ps, count, plan, ep, &bg, pws, *d,

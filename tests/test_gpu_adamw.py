@@ -333,3 +333,22 @@ def test_refusals():
     with pytest.raises(L.PootLinearError):
         L.adamw_step([p[0], p[0]], [g[0], g[0]], L.AdamWState([s.m[0]] * 2, [s.v[0]] * 2), **ok)   # twice the same
     assert all(torch.equal(a, b) for a, b in zip(before, (*p, *s.m)))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_tensors_beyond_2_to_the_31_elements(bits):
+    n, tail = 2 ** 31 + 777, 5000
+    p = [torch.zeros(n, dtype=torch.bfloat16, device=DEV)]
+    g = [torch.zeros(n, dtype=torch.bfloat16, device=DEV)]
+    state = L.adamw_state(p, bits=bits)
+    cut = (n - tail) // 256 * 256
+    gen = torch.Generator(device=DEV).manual_seed(13)
+    p[0][cut:] = torch.randn(n - cut, generator=gen, device=DEV)
+    g[0][cut:] = torch.randn(n - cut, generator=gen, device=DEV)
+    small_p, small_g = [p[0][cut:].clone()], [g[0][cut:].clone()]
+    small = L.adamw_state(small_p, bits=bits)
+    L.adamw_step(p, g, state, **HYPER)
+    L.adamw_step(small_p, small_g, small, **HYPER)
+    assert torch.equal(p[0][cut:], small_p[0]) and not bool(p[0][:cut].any())
+    for a, b in zip(lists(state), lists(small)):
+        assert torch.equal(a[0][-b[0].numel():], b[0])

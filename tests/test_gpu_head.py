@@ -15,6 +15,7 @@ SIZES = [  # one of each, odd ones, tiles' edges, one and several chunks of K
     (1, 1, 1), (1, 1000, 64), (3, 7, 5), (16, 4096, 128), (17, 1003, 770), (130, 513, 1030), (128, 256, 1024),
     (300, 2049, 200), (1024, 1024, 768), (129, 40001, 72), (5, 300, 2500), (257, 255, 33), (2, 131, 9000),
     (600, 5000, 1000), (70, 64, 33000),
+    (1, 50001, 200), (7, 70000, 64), (100, 9000, 520), (128, 20000, 264),   # few rows on a stream of W
 ]
 
 
@@ -320,3 +321,25 @@ def test_refusals():
             L.linear_cross_entropy_backward(**{**good, **bad})
     with pytest.raises(L.PootLinearError):
         L.linear_cross_entropy(x, w[:0], t)
+
+
+def test_operands_beyond_2_to_the_31_elements():
+    """Rows of x gigabytes apart; a W and its gradient whose last rows' offsets pass 32 bits."""
+    x, w, t, b, dloss = make(1000, 300, 72, torch.float16, seed=21)
+    big = torch.empty(1000 * 3_000_000, dtype=torch.float16, device=DEV)
+    y = big.as_strided(x.shape, (3_000_000, 1)).copy_(x)
+    loss, lse = L.linear_cross_entropy(x, w, t, b, save=True)
+    assert torch.equal(L.linear_cross_entropy(y, w, t, b), loss)
+    want = L.linear_cross_entropy_backward(dloss, x, w, t, lse, b, need_db=True)
+    got = L.linear_cross_entropy_backward(dloss, y, w, t, lse, b, need_db=True)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    del big, y
+    M, V, K = 5, 600_001, 4096
+    g = torch.Generator(device=DEV).manual_seed(22)
+    w = torch.empty(V, K, dtype=torch.bfloat16, device=DEV)
+    for i in range(0, V, 100_000):
+        w[i:i + 100_000] = torch.randn(min(100_000, V - i), K, generator=g, device=DEV) * 0.02
+    x = torch.randn(M, K, generator=g, device=DEV).bfloat16()
+    t = torch.tensor([0, V - 1, 524_287, 524_288, V - 2], device=DEV)
+    _, lse = check_loss(x, w, t, None)
+    check_grads(torch.rand(M, generator=g, device=DEV) + 0.5, x, w, t, lse, None, need_db=False)
