@@ -247,24 +247,22 @@ __device__ __forceinline__ AdamScale adam_scale(uint32_t most) {
   return {__fmul_rn(f, kPart), __fmul_rn(__frcp_rn(f), kSquare)};
 }
 
-// Two integers c nearest to sqrt(y), y in 0 .. 255^2 (1 + 2^-22): c + 1 from y > (c + 1/2)^2 on.
-// The square root is approximate; taken 2^-10 low, its rounding is the result or
+// 2^23 + c for two integers c nearest to sqrt(y), y in 0 .. 255^2 (1 + 2^-22): c + 1 from y >
+// (c + 1/2)^2 on.  The square root is approximate; taken 2^-10 low, its rounding is the result or
 // one less, and the comparison, exact in FP32, decides.
 __device__ __forceinline__ float2 adam_code(float2 y) {
   float2 s, up;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(y.x));
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(y.y));
   // (beside 2^23 only integers are left)
-  const float2 c = adam_add(adam_add(adam_add(s, adam_both(-0.0009765625f)), adam_both(8388608.0f)), adam_both(-8388608.0f));
-  const float2 edge = adam_add(adam_fma(c, c, c), adam_both(0.25f));
+  const float2 t = adam_add(adam_add(s, adam_both(-0.0009765625f)), adam_both(8388608.0f));
+  const float2 half = adam_add(t, adam_both(-8388607.5f)), edge = adam_mul(half, half);
   asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(up.x) : "f"(y.x), "f"(edge.x));
   asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(up.y) : "f"(y.y), "f"(edge.y));
-  return adam_add(c, up);
+  return adam_add(t, up);
 }
-// The low bytes of four integers, in two's complement.
+// The low bytes of four.
 __device__ __forceinline__ uint32_t adam_pack(float2 a, float2 b) {
-  a = adam_add(a, adam_both(12582912.0f));  // 1.5 2^23
-  b = adam_add(b, adam_both(12582912.0f));
   const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
   const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
   return __byte_perm(lo, hi, 0x5410);
@@ -295,22 +293,31 @@ __device__ __forceinline__ float2 adam_sqrt(float2 v) {
   return adam_fma(adam_fma(g, g, adam_neg(v)), h, g);
 }
 
-// m / d rounded to nearest likewise, for d of 2^-60 .. 2^60 and m of 2^-75 or more (below, the
-// remainder may be subnormal and the last place off by one).
-__device__ __forceinline__ float2 adam_div(float2 m, float2 d) {
+// 1 / d for d of 2^-100 .. 2^100: an approximate one and a Newton step, rounded to nearest.
+__device__ __forceinline__ float2 adam_reciprocal(float2 d) {
   float2 r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
-  const float2 n = adam_neg(d);
-  r = adam_fma(adam_fma(n, r, adam_both(1.0f)), r, r);
+  return adam_fma(adam_fma(adam_neg(d), r, adam_both(1.0f)), r, r);
+}
+
+// m / d rounded to nearest likewise, for d of 2^-60 .. 2^60 and m of 2^-75 or more (below, the
+// remainder may be subnormal and the last place off by one).
+__device__ __forceinline__ float2 adam_div(float2 m, float2 d) {
+  const float2 n = adam_neg(d), r = adam_reciprocal(d);
   const float2 q = adam_mul(m, r);
   return adam_fma(adam_fma(n, q, m), r, q);
 }
 
-// NaN where one is
-__device__ __forceinline__ float adam_max(float a, float b) {
+// The largest and the smallest of three, NaN where one is.
+__device__ __forceinline__ float adam_max(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float adam_min(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -329,8 +336,8 @@ __device__ __forceinline__ bool adam_update(const AdamHyper& h, float decay, con
     m[j + 1] = a.y;
     v[j] = b.x;
     v[j + 1] = b.y;
-    lo = fminf(lo, fminf(b.x, b.y));
-    hi = adam_max(hi, adam_max(b.x, b.y));
+    lo = adam_min(lo, b.x, b.y);
+    hi = adam_max(hi, b.x, b.y);
   }
   most = hi;
   // (zeros, of elements that have had no gradient yet, and NaN take the second way)
@@ -439,14 +446,29 @@ __device__ __forceinline__ void adam_chunk(const AdamTensor& t, const AdamHyper&
       v[j + 1] = b.y;
     }
     const bool positive = adam_update(h, t.decay, g, p, m, v, root, most_v);
-    float most_m = 0.0f;
+    float up = 0.0f, down = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) most_m = adam_max(most_m, fabsf(m[j]));
+    for (int j = 0; j < 8; j += 2) {
+      up = adam_max(up, m[j], m[j + 1]);
+      down = adam_min(down, m[j], m[j + 1]);
+    }
     // (elements that do not exist are zeros times the scale: NaN in a block that was not finite, as it stays.
     // The largest sqrt(v) is the largest v's.)
-    const AdamScale sm = adam_scale<127>(__reduce_max_sync(0xffffffffu, __float_as_uint(most_m)));
-    const AdamScale sv = adam_scale<255>(__float_as_uint(
-        __fsqrt_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most_v))))));
+    const float most_m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(adam_max(up, -down, 0.0f))));
+    const float2 most = make_float2(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most_v))), most_m);
+    AdamScale sm, sv;
+    if (positive && most_m >= 7.888609052210118e-31f && most_m <= 1.2676506002282294e30f) {
+      // both at once, as adam_scale does
+      const float root_v = adam_sqrt(adam_both(most.x)).x;
+      const float2 f = make_float2(most_m, root_v), r = adam_reciprocal(f);
+      const float2 scale = adam_mul(f, make_float2(1.0 / (127 * 127), 1.0 / (255 * 255)));
+      const float2 inverse = adam_mul(r, make_float2(127 * 127, 255 * 255));
+      sm = {scale.x, inverse.x};
+      sv = {scale.y, inverse.y};
+    } else {
+      sm = adam_scale<127>(__float_as_uint(most_m));
+      sv = adam_scale<255>(__float_as_uint(__fsqrt_rn(most.x)));
+    }
     AdamCodes<VEC> cm, cv;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
@@ -455,12 +477,16 @@ __device__ __forceinline__ void adam_chunk(const AdamTensor& t, const AdamHyper&
       for (int i = 0; i < 2; ++i) {
         const int j = 4 * w + 2 * i;
         c[i] = adam_code(make_float2(__fmul_rn(fabsf(m[j]), sm.inverse), __fmul_rn(fabsf(m[j + 1]), sm.inverse)));
+        // with its sign, beside 1.5 2^23: in two's complement
+        c[i] = adam_add(c[i], adam_both(-8388608.0f));
         c[i] = make_float2(copysignf(c[i].x, m[j]), copysignf(c[i].y, m[j + 1]));
+        c[i] = adam_add(c[i], adam_both(12582912.0f));
         k[i] = adam_code(adam_mul(make_float2(root[j], root[j + 1]), adam_both(sv.inverse)));
+        constexpr float kOne = 8388609.0f;
         if (positive)
-          k[i] = make_float2(fmaxf(k[i].x, 1.0f), fmaxf(k[i].y, 1.0f));
+          k[i] = make_float2(fmaxf(k[i].x, kOne), fmaxf(k[i].y, kOne));
         else
-          k[i] = make_float2(root[j] > 0.0f ? fmaxf(k[i].x, 1.0f) : k[i].x, root[j + 1] > 0.0f ? fmaxf(k[i].y, 1.0f) : k[i].y);
+          k[i] = make_float2(root[j] > 0.0f ? fmaxf(k[i].x, kOne) : k[i].x, root[j + 1] > 0.0f ? fmaxf(k[i].y, kOne) : k[i].y);
       }
       cm.w[w] = adam_pack(c[0], c[1]);
       cv.w[w] = adam_pack(k[0], k[1]);
@@ -584,8 +610,8 @@ __device__ __forceinline__ int adam_find(const long long (&first)[T], int count,
 
 // A block has consecutive chunks of all tensors', in equal shares, and its warps take them
 // in turn.  GB300, 705M bfloat16 elements: states in FP32 2.24 ms (6.9 TB/s, four blocks of 64 registers
-// an SM; 2.38 with one share for each resident block, as SMs differ in speed); in 8 bits 1.64 ms (4.3 TB/s, three
-// blocks of 80 registers; 1.70 with four, whose register pairs for packed constants spill), bound by the
+// an SM; 2.38 with one share for each resident block, as SMs differ in speed); in 8 bits 1.61 ms (4.4 TB/s, three
+// blocks of 80 registers; 0.06 more with four, whose register pairs for packed constants spill), bound by the
 // issue of about 65 instructions an element.
 template <int T, int BITS>
 __global__ void __launch_bounds__(kAdamThreads, BITS == 8 ? 3 : 4) adamw_kernel(const __grid_constant__ AdamTable<T> t, const AdamArgs a) {

@@ -190,6 +190,26 @@ def test_roots_and_quotients_are_rounded_to_nearest():
             assert torch.equal(p, -(m / s.sqrt()))
 
 
+def test_codes_of_every_reciprocal():
+    """A block's largest value, of every significand, decides its codes through its
+    reciprocal: 65536 significands a pass, each with 255 values spread below it."""
+    gen = torch.Generator().manual_seed(14)
+    below = torch.rand(255, generator=gen).square()
+    for part in (0, 37, 77, 127):
+        top = (torch.arange(1 << 16) + (part << 16) + 0x3f800000).to(torch.int32).view(torch.float32)
+        m = torch.cat([top[:, None], top[:, None] * below], 1).flatten()
+        v = m.square()
+        m8 = L.AdamWState([torch.zeros(m.numel(), dtype=torch.int8, device=DEV)],
+                          [torch.zeros(m.numel(), dtype=torch.uint8, device=DEV)],
+                          [torch.zeros(1 << 16, device=DEV)], [torch.zeros(1 << 16, device=DEV)])
+        # from a state of zeros with betas of 0 the averages are g and g^2
+        p = [torch.zeros(m.numel(), device=DEV)]
+        L.adamw_step(p, [m.to(DEV)], m8, step=1, lr=0.0, betas=(0.0, 0.0), eps=1.0, weight_decay=0.0)
+        (cm, sm), (cv, sv) = encode(m, 127), encode(v.sqrt(), 255)
+        for got, ref in zip(state_of(m8, 0), (cm, cv, sm, sv)):
+            assert torch.equal(got, ref), part
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_copies_of_master_weights(bits):
     host, dev = make([300, 4096, 77, 1000], torch.float32, torch.bfloat16, bits, 4)
