@@ -1150,7 +1150,15 @@ __global__ void __launch_bounds__(ffn_threads(MODE == kFfnGated), 1)
           }
           if constexpr (MODE == kFfnDz) head_gradient(r, hrow, nc);
           if (job.split > 1 || (MODE == kFfnScaled && ji == 0 && head_sums(args))) store_partial(r, g * job.split + s, nc);
-          else if constexpr (MODE == kFfnScaled)
+          else if constexpr (MODE == kFfnDz) {
+            store_box(g, nc, [&](int i) { return ep_pack_t<DT>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])); });
+            if (args.head.sums != nullptr) {
+              // The bias's gradient: sums of the values before their rounding.  (Read back from
+              // q by the products' kernel they would take it 60 us more at 2048 x 32000 x 768.)
+              const float sum = head_column_sum(r, lane);
+              if (nc + lane < N) args.head.sums[(size_t)(m0 >> 5) * args.head.sums_pitch + nc + lane] = sum;
+            }
+          } else if constexpr (MODE == kFfnScaled)
             store_box(g, nc, [&](int i) {
               return ep_pack_t<DT>(__uint_as_float(r[2 * i]) * out_scale, __uint_as_float(r[2 * i + 1]) * out_scale);
             });

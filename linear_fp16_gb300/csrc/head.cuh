@@ -34,6 +34,8 @@ struct HeadArgs {
   const float* lse;          // [M]
   const float* dloss;        // [M], elements dloss_stride apart
   long long dloss_stride;
+  float* sums;               // [row blocks of 32][pitch]: column sums of q, or nullptr
+  int sums_pitch;            // the launch's columns rounded up to 8
   const float* scale;        // dz: scale[0] goes into q; scaled: scale[1] takes it out
   // scaled
   int sum_dx;                // dx is stored as FP32 sums
@@ -128,6 +130,21 @@ __device__ __forceinline__ void head_gradient(uint32_t (&r)[32], const HeadRow& 
 #pragma unroll
   for (int j = 0; j < 32; ++j)
     if (j == d) r[j] = __float_as_uint(__uint_as_float(r[j]) - h.scale * kHeadLiftScale);
+}
+
+// Sums over the warp's rows of 32 columns: lane l gets column l's.  Each step halves
+// the columns of a lane and adds the other half's of the lane opposite.  FP32, in a fixed order.
+__device__ __forceinline__ float head_column_sum(uint32_t (&r)[32], int lane) {
+#pragma unroll
+  for (int off = 16; off > 0; off /= 2) {
+    const bool upper = (lane & off) != 0;
+#pragma unroll
+    for (int i = 0; i < off; ++i) {
+      const uint32_t keep = upper ? r[i + off] : r[i], send = upper ? r[i] : r[i + off];
+      r[i] = __float_as_uint(__uint_as_float(keep) + __uint_as_float(__shfl_xor_sync(0xffffffffu, send, off)));
+    }
+  }
+  return __uint_as_float(r[0]);
 }
 
 }  // namespace poot

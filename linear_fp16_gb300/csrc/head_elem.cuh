@@ -123,50 +123,6 @@ __global__ void __launch_bounds__(256) head_prep_kernel(const __grid_constant__ 
   }
 }
 
-struct HeadSumsArgs {
-  const uint16_t* q;  // [M][cols], row pitch ld (a multiple of 64)
-  float* sums;        // [row blocks][pitch]
-  long long ld, M;
-  int cols, pitch;    // pitch: cols rounded up to 8
-  int rows;           // of a block
-};
-
-// Column sums of q over blocks of rows, FP32 in a fixed order, for the bias's gradient: a lane
-// has eight columns of every eighth row, eight rows in flight.  The products'
-// epilogue warps join the blocks (as they do the gate's); they could read q themselves, but each CTA's
-// share is then a strip of a few hundred bytes a row before its first tile (2048 x 32000 x 768: 259 us in
-// all, 238 so, 198 - 210 without the bias; 1024 x 1024 x 768, whose q is small: 22 us, 28 so).
-template <int DT>
-__global__ void __launch_bounds__(256) head_sums_kernel(const HeadSumsArgs a) {
-  __shared__ float red[8][256];
-  grid_dep_wait();
-  grid_dep_launch();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int strips = (a.pitch + 255) / 256, strip = blockIdx.x % strips;
-  const long long rb = blockIdx.x / strips, end = min(a.M, (rb + 1) * a.rows);
-  const int c = strip * 256 + lane * 8;
-  float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  if (c < a.pitch) {
-#pragma unroll 8
-    for (long long r = rb * a.rows + warp; r < end; r += 8) {
-      float f[8];
-      ffn_unpack8<DT>(__ldg(reinterpret_cast<const uint4*>(a.q + r * a.ld + c)), f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] += f[j];
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) red[warp][lane * 8 + j] = s[j];
-  __syncthreads();
-  const int col = strip * 256 + threadIdx.x;
-  if (col < a.pitch) {
-    float t = red[0][threadIdx.x];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) t += red[w][threadIdx.x];
-    a.sums[rb * a.pitch + col] = t;
-  }
-}
-
 struct HeadReduceArgs {
   const float* ws;  // [S][M][ldw]
   uint16_t* y;      // [M][N]

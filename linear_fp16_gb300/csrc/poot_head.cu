@@ -302,9 +302,8 @@ int linear_cross_entropy_backward(const poot_linear_cross_entropy_backward_args*
   }
   FfnPlan plan = plan_ffn(ps, count, d->sms);
   FfnSpace zspace(zs, 1, zplan, p.dtype, d->sms);
-  // column sums of q in a launch of their own where q is large and has many rows
-  const int64_t sum_rows = 256;
-  const int64_t sum_blocks = want_db && M >= 1024 && M * Vc >= (int64_t(1) << 24) ? ceil_div(M, sum_rows) : 0;
+  // column sums of q, of 32 rows each
+  const int64_t sum_blocks = want_db ? ceil_div(M, 32) : 0;
   const size_t sbytes = round256(size_t(sum_blocks) * ceil8(Vc) * 4);
   const size_t qbytes = round256(size_t(M) * ldq * 2);
   size_t space;
@@ -378,6 +377,8 @@ int linear_cross_entropy_backward(const poot_linear_cross_entropy_backward_args*
     const Operand qc = {q, M, cols, ldq};
     h.bias = p.b == nullptr ? nullptr : static_cast<const uint16_t*>(p.b) + c0;
     h.col0 = static_cast<int>(c0);
+    h.sums = want_db ? sums : nullptr;
+    h.sums_pitch = static_cast<int>(ceil8(cols));
     z.a[0] = x;
     z.b[0] = wc;
     z.cols = cols;
@@ -404,28 +405,8 @@ int linear_cross_entropy_backward(const poot_linear_cross_entropy_backward_args*
       bg.outputs = 1;
       bg.N = static_cast<int>(cols);
       bg.out[0] = static_cast<uint16_t*>(p.db) + c0;
-      if (sum_blocks > 0) {
-        HeadSumsArgs s;
-        std::memset(&s, 0, sizeof(s));
-        s.q = reinterpret_cast<const uint16_t*>(q);
-        s.sums = sums;
-        s.ld = ldq;
-        s.M = M;
-        s.cols = static_cast<int>(cols);
-        s.pitch = static_cast<int>(ceil8(cols));
-        s.rows = static_cast<int>(sum_rows);
-        const int64_t blocks = sum_blocks * ceil_div(s.pitch, 256);
-        if (blocks > INT32_MAX) return finish(lease, POOT_ERR_INVALID_ARG);
-        e = launch(p.dtype == POOT_DTYPE_BF16 ? head_sums_kernel<kEpiBf16> : head_sums_kernel<kEpiF16>,
-                   dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, s);
-        if (e != cudaSuccess) return finish(lease, cuda_fail(e));
-        bg.sums = sums;
-        bg.rows = sum_blocks;
-      } else {
-        bg.d = reinterpret_cast<const uint16_t*>(q);
-        bg.ld = ldq;
-        bg.rows = M;
-      }
+      bg.sums = sums;
+      bg.rows = sum_blocks;
     }
     r = run_products(
         ps, count, plan, ep, &bg, pws, *d,

@@ -14,6 +14,7 @@ Elementwise bounds, from the operators' stated numerics (u = 2^-24):
 * q is rounded to the head dtype (p = 11 or 8 bits) times a power of two that
   puts the largest |dloss| at 2^14 or above: u_p of itself, and in binary16 a step of 2^-25
   over that power;
+* a column's sum for db is one of unrounded values;
 * results are rounded once.
 """
 import torch
@@ -64,13 +65,14 @@ def grads64(dloss, x, w, target, lse, b, ignore=IGNORE):
     d = torch.where(used, dloss, 0.0).double()[:, None]
     q = p.scatter_add(1, torch.where(used, target, 0)[:, None], -used.double()[:, None]) * d
     eq = d.abs() * ep + q.abs() * 2.0 ** -22
+    ef = eq  # before it is rounded
     tiny = TINY[dt] * float(d.abs().max()) * 2.0 ** -14
     eq = eq + (q.abs() + eq) * 2.0 ** -P[dt] + tiny
     qa = q.abs() + eq
     X, W = x.double(), w.double()
     return [(q @ W, eq @ W.abs() + acc_err(V) * (qa @ W.abs())),
             (q.T @ X, eq.T @ X.abs() + acc_err(M) * (qa.T @ X.abs())),
-            (q.sum(0), eq.sum(0) + (M / 8 + 64) * 2.0 ** -24 * qa.sum(0))]
+            (q.sum(0), ef.sum(0) + (M / 8 + 64) * 2.0 ** -24 * qa.sum(0))]
 
 
 def check(got, ref, err, name):
