@@ -1,5 +1,6 @@
 """The vocabulary head's loss and gradients against their 64-bit forms (head_ref)."""
 import math
+import threading
 
 import pytest
 import torch
@@ -343,3 +344,30 @@ def test_operands_beyond_2_to_the_31_elements():
     t = torch.tensor([0, V - 1, 524_287, 524_288, V - 2], device=DEV)
     _, lse = check_loss(x, w, t, None)
     check_grads(torch.rand(M, generator=g, device=DEV) + 0.5, x, w, t, lse, None, need_db=False)
+
+
+def test_two_threads_on_one_stream():
+    """Their calls share the stream's workspace, one call at a time."""
+    sets = [make(200 + 90 * i, 1500, 70 + 8 * i, torch.float16, seed=23 + i) for i in range(2)]
+
+    def step(s):
+        x, w, t, b, dloss = s
+        loss, lse = L.linear_cross_entropy(x, w, t, b, save=True)
+        return (loss, *L.linear_cross_entropy_backward(dloss, x, w, t, lse, b, need_db=True))
+    want = [step(s) for s in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        for _ in range(20):
+            got[i].append(step(sets[i]))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 20
+        for out in got[i]:
+            assert all(torch.equal(p, q) for p, q in zip(out, want[i]))
