@@ -58,7 +58,7 @@ POOT_API int poot_linear_cross_entropy(const poot_linear_cross_entropy_args* arg
  *   q[i, v] = dloss[i] (exp(z[i, v] - lse[i]) - [v == target[i]])   0 in ignored rows
  *   dx = q W [M, K],   dw = q^T x [V, K],   db = column sums of q [V] (FP32, before q is rounded)
  * dloss: FP32, elements dloss_stride apart (0: one value for all rows; it is
- * not read in ignored rows).  The logits are computed again, over pieces of the vocabulary:
+ * not used in ignored rows).  The logits are computed again, over pieces of the vocabulary:
  * q of a piece is held in the workspace in the head dtype (at most 256 MB, or
  * 512 columns), scaled by a power of two that brings the largest |dloss| to
  * [2^14, 2^15), so that in binary16 probabilities down to 2^-28 keep their precision in the rows

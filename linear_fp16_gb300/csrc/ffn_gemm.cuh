@@ -20,7 +20,7 @@
 // (GB300, bfloat16: lse of 8192 x 131072 x 4096 4.87 ms, 1.81 PFLOP/s, tensor pipe
 // 96% active; dz and scaled, in pieces of 16384 columns, 15.4 ms, 1.71 PFLOP/s under the
 // power cap; lse of one row of 131072 x 4096 162 us, 6.6 TB/s.  Short K shows
-// the epilogues: lse of 2048 x 32000 x 768 70 us, 1.44 PFLOP/s.)
+// the epilogues: lse of 2048 x 32000 x 768 69 us, 1.47 PFLOP/s.)
 //
 // A persistent CTA (or a CTA pair on one 256-row tile, 2-SM MMA) per SM walks
 // output tiles.  Warp roles as in the linear's GEMM: epilogue warps, one
@@ -557,19 +557,21 @@ __device__ __forceinline__ void ffn_lse_rows(const FfnHeadGemmArgs& args, const 
   uint32_t buf_phase = 0;
   // Where this warp works in tile ti, its rows' targets and, a lane each, its columns' biases: read
   // a tile ahead, as their latency would be the longest part of a short tile's epilogue.
+  // (as loaded: nothing waits for the values before their tile)
   struct Place {
-    int m0, nc, nb, target;
-    float bias[2];
+    int m0, nc, nb;
+    long long target;
+    uint16_t bias[2];
   };
   auto place = [&](int ti) {
     const FfnTile tile(job, (uint32_t)sched.tile(0, ti));
-    Place p{tile.mb * CL * kFfnBM + rank * kFfnBM + q * 32, tile.nb * args.cols + part * 32, tile.nb, -1, {0.0f, 0.0f}};
-    if (p.m0 + lane < job.M) p.target = head_target(head, p.m0 + lane);
+    Place p{tile.mb * CL * kFfnBM + rank * kFfnBM + q * 32, tile.nb * args.cols + part * 32, tile.nb, head.ignore, {0, 0}};
+    if (p.m0 + lane < job.M) p.target = __ldg(head.target + p.m0 + lane);
     if (head.bias != nullptr) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const int col = p.nc + b * 128 + lane;
-        if (part + 4 * b < boxes && col < job.N) p.bias[b] = ep_unpack_t<DT>(__ldg(head.bias + col)).x;
+        if (part + 4 * b < boxes && col < job.N) p.bias[b] = __ldg(head.bias + col);
       }
     }
     return p;
@@ -579,13 +581,13 @@ __device__ __forceinline__ void ffn_lse_rows(const FfnHeadGemmArgs& args, const 
   for (int ti = 0; ti < tiles; ++ti) {
     const Place at = next;
     if (ti + 1 < tiles) next = place(ti + 1);
-    const int m0 = at.m0, nc = at.nc, row = m0 + lane, target = at.target;
+    const int m0 = at.m0, nc = at.nc, row = m0 + lane;
     // boxes of this warp with columns of the vocabulary: 0, 1 or 2, 128 columns apart
     const int mine = m0 < job.M ? (part < boxes && nc < job.N) + (part + 4 < boxes && nc + 128 < job.N) : 0;
     if (head.bias != nullptr) {
       __syncwarp();
-      sbias[lane] = at.bias[0];
-      sbias[32 + lane] = at.bias[1];
+      sbias[lane] = ep_unpack_t<DT>(at.bias[0]).x;
+      sbias[32 + lane] = ep_unpack_t<DT>(at.bias[1]).x;
       __syncwarp();
     }
     float z[2][32];
@@ -621,6 +623,7 @@ __device__ __forceinline__ void ffn_lse_rows(const FfnHeadGemmArgs& args, const 
       }
       if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
     }
+    const int target = head_target(head, at.target);
     float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -901,13 +904,15 @@ __global__ void __launch_bounds__(ffn_threads(MODE == kFfnGated), 1)
     const int tiles0 = MODE == kFfnLse ? 0 : sched.count(sched.first),
               tiles = tiles0 + (ROWS ? 0 : sched.count(1 - sched.first));
     // dz: what a lane's row and columns of a tile need, read a tile ahead
-    HeadRow next_row;
+    HeadRowRaw next_row;
+    float q_scale = 0.0f;
+    if constexpr (MODE == kFfnDz) q_scale = args.head.scale[0];
     uint16_t next_bias[2];
     auto read_ahead = [&](int ti) {
       if constexpr (MODE == kFfnDz) {
         if (ti >= tiles) return;
         const FfnTile t(args.job[0], (uint32_t)sched.tile(0, ti));
-        next_row = head_row(args.head, t.mb * tile_rows + (int)rank * kFfnBM + q * 32 + lane, args.job[0].M);
+        next_row = head_row_load(args.head, t.mb * tile_rows + (int)rank * kFfnBM + q * 32 + lane, args.job[0].M);
         if (args.head.bias != nullptr) {
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
@@ -1040,7 +1045,7 @@ __global__ void __launch_bounds__(ffn_threads(MODE == kFfnGated), 1)
           else mbar_arrive(bar_cempty(buf));
         }
       };
-      const HeadRow hrow = next_row;
+      const HeadRowRaw hraw = next_row;
       const uint16_t hbias[2] = {next_bias[0], next_bias[1]};
       read_ahead(ti + 1);
       bool ok = true;
@@ -1066,6 +1071,8 @@ __global__ void __launch_bounds__(ffn_threads(MODE == kFfnGated), 1)
         }
       }
       if (!ok || !wait_sums()) break;
+      HeadRow hrow;
+      if constexpr (MODE == kFfnDz) hrow = head_row(args.head, hraw, q_scale);
       bool held = true;
 #pragma unroll 1
       for (int bx = part; bx < boxes; bx += EPI_WARPS / 4) {

@@ -42,9 +42,8 @@ struct HeadArgs {
   int accumulate;            // and added to those of earlier launches
 };
 
-// A row's column among all, or -1 (ignored, or outside the vocabulary).
-__device__ __forceinline__ int head_target(const HeadArgs& h, int row) {
-  const long long t = __ldg(h.target + row);
+// The column among all of a row with target t, or -1 (ignored, or outside the vocabulary).
+__device__ __forceinline__ int head_target(const HeadArgs& h, long long t) {
   return t != h.ignore && t >= 0 && t < h.vocab ? (int)t : -1;
 }
 
@@ -105,16 +104,27 @@ struct HeadRow {
   int target;
   bool used;
 };
-__device__ __forceinline__ HeadRow head_row(const HeadArgs& h, int row, int rows) {
-  HeadRow r{0.0f, 0.0f, -1, false};
-  if (row >= rows) return r;
-  const long long t = __ldg(h.target + row);
-  if (t == h.ignore) return r;
-  r.used = true;
-  r.lse2 = fmaf(__ldg(h.lse + row), kHeadLog2e, -kHeadLift);
-  const bool inside = t >= 0 && t < h.vocab;
-  r.scale = inside ? __ldg(h.dloss + row * h.dloss_stride) * (h.scale[0] / kHeadLiftScale) : NAN;
-  r.target = inside ? (int)t - h.col0 : -1;
+// As it is loaded, a tile ahead: nothing waits for the values before their tile.
+struct HeadRowRaw {
+  long long target;
+  float lse, dloss;
+};
+__device__ __forceinline__ HeadRowRaw head_row_load(const HeadArgs& h, int row, int rows) {
+  HeadRowRaw r{h.ignore, 0.0f, 0.0f};
+  if (row < rows) {
+    r.target = __ldg(h.target + row);
+    r.lse = __ldg(h.lse + row);
+    r.dloss = __ldg(h.dloss + row * h.dloss_stride);
+  }
+  return r;
+}
+__device__ __forceinline__ HeadRow head_row(const HeadArgs& h, const HeadRowRaw& raw, float scale) {
+  HeadRow r;
+  r.used = raw.target != h.ignore;
+  r.lse2 = fmaf(raw.lse, kHeadLog2e, -kHeadLift);
+  const bool inside = raw.target >= 0 && raw.target < h.vocab;
+  r.scale = inside ? raw.dloss * (scale / kHeadLiftScale) : NAN;
+  r.target = inside && r.used ? (int)raw.target - h.col0 : -1;
   return r;
 }
 
