@@ -540,7 +540,7 @@ __device__ __forceinline__ void ffn_add_scratch(const float4* p, uint32_t (&r)[3
 
 // The epilogue of the lse kernel: a lane has a row of its tile, a warp every
 // fourth box of 32 columns, at most two.  The sums of a tile's chunks of K are added up in
-// registers, rounded to nearest (64 a lane; sixteen warps leave 112 registers
+// registers, rounded to nearest (64 a lane of the 96 that eighteen warps leave
 // each): the tensor core's truncation, 6.3e-9 of a sum per term, would come
 // through to the loss unrounded.  With an accumulator's columns drained in
 // about 500 cycles a chunk of 1024 (16 x 512 cycles of MMAs a CTA) hides it.
